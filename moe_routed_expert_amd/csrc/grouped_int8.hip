@@ -1,0 +1,381 @@
+// Grouped products of the routed experts in 8-bit integers (gfx950): int8 rows
+// with one scale each times int8 weights with one scale per output channel,
+// summed exactly in int32 by v_mfma_i32_16x16x64_i8.
+//
+//   gate_up: y[r, j] = bf16(silu(min(g, L)) * clamp(u, -L, L) * p[r]),
+//            g = sum_h a[t, h] wg[e, j, h] * sa[t] * sg[e, j], u likewise,
+//            t = slot_of[r] / top_k: the tokens are read in place, a row of
+//            each for every expert that takes it, with no gathered copy;
+//   down:    out[r, n] = round(sum_i h[r, i] wd[e, n, i] * sh[r] * p[r] * sd[e, n]).
+//
+// The integer sums carry no rounding, so their order is free: tiles, steps
+// and wavefronts may be arranged at will without changing a bit.
+//
+// Tile kernel: a block covers 256 rows of one expert and 128 columns of each
+// of two weight tiles (gate and up of the same columns; two neighbouring
+// column ranges of the down weights), eight wavefronts of 64 x 64 x 2, 128
+// accumulators per lane. Steps of 128 along K: a row of a tile is then 128
+// bytes, eight 16-byte chunks, XOR-swizzled so that a fragment read (one
+// chunk of each of 16 rows) takes 16 different bank groups. Global memory
+// goes straight to LDS in two stages; the next stage's loads are in flight
+// while this one's products run.
+#include "epi_common.h"
+#include "grouped_map.h"
+#include "moe_routed.h"
+#include "swiglu_math.h"
+
+namespace moe_epi {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kStep = 128;            // bytes (elements) of K per step
+constexpr int kChunks = kStep / 16;   // 16-byte chunks of a tile row
+constexpr int64_t kMaxK = 131072;     // below it |sum| < 2^31 even for -128 * -128
+
+// Rows of a that the rows of an expert read: row r itself, or the token of its slot.
+struct Rows {
+    const float* scale;
+    const int32_t* slot_of;  // NULL: rows are their own
+    uint32_t top_k;
+    int64_t slots;
+    // The row of a for row r; -1 for a slot out of range (read row 0, count it as zeros).
+    __device__ __forceinline__ int64_t of(int64_t r) const {
+        if (!slot_of) return r;
+        const int32_t s = slot_of[r];
+        return s >= 0 && s < slots ? static_cast<int64_t>(static_cast<uint32_t>(s) / top_k) : -1;
+    }
+};
+
+enum class Out { kSwiglu, kBf16, kF32 };
+
+template <int BM_, int BN_, int WM_, int WN_, int GM_>
+struct Tile {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, GM = GM_;
+    static constexpr int kThreads = 64 * WM * WN;
+    static constexpr int MI = BM / (16 * WM), NI = BN / (16 * WN);
+    static constexpr int kABytes = BM * kStep, kWBytes = BN * kStep, kStage = kABytes + 2 * kWBytes;
+    static constexpr int kALoads = BM * kChunks / kThreads, kWLoads = BN * kChunks / kThreads;
+    static constexpr int kLds = 2 * kStage;
+    static constexpr int kLdo = BN + 8;  // elements per row of a staged bf16 tile
+    static_assert(BM * kLdo * 2 <= kLds && BM * BN * 4 <= kLds, "a staged output tile fits");
+    static_assert(kALoads >= 1 && kWLoads >= 1 && BM * kChunks % kThreads == 0 && BN * kChunks % kThreads == 0,
+                  "whole chunks per lane");
+    static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && BM <= kThreads, "whole MFMA tiles");
+};
+
+__device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0) only (gfx9 encoding)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// This wavefront's loads and LDS accesses are done, then the block meets.
+__device__ __forceinline__ void stage_barrier() {
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <class C, Out kOut>
+__global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
+    const int8_t* __restrict__ a, Rows rows_of, const int8_t* __restrict__ w1, const float* __restrict__ s1,
+    const int8_t* __restrict__ w2, const float* __restrict__ s2, const int32_t* __restrict__ offs,
+    const float* __restrict__ probs, void* __restrict__ out, int64_t rows, int64_t k_dim, int64_t n_dim,
+    int64_t experts, float limit, int64_t n_tiles, int64_t n_blocks) {
+    constexpr bool kPair = kOut == Out::kSwiglu;  // two weights of the same columns
+    constexpr int MI = C::MI, NI = C::NI;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds + C::BM * 8];
+    float* const row_scale = reinterpret_cast<float*>(lds + C::kLds);
+    float* const row_prob = row_scale + C::BM;
+
+    int64_t mt, nt;
+    tile_of(blockIdx.x, n_blocks / n_tiles, n_tiles, C::GM, &mt, &nt);
+    const TileRows tr = find_row_tile(offs, rows, experts, mt, C::BM);
+    if (tr.rows == 0) return;
+    const int64_t col1 = nt * (kPair ? C::BN : 2 * C::BN), col2 = kPair ? col1 : col1 + C::BN;
+    const int n1 = static_cast<int>(n_dim - col1 < C::BN ? n_dim - col1 : C::BN);
+    const int n2 = static_cast<int>(n_dim - col2 <= 0 ? 0 : (n_dim - col2 < C::BN ? n_dim - col2 : C::BN));
+
+    const int tid = static_cast<int>(threadIdx.x), lane = tid % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+
+    if (tid < C::BM) {
+        const int64_t r = tr.row0 + (tid < tr.rows ? tid : tr.rows - 1), u = rows_of.of(r);
+        row_scale[tid] = u >= 0 ? rows_of.scale[u] : 0.0f;
+        row_prob[tid] = probs ? probs[r] : 1.0f;
+    }
+
+    // This lane's chunks of a stage: slot row * 8 + (chunk ^ swizzle(row)) holds
+    // chunk `chunk` of tile row `row`. Rows past the tile repeat its last one.
+    const int8_t* pa[C::kALoads];
+    const int8_t* pw1[C::kWLoads];
+    const int8_t* pw2[C::kWLoads];
+    int kq[C::kALoads > C::kWLoads ? C::kALoads : C::kWLoads];
+#pragma unroll
+    for (int i = 0; i < C::kALoads; ++i) {
+        const int s = i * C::kThreads + tid, row = s / kChunks;
+        kq[i] = ((s % kChunks) ^ swizzle(row)) * 16;
+        const int64_t u = rows_of.of(tr.row0 + (row < tr.rows ? row : tr.rows - 1));
+        pa[i] = a + (u >= 0 ? u : 0) * k_dim;
+    }
+    const int8_t* t1 = w1 + (tr.expert * n_dim + col1) * k_dim;
+    const int8_t* t2 = w2 + (tr.expert * n_dim + (n2 > 0 ? col2 : col1)) * k_dim;
+    const int m2 = n2 > 0 ? n2 : n1;
+#pragma unroll
+    for (int i = 0; i < C::kWLoads; ++i) {
+        const int s = i * C::kThreads + tid, row = s / kChunks;
+        kq[i] = ((s % kChunks) ^ swizzle(row)) * 16;
+        pw1[i] = t1 + static_cast<int64_t>(row < n1 ? row : n1 - 1) * k_dim;
+        pw2[i] = t2 + static_cast<int64_t>(row < m2 ? row : m2 - 1) * k_dim;
+    }
+
+    i32x4 acc1[MI][NI], acc2[MI][NI];
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni) acc1[mi][ni] = acc2[mi][ni] = i32x4{0, 0, 0, 0};
+
+    auto load = [&](const int8_t* src, uint8_t* dst) {
+        __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+    };
+    // Chunks past the end of K load the start of their row instead; the rows
+    // of a are then cleared there, so that whatever the weights hold counts 0.
+    auto issue = [&](int64_t kt) {
+        uint8_t* st = lds + (kt & 1) * C::kStage;
+        const int64_t k0 = kt * kStep;
+#pragma unroll
+        for (int i = 0; i < C::kALoads; ++i)
+            load(pa[i] + (k0 + kq[i] < k_dim ? k0 + kq[i] : 0), st + (i * C::kThreads + wave * 64) * 16);
+#pragma unroll
+        for (int i = 0; i < C::kWLoads; ++i) {
+            const int64_t k = k0 + kq[i] < k_dim ? k0 + kq[i] : 0;
+            load(pw1[i] + k, st + C::kABytes + (i * C::kThreads + wave * 64) * 16);
+            load(pw2[i] + k, st + C::kABytes + C::kWBytes + (i * C::kThreads + wave * 64) * 16);
+        }
+    };
+    auto fragment = [&](const uint8_t* tile, int row, int chunk) {
+        return *reinterpret_cast<const i32x4*>(tile + (row * kChunks + (chunk ^ swizzle(row))) * 16);
+    };
+
+    const int64_t nk = (k_dim + kStep - 1) / kStep;
+    issue(0);
+    for (int64_t kt = 0; kt < nk; ++kt) {
+        uint8_t* st = lds + (kt & 1) * C::kStage;
+        stage_barrier();  // step kt has landed, and nobody reads the other stage any more
+        if (kt + 1 < nk) issue(kt + 1);
+        if (kt + 1 == nk && k_dim % kStep != 0) {
+            const int64_t k0 = kt * kStep;
+#pragma unroll
+            for (int i = 0; i < C::kALoads; ++i)
+                if (k0 + kq[i] >= k_dim) *reinterpret_cast<i32x4*>(st + (i * C::kThreads + tid) * 16) = i32x4{0, 0, 0, 0};
+            lds_barrier();
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            i32x4 fa[MI], f1[NI], f2[NI];
+            const int chunk = 4 * kk + lane / 16;
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) fa[mi] = fragment(st, wm * (C::BM / C::WM) + mi * 16 + lane % 16, chunk);
+#pragma unroll
+            for (int ni = 0; ni < NI; ++ni) {
+                const int row = wn * (C::BN / C::WN) + ni * 16 + lane % 16;
+                f1[ni] = fragment(st + C::kABytes, row, chunk);
+                f2[ni] = fragment(st + C::kABytes + C::kWBytes, row, chunk);
+            }
+#pragma unroll
+            for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) {
+                    acc1[mi][ni] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f1[ni], fa[mi], acc1[mi][ni], 0, 0, 0);
+                    acc2[mi][ni] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f2[ni], fa[mi], acc2[mi][ni], 0, 0, 0);
+                }
+        }
+    }
+    lds_barrier();  // all fragment reads done before the stages become the output tile
+
+    // Lane l holds, in register j of tile (mi, ni), row mi * 16 + l % 16 and
+    // column ni * 16 + 4 * (l / 16) + j of the wavefront's part.
+    const int64_t wrow = tr.expert * n_dim;
+    auto col_scale = [&](const float* s, int64_t col, int n) {
+        f32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = n > j ? s[wrow + col + j] : 0.0f;
+        return v;
+    };
+    if constexpr (kOut != Out::kF32) {
+        uint16_t* stage = reinterpret_cast<uint16_t*>(lds);
+        uint16_t* o = static_cast<uint16_t*>(out);
+#pragma unroll
+        for (int half = 0; half < (kPair ? 1 : 2); ++half) {
+            const int64_t c0 = half == 0 ? col1 : col2;
+            const int n = half == 0 ? n1 : n2;
+            if (half == 1) lds_barrier();
+#pragma unroll
+            for (int ni = 0; ni < NI; ++ni) {
+                const int c = wn * (C::BN / C::WN) + ni * 16 + 4 * (lane / 16);
+                const f32x4 sc1 = col_scale(half == 0 ? s1 : s2, c0 + c, n - c);
+                f32x4 sc2{};
+                if constexpr (kPair) sc2 = col_scale(s2, c0 + c, n - c);
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) {
+                    const int r = wm * (C::BM / C::WM) + mi * 16 + lane % 16;
+                    const float sa = row_scale[r], p = row_prob[r];
+                    float v[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (kPair) {
+                            const float g = static_cast<float>(acc1[mi][ni][j]) * sa * sc1[j];
+                            const float u = static_cast<float>(acc2[mi][ni][j]) * sa * sc2[j];
+                            v[j] = fwd_elem(g, u, p, limit);
+                        } else {
+                            const int q = half == 0 ? acc1[mi][ni][j] : acc2[mi][ni][j];
+                            v[j] = static_cast<float>(q) * sa * sc1[j] * p;
+                        }
+                    }
+                    *reinterpret_cast<u32x2*>(stage + r * C::kLdo + c) =
+                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                }
+            }
+            lds_barrier();
+#pragma unroll
+            for (int i = 0; i < C::BM * C::BN / 8 / C::kThreads; ++i) {
+                const int s = i * C::kThreads + tid, row = s / (C::BN / 8), c = s % (C::BN / 8) * 8;
+                if (row < tr.rows && c < n)
+                    *reinterpret_cast<u32x4*>(o + (tr.row0 + row) * n_dim + c0 + c) =
+                        *reinterpret_cast<const u32x4*>(stage + row * C::kLdo + c);
+            }
+        }
+    } else {
+        // float32, one weight tile at a time; 16-byte chunks of a row swizzled by the row
+        float* stage = reinterpret_cast<float*>(lds);
+        float* o = static_cast<float*>(out);
+        auto at = [](int row, int c) { return row * C::BN + (c ^ ((row & 15) << 2)); };
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int64_t c0 = half == 0 ? col1 : col2;
+            const int n = half == 0 ? n1 : n2;
+            if (half == 1) lds_barrier();
+#pragma unroll
+            for (int ni = 0; ni < NI; ++ni) {
+                const int c = wn * (C::BN / C::WN) + ni * 16 + 4 * (lane / 16);
+                const f32x4 sc = col_scale(half == 0 ? s1 : s2, c0 + c, n - c);
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) {
+                    const int r = wm * (C::BM / C::WM) + mi * 16 + lane % 16;
+                    const float sa = row_scale[r], p = row_prob[r];
+                    f32x4 v;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int q = half == 0 ? acc1[mi][ni][j] : acc2[mi][ni][j];
+                        v[j] = static_cast<float>(q) * sa * sc[j] * p;
+                    }
+                    *reinterpret_cast<f32x4*>(stage + at(r, c)) = v;
+                }
+            }
+            lds_barrier();
+#pragma unroll
+            for (int i = 0; i < C::BM * C::BN / 4 / C::kThreads; ++i) {
+                const int s = i * C::kThreads + tid, row = s / (C::BN / 4), c = s % (C::BN / 4) * 4;
+                if (row < tr.rows && c < n)
+                    store_nt16(o + (tr.row0 + row) * n_dim + c0 + c, *reinterpret_cast<const u32x4*>(stage + at(row, c)));
+            }
+        }
+    }
+}
+
+typedef Tile<256, 128, 4, 2, 2> GateUpTile;
+typedef Tile<256, 128, 4, 2, 32> DownTile;
+
+template <class C, Out kOut>
+int launch_int8(const int8_t* a, const Rows& rows_of, const int8_t* w1, const float* s1, const int8_t* w2,
+                const float* s2, const int32_t* offs, const float* probs, void* out, int64_t rows, int64_t k_dim,
+                int64_t n_dim, int64_t experts, float limit, hipStream_t st) {
+    int64_t n_tiles, n_blocks;
+    const int64_t grid =
+        grouped_grid(rows, n_dim, kOut == Out::kSwiglu ? C::BN : 2 * C::BN, experts, C::BM, &n_tiles, &n_blocks);
+    if (grid == 0) return MOE_EPI_ERR_BAD_SHAPE;
+    (void)hipGetLastError();
+    hipLaunchKernelGGL((grouped_int8_kernel<C, kOut>), dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), 0, st, a,
+                       rows_of, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim, experts, limit, n_tiles,
+                       n_blocks);
+    return launch_status();
+}
+
+bool shape_ok(int64_t rows, int64_t k_dim, int64_t n_dim, int64_t experts) {
+    return rows >= 0 && rows <= INT32_MAX && k_dim > 0 && k_dim < kMaxK && k_dim % 16 == 0 && n_dim > 0 &&
+           n_dim % 8 == 0 && experts > 0 && experts <= INT64_MAX / 4 / n_dim;
+}
+
+}  // namespace
+}  // namespace moe_epi
+
+using namespace moe_epi;
+
+extern "C" int grouped_gate_up_swiglu_int8_fwd(const int8_t* a, const float* a_scale, const int32_t* slot_of,
+                                               const int8_t* w_gate, const float* w_gate_scale, const int8_t* w_up,
+                                               const float* w_up_scale, const int32_t* offs, const float* probs,
+                                               uint16_t* y, int64_t rows, int64_t tokens, int64_t top_k,
+                                               int64_t hidden, int64_t inter, int64_t experts, float limit,
+                                               void* stream) {
+    if (!shape_ok(rows, hidden, inter, experts) || tokens < 0 || top_k < 1 || tokens > INT32_MAX / top_k)
+        return MOE_EPI_ERR_BAD_SHAPE;
+    if (!slot_of && (top_k != 1 || tokens != rows)) return MOE_EPI_ERR_BAD_SHAPE;
+    int64_t ab, wb, yb, tb, rb, sb, ob;
+    if (!bytes_ok(tokens, hidden, 1, &ab) || !bytes_ok(experts * inter, hidden, 1, &wb) ||
+        !bytes_ok(rows, inter, 2, &yb) || !bytes_ok(tokens, 1, 4, &tb) || !bytes_ok(rows, 1, 4, &rb) ||
+        !bytes_ok(experts, inter, 4, &sb) || !bytes_ok(experts, 1, 4, &ob))
+        return MOE_EPI_ERR_BAD_SHAPE;
+    if (!(limit > 0.0f) || !isfinite(limit)) return MOE_EPI_ERR_BAD_LIMIT;
+    if (rows == 0 || tokens == 0) return MOE_EPI_SUCCESS;
+    if (!a || !a_scale || !w_gate || !w_gate_scale || !w_up || !w_up_scale || !offs || !y)
+        return MOE_EPI_ERR_NULL_POINTER;
+    if (!aligned(a, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(y, 16) || !aligned(a_scale, 4) ||
+        !aligned(slot_of, 4) || !aligned(w_gate_scale, 4) || !aligned(w_up_scale, 4) || !aligned(offs, 4) ||
+        !aligned(probs, 4))
+        return MOE_EPI_ERR_MISALIGNED;
+    const Range ry = range_of(y, yb);
+    for (const Range& r : {range_of(a, ab), range_of(a_scale, tb), range_of(slot_of, slot_of ? rb : 0),
+                           range_of(w_gate, wb), range_of(w_up, wb), range_of(w_gate_scale, sb),
+                           range_of(w_up_scale, sb), range_of(offs, ob), range_of(probs, probs ? rb : 0)})
+        if (overlaps(ry, r)) return MOE_EPI_ERR_ALIAS;
+    const Rows rows_of{a_scale, slot_of, static_cast<uint32_t>(top_k), tokens * top_k};
+    return launch_int8<GateUpTile, Out::kSwiglu>(a, rows_of, w_gate, w_gate_scale, w_up, w_up_scale, offs, probs, y,
+                                                 rows, hidden, inter, experts, limit, as_stream(stream));
+}
+
+extern "C" int grouped_down_router_int8_fwd(const int8_t* h, const float* h_scale, const int8_t* w_down,
+                                            const float* w_down_scale, const int32_t* offs, const float* probs,
+                                            void* out, int out_dtype, int64_t rows, int64_t inter, int64_t hidden,
+                                            int64_t experts, void* stream) {
+    if (out_dtype != MOE_EPI_BF16 && out_dtype != MOE_EPI_F32) return MOE_EPI_ERR_BAD_DTYPE;
+    if (!shape_ok(rows, inter, hidden, experts)) return MOE_EPI_ERR_BAD_SHAPE;
+    int64_t hb, wb, ob, rb, sb, fb;
+    if (!bytes_ok(rows, inter, 1, &hb) || !bytes_ok(experts * hidden, inter, 1, &wb) ||
+        !bytes_ok(rows, hidden, elem_bytes(out_dtype), &ob) || !bytes_ok(rows, 1, 4, &rb) ||
+        !bytes_ok(experts, hidden, 4, &sb) || !bytes_ok(experts, 1, 4, &fb))
+        return MOE_EPI_ERR_BAD_SHAPE;
+    if (rows == 0) return MOE_EPI_SUCCESS;
+    if (!h || !h_scale || !w_down || !w_down_scale || !offs || !out) return MOE_EPI_ERR_NULL_POINTER;
+    if (!aligned(h, 16) || !aligned(w_down, 16) || !aligned(out, 16) || !aligned(h_scale, 4) ||
+        !aligned(w_down_scale, 4) || !aligned(offs, 4) || !aligned(probs, 4))
+        return MOE_EPI_ERR_MISALIGNED;
+    const Range ro = range_of(out, ob);
+    for (const Range& r : {range_of(h, hb), range_of(h_scale, rb), range_of(w_down, wb), range_of(w_down_scale, sb),
+                           range_of(offs, fb), range_of(probs, probs ? rb : 0)})
+        if (overlaps(ro, r)) return MOE_EPI_ERR_ALIAS;
+    const Rows rows_of{h_scale, nullptr, 1u, rows};
+    const hipStream_t st = as_stream(stream);
+    if (out_dtype == MOE_EPI_F32)
+        return launch_int8<DownTile, Out::kF32>(h, rows_of, w_down, w_down_scale, w_down, w_down_scale, offs, probs,
+                                                out, rows, inter, hidden, experts, 1.0f, st);
+    return launch_int8<DownTile, Out::kBf16>(h, rows_of, w_down, w_down_scale, w_down, w_down_scale, offs, probs, out,
+                                             rows, inter, hidden, experts, 1.0f, st);
+}

@@ -1,0 +1,506 @@
+// Moves of the tokens into expert order and back, and their gradients (gfx950).
+//
+//   dispatch        out[r] = x[slot_of[r] / k]                               (bits copied)
+//   its gradient    grad_x[t] = sum_j grad_out[row_of[t, j]]
+//   combine         out[t] = sum_j w[t, j] * rows[row_of[t, j]]
+//   its gradients   grad_rows[row_of[t, j]] = w[t, j] * grad_out[t]
+//                   grad_w[t, j] = sum_h grad_out[t, h] * rows[row_of[t, j], h]
+//
+// All of them are bound by the bytes they move: each row is read or written
+// once and each token once, with a multiply-add per element at most. Sums are
+// float32 in a fixed order (slots ascending; lanes, then wavefronts for the
+// weights' gradient), rounded once when stored, so that a run repeats bit for
+// bit: the alternative, one row per block with atomic additions into the
+// token, would read and write the token once per row and in any order.
+//
+// A lane moves vectors of N elements: 16 bytes of 16-bit storage, or 4
+// elements where float32 takes part (16 bytes of float32), so that the
+// accesses of a wavefront are one contiguous run on both sides. Rows of odd
+// width or address are moved by the same vectors at the element's alignment
+// (the hardware takes any), with the last few elements one per lane.
+#include "epi_common.h"
+#include "moe_routed.h"
+
+namespace moe_epi {
+namespace {
+
+constexpr int64_t kMaxTopK = 1024;
+constexpr int kSlotChunk = 8;  // slots taken together: their indices are read at once
+
+// ---- N elements of storage type T at element `e` of a row --------------------------
+
+template <int T>
+constexpr int kBytesOf = T == MOE_EPI_F32 ? 4 : 2;
+
+// Unsigned vectors of 1 to 16 bytes, at their own or at the element's alignment.
+template <int kBytes, int kAlign> struct Word;
+#define MOE_WORD(BYTES, TYPE, ALIGN)                                   \
+    template <> struct Word<BYTES, ALIGN> {                            \
+        typedef TYPE plain;                                            \
+        typedef TYPE type __attribute__((aligned(ALIGN)));             \
+    };
+MOE_WORD(16, u32x4, 16)
+MOE_WORD(16, u32x4, 4)
+MOE_WORD(16, u32x4, 2)
+MOE_WORD(8, u32x2, 8)
+MOE_WORD(8, u32x2, 4)
+MOE_WORD(8, u32x2, 2)
+#undef MOE_WORD
+
+template <int kBytes, int kAlign>
+__device__ __forceinline__ typename Word<kBytes, kAlign>::plain load_word(const void* p) {
+    return __builtin_nontemporal_load(static_cast<const typename Word<kBytes, kAlign>::type*>(p));
+}
+template <int kBytes, int kAlign>
+__device__ __forceinline__ void store_word(void* p, typename Word<kBytes, kAlign>::plain v) {
+    __builtin_nontemporal_store(v, static_cast<typename Word<kBytes, kAlign>::type*>(p));
+}
+
+__device__ __forceinline__ float half_at(uint32_t w, int hi) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(hi ? w >> 16 : w & 0xFFFFu)));
+}
+
+// N consecutive elements widened to float32, and rounded back to T.
+template <int T, int N, bool kAligned>
+struct Vec {
+    static constexpr int kBytes = N * kBytesOf<T>, kAlign = kAligned ? kBytes : kBytesOf<T>;
+    static_assert(kBytes == 16 || kBytes == 8, "one access");
+    typedef typename Word<kBytes, kAlign>::plain Raw;
+
+    __device__ __forceinline__ static Raw load(const void* row, uint32_t e) {
+        return load_word<kBytes, kAlign>(static_cast<const char*>(row) + e * kBytesOf<T>);
+    }
+    __device__ __forceinline__ static void widen(Raw r, float (&f)[N]) {
+#pragma unroll
+        for (int i = 0; i < kBytes / 4; ++i) {
+            const uint32_t w = r[i];
+            if constexpr (T == MOE_EPI_F32) {
+                f[i] = __uint_as_float(w);
+            } else if constexpr (T == MOE_EPI_BF16) {
+                f[2 * i] = bf16_lo(w);
+                f[2 * i + 1] = bf16_hi(w);
+            } else {
+                f[2 * i] = half_at(w, 0);
+                f[2 * i + 1] = half_at(w, 1);
+            }
+        }
+    }
+    __device__ __forceinline__ static void store(void* row, uint32_t e, const float (&f)[N]) {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < kBytes / 4; ++i) {
+            if constexpr (T == MOE_EPI_F32) {
+                r[i] = __float_as_uint(f[i]);
+            } else if constexpr (T == MOE_EPI_BF16) {
+                r[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+            } else {
+                // finished binary32 values first: see Elem<MOE_EPI_F16>::store1
+                float a = f[2 * i], b = f[2 * i + 1];
+                asm volatile("" : "+v"(a), "+v"(b));
+                r[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, f16x2_t));
+            }
+        }
+        store_word<kBytes, kAlign>(static_cast<char*>(row) + e * kBytesOf<T>, r);
+    }
+};
+
+// ---- dispatch ------------------------------------------------------------------------
+
+constexpr int kCopyLanes = 128;
+constexpr int kCopyVecs = 4;  // 16-byte pieces per lane
+
+// One block per (row, segment of kCopyLanes * kCopyVecs pieces): bytes are
+// copied, whatever they stand for. kAlign: of every row on both sides.
+template <int kAlign>
+__global__ __launch_bounds__(kCopyLanes) void moe_dispatch_kernel(const char* __restrict__ x,
+                                                                  const int32_t* __restrict__ slot_of,
+                                                                  char* __restrict__ out, int64_t rows, int64_t slots,
+                                                                  uint32_t top_k, int64_t row_bytes, uint32_t nseg) {
+    const uint32_t pieces = static_cast<uint32_t>(row_bytes / 16);
+    const int64_t pairs = rows * static_cast<int64_t>(nseg);
+    for (int64_t b = blockIdx.x; b < pairs; b += gridDim.x) {
+        const int64_t r = b / nseg;
+        const uint32_t seg = static_cast<uint32_t>(b - r * nseg);
+        const int32_t slot = __builtin_amdgcn_readfirstlane(slot_of[r]);
+        const bool has = slot >= 0 && slot < slots;  // a row without a slot is zeros
+        const char* src = x + (has ? static_cast<int64_t>(static_cast<uint32_t>(slot) / top_k) * row_bytes : 0);
+        char* dst = out + r * row_bytes;
+        const uint32_t c0 = seg * (kCopyLanes * kCopyVecs) + threadIdx.x;
+        u32x4 v[kCopyVecs];
+#pragma unroll
+        for (int k = 0; k < kCopyVecs; ++k) {
+            v[k] = u32x4{0u, 0u, 0u, 0u};
+            if (has && c0 + k * kCopyLanes < pieces) v[k] = load_word<16, kAlign>(src + (c0 + k * kCopyLanes) * 16u);
+        }
+#pragma unroll
+        for (int k = 0; k < kCopyVecs; ++k)
+            if (c0 + k * kCopyLanes < pieces) store_word<16, kAlign>(dst + (c0 + k * kCopyLanes) * 16u, v[k]);
+        if constexpr (kAlign < 16) {  // the row's last bytes, two at a time
+            const uint32_t done = pieces * 16, left = static_cast<uint32_t>(row_bytes) - done;
+            if (seg + 1 == nseg && threadIdx.x < left / 2)
+                *reinterpret_cast<uint16_t*>(dst + done + 2 * threadIdx.x) =
+                    has ? *reinterpret_cast<const uint16_t*>(src + done + 2 * threadIdx.x) : uint16_t{0};
+        }
+    }
+}
+
+// ---- sums over a token's rows ------------------------------------------------------
+
+constexpr int kSumLanes = 128;
+constexpr int kSumVecs = 2;  // vectors per lane of a segment
+constexpr int kSumRows = 4;  // rows whose loads are in flight together
+
+// One block per (token, segment). The slots' rows and weights are the same
+// for the whole block (scalar loads); those with a row are kept as a bit mask
+// and taken in ascending order, kSumRows at a time.
+template <int TI, int TO, int N, bool kWeighted, bool kAligned>
+__global__ __launch_bounds__(kSumLanes) void moe_row_sum_kernel(const char* __restrict__ in,
+                                                                const int32_t* __restrict__ row_of,
+                                                                const float* __restrict__ weights,
+                                                                char* __restrict__ out, int64_t rows, int64_t tokens,
+                                                                int64_t top_k, int64_t hidden, uint32_t nseg) {
+    typedef Vec<TI, N, kAligned> In;
+    typedef Vec<TO, N, kAligned> Out;
+    const uint32_t nvec = static_cast<uint32_t>(hidden / N), done = nvec * N;
+    const uint32_t left = static_cast<uint32_t>(hidden) - done;
+    const int64_t pairs = tokens * static_cast<int64_t>(nseg);
+    for (int64_t b = blockIdx.x; b < pairs; b += gridDim.x) {
+        const int64_t t = b / nseg;
+        const uint32_t seg = static_cast<uint32_t>(b - t * nseg);
+        const uint32_t c0 = seg * (kSumLanes * kSumVecs) + threadIdx.x;
+        const bool tail = !kAligned && seg + 1 == nseg && threadIdx.x < left;
+        float acc[kSumVecs][N] = {};
+        float acc1 = 0.0f;
+        for (int64_t j0 = 0; j0 < top_k; j0 += kSlotChunk) {
+            int32_t r[kSlotChunk];
+            float w[kSlotChunk];
+            uint32_t mask = 0;
+#pragma unroll
+            for (int j = 0; j < kSlotChunk; ++j) {
+                r[j] = -1;
+                w[j] = 1.0f;
+                if (j0 + j < top_k) {
+                    r[j] = __builtin_amdgcn_readfirstlane(row_of[t * top_k + j0 + j]);
+                    if constexpr (kWeighted) w[j] = weights[t * top_k + j0 + j];
+                    if (r[j] >= 0 && r[j] < rows) mask |= 1u << j;
+                }
+            }
+            while (mask) {
+                int64_t at[kSumRows];
+                float ww[kSumRows];
+                int n = 0;
+#pragma unroll
+                for (int q = 0; q < kSumRows; ++q) {
+                    at[q] = 0;
+                    ww[q] = 0.0f;
+                    if (mask) {  // the lowest flagged slot, picked by compile-time indices only
+                        const int j = __builtin_ctz(mask);
+                        mask &= mask - 1;
+#pragma unroll
+                        for (int jj = 0; jj < kSlotChunk; ++jj)
+                            if (j == jj) {
+                                at[q] = r[jj];
+                                ww[q] = w[jj];
+                            }
+                        n = q + 1;
+                    }
+                }
+                typename In::Raw v[kSumRows][kSumVecs];
+                float v1[kSumRows];
+#pragma unroll
+                for (int q = 0; q < kSumRows; ++q) {
+                    v1[q] = 0.0f;
+                    if (q >= n) continue;
+                    const void* row = in + at[q] * hidden * kBytesOf<TI>;
+#pragma unroll
+                    for (int k = 0; k < kSumVecs; ++k) {
+                        const uint32_t c = c0 + k * kSumLanes;
+                        v[q][k] = c < nvec ? In::load(row, c * N) : typename In::Raw{};
+                    }
+                    if (tail) v1[q] = Elem<TI>::load1(row, done + threadIdx.x);
+                }
+#pragma unroll
+                for (int q = 0; q < kSumRows; ++q) {
+                    if (q >= n) continue;
+#pragma unroll
+                    for (int k = 0; k < kSumVecs; ++k) {
+                        float f[N];
+                        In::widen(v[q][k], f);
+#pragma unroll
+                        for (int i = 0; i < N; ++i)
+                            acc[k][i] = kWeighted ? __fmaf_rn(ww[q], f[i], acc[k][i]) : acc[k][i] + f[i];
+                    }
+                    acc1 = kWeighted ? __fmaf_rn(ww[q], v1[q], acc1) : acc1 + v1[q];
+                }
+            }
+        }
+        char* orow = out + t * hidden * kBytesOf<TO>;
+#pragma unroll
+        for (int k = 0; k < kSumVecs; ++k) {
+            const uint32_t c = c0 + k * kSumLanes;
+            if (c < nvec) Out::store(orow, c * N, acc[k]);
+        }
+        if (tail) Elem<TO>::store1(orow, done + threadIdx.x, acc1);
+    }
+}
+
+// ---- gradients of the weighted combine -----------------------------------------------
+
+constexpr int kGradLanes = 256;
+constexpr int kGradWaves = kGradLanes / 64;
+
+// One block per token: its gradient is read once for up to kSlotChunk slots,
+// each of their rows is read and its gradient written in the same pass, and
+// the products' partial sums stay in one register per slot.
+template <int TG, int TE, int N, bool kDot, bool kAligned>
+__global__ __launch_bounds__(kGradLanes) void moe_combine_grad_kernel(
+    const char* __restrict__ grad, const char* __restrict__ in, const int32_t* __restrict__ row_of,
+    const float* __restrict__ weights, char* __restrict__ grad_in, float* __restrict__ grad_w, int64_t rows,
+    int64_t tokens, int64_t top_k, int64_t hidden) {
+    typedef Vec<TG, N, kAligned> G;
+    typedef Vec<TE, N, kAligned> E;
+    __shared__ float part[kGradWaves][kSlotChunk];
+    const uint32_t nvec = static_cast<uint32_t>(hidden / N), done = nvec * N;
+    const uint32_t left = static_cast<uint32_t>(hidden) - done;
+    for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+        const char* grow = grad + t * hidden * kBytesOf<TG>;
+        for (int64_t j0 = 0; j0 < top_k; j0 += kSlotChunk) {
+            int64_t at[kSlotChunk];
+            float w[kSlotChunk], dot[kSlotChunk];
+            uint32_t mask = 0;
+#pragma unroll
+            for (int j = 0; j < kSlotChunk; ++j) {
+                at[j] = 0;
+                w[j] = dot[j] = 0.0f;
+                if (j0 + j < top_k) {
+                    const int32_t r = __builtin_amdgcn_readfirstlane(row_of[t * top_k + j0 + j]);
+                    w[j] = weights[t * top_k + j0 + j];
+                    if (r >= 0 && r < rows) mask |= 1u << j;
+                    at[j] = static_cast<int64_t>(r) * hidden * kBytesOf<TE>;
+                }
+            }
+            if (mask) {
+                for (uint32_t c = threadIdx.x; c < nvec; c += kGradLanes) {
+                    float g[N];
+                    G::widen(G::load(grow, c * N), g);
+#pragma unroll
+                    for (int j = 0; j < kSlotChunk; ++j) {
+                        if (!(mask >> j & 1u)) continue;
+                        float o[N];
+                        if constexpr (kDot) {
+                            float f[N];
+                            E::widen(E::load(in + at[j], c * N), f);
+#pragma unroll
+                            for (int i = 0; i < N; ++i) dot[j] = __fmaf_rn(g[i], f[i], dot[j]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < N; ++i) o[i] = w[j] * g[i];
+                        E::store(grad_in + at[j], c * N, o);
+                    }
+                }
+                if (!kAligned && threadIdx.x < left) {
+                    const float g = Elem<TG>::load1(grow, done + threadIdx.x);
+#pragma unroll
+                    for (int j = 0; j < kSlotChunk; ++j) {
+                        if (!(mask >> j & 1u)) continue;
+                        if constexpr (kDot)
+                            dot[j] = __fmaf_rn(g, Elem<TE>::load1(in + at[j], done + threadIdx.x), dot[j]);
+                        Elem<TE>::store1(grad_in + at[j], done + threadIdx.x, w[j] * g);
+                    }
+                }
+            }
+            if constexpr (kDot) {
+                const int lane = static_cast<int>(threadIdx.x & 63u), wave = static_cast<int>(threadIdx.x >> 6);
+#pragma unroll
+                for (int j = 0; j < kSlotChunk; ++j) {
+                    const float s = mask >> j & 1u ? group_sum<64>(dot[j]) : 0.0f;
+                    if (lane == 0) part[wave][j] = s;
+                }
+                __syncthreads();
+                if (threadIdx.x < kSlotChunk && j0 + threadIdx.x < top_k) {
+                    float s = 0.0f;
+#pragma unroll
+                    for (int v = 0; v < kGradWaves; ++v) s += part[v][threadIdx.x];
+                    grad_w[t * top_k + j0 + threadIdx.x] = s;
+                }
+                __syncthreads();
+            }
+        }
+    }
+}
+
+// ---- launches ------------------------------------------------------------------------
+
+template <int TI, int TO, bool kWeighted>
+int launch_sum(const void* in, const int32_t* row_of, const float* weights, void* out, int64_t rows, int64_t tokens,
+               int64_t top_k, int64_t hidden, hipStream_t st) {
+    constexpr int N = TI == MOE_EPI_F32 || TO == MOE_EPI_F32 ? 4 : 8;
+    const bool fit = hidden % N == 0 && aligned(in, N * kBytesOf<TI>) && aligned(out, N * kBytesOf<TO>);
+    const int64_t nvec = hidden / N, per = kSumLanes * kSumVecs;
+    const int64_t nseg = nvec <= per ? 1 : (nvec + per - 1) / per;
+    const dim3 grid(grid_for_rows(tokens * nseg, 1)), block(kSumLanes);
+    const char* i = static_cast<const char*>(in);
+    char* o = static_cast<char*>(out);
+    (void)hipGetLastError();
+    if (fit)
+        hipLaunchKernelGGL((moe_row_sum_kernel<TI, TO, N, kWeighted, true>), grid, block, 0, st, i, row_of, weights, o,
+                           rows, tokens, top_k, hidden, static_cast<uint32_t>(nseg));
+    else
+        hipLaunchKernelGGL((moe_row_sum_kernel<TI, TO, N, kWeighted, false>), grid, block, 0, st, i, row_of, weights,
+                           o, rows, tokens, top_k, hidden, static_cast<uint32_t>(nseg));
+    return launch_status();
+}
+
+template <int TG, int TE>
+int launch_grad(const void* grad, const void* in, const int32_t* row_of, const float* weights, void* grad_in,
+                float* grad_w, int64_t rows, int64_t tokens, int64_t top_k, int64_t hidden, hipStream_t st) {
+    constexpr int N = TG == MOE_EPI_F32 || TE == MOE_EPI_F32 ? 4 : 8;
+    const bool fit = hidden % N == 0 && aligned(grad, N * kBytesOf<TG>) && aligned(in, N * kBytesOf<TE>) &&
+                     aligned(grad_in, N * kBytesOf<TE>);
+    const dim3 grid(grid_for_rows(tokens, 1)), block(kGradLanes);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, block, 0, st, static_cast<const char*>(grad), static_cast<const char*>(in),
+                           row_of, weights, static_cast<char*>(grad_in), grad_w, rows, tokens, top_k, hidden);
+    };
+    (void)hipGetLastError();
+    if (fit && grad_w)
+        go(moe_combine_grad_kernel<TG, TE, N, true, true>);
+    else if (fit)
+        go(moe_combine_grad_kernel<TG, TE, N, false, true>);
+    else if (grad_w)
+        go(moe_combine_grad_kernel<TG, TE, N, true, false>);
+    else
+        go(moe_combine_grad_kernel<TG, TE, N, false, false>);
+    return launch_status();
+}
+
+// Sizes and byte counts shared by the calls below.
+struct Sizes {
+    int64_t row_bytes = 0, token_bytes = 0, slot_bytes = 0;
+    bool ok = false;
+    Sizes(int64_t rows, int64_t tokens, int64_t top_k, int64_t hidden, int row_elem, int token_elem) {
+        ok = rows >= 0 && tokens >= 0 && rows <= INT32_MAX && top_k >= 1 && top_k <= kMaxTopK && hidden >= 1 &&
+             row_fits_u32_offsets(hidden, 4) && tokens <= INT32_MAX / top_k &&
+             bytes_ok(rows, hidden, row_elem, &row_bytes) && bytes_ok(tokens, hidden, token_elem, &token_bytes);
+        slot_bytes = ok ? tokens * top_k * 4 : 0;
+    }
+};
+
+}  // namespace
+}  // namespace moe_epi
+
+using namespace moe_epi;
+
+extern "C" int moe_dispatch_fwd(const void* x, int dtype, const int32_t* slot_of, void* out, int64_t rows,
+                                int64_t tokens, int64_t top_k, int64_t hidden, void* stream) {
+    if (!dtype_ok(dtype)) return MOE_EPI_ERR_BAD_DTYPE;
+    const int e = elem_bytes(dtype);
+    const Sizes n(rows, tokens, top_k, hidden, e, e);
+    if (!n.ok) return MOE_EPI_ERR_BAD_SHAPE;
+    if (rows == 0) return MOE_EPI_SUCCESS;
+    if ((tokens > 0 && !x) || !slot_of || !out) return MOE_EPI_ERR_NULL_POINTER;
+    if (!aligned(x, e) || !aligned(out, e) || !aligned(slot_of, 4)) return MOE_EPI_ERR_MISALIGNED;
+    const Range ro = range_of(out, n.row_bytes);
+    if (overlaps(ro, range_of(x, n.token_bytes)) || overlaps(ro, range_of(slot_of, rows * 4))) return MOE_EPI_ERR_ALIAS;
+    const int64_t bytes = hidden * e, per = kCopyLanes * kCopyVecs;
+    const int64_t nseg = bytes / 16 <= per ? 1 : (bytes / 16 + per - 1) / per;
+    const dim3 grid(grid_for_rows(rows * nseg, 1)), block(kCopyLanes);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, block, 0, as_stream(stream), static_cast<const char*>(x), slot_of,
+                           static_cast<char*>(out), rows, tokens * top_k, static_cast<uint32_t>(top_k), bytes,
+                           static_cast<uint32_t>(nseg));
+    };
+    (void)hipGetLastError();
+    if (bytes % 16 == 0 && aligned(x, 16) && aligned(out, 16))
+        go(moe_dispatch_kernel<16>);
+    else if (bytes % 4 == 0 && aligned(x, 4) && aligned(out, 4))
+        go(moe_dispatch_kernel<4>);
+    else
+        go(moe_dispatch_kernel<2>);
+    return launch_status();
+}
+
+extern "C" int moe_dispatch_bwd(const void* grad_out, int dtype, const int32_t* row_of, void* grad_x, int64_t rows,
+                                int64_t tokens, int64_t top_k, int64_t hidden, void* stream) {
+    if (!dtype_ok(dtype)) return MOE_EPI_ERR_BAD_DTYPE;
+    const int e = elem_bytes(dtype);
+    const Sizes n(rows, tokens, top_k, hidden, e, e);
+    if (!n.ok) return MOE_EPI_ERR_BAD_SHAPE;
+    if (tokens == 0) return MOE_EPI_SUCCESS;
+    if ((rows > 0 && !grad_out) || !row_of || !grad_x) return MOE_EPI_ERR_NULL_POINTER;
+    if (!aligned(grad_out, e) || !aligned(grad_x, e) || !aligned(row_of, 4)) return MOE_EPI_ERR_MISALIGNED;
+    const Range ro = range_of(grad_x, n.token_bytes);
+    if (overlaps(ro, range_of(grad_out, n.row_bytes)) || overlaps(ro, range_of(row_of, n.slot_bytes)))
+        return MOE_EPI_ERR_ALIAS;
+    const hipStream_t st = as_stream(stream);
+    switch (dtype) {
+        case MOE_EPI_BF16:
+            return launch_sum<MOE_EPI_BF16, MOE_EPI_BF16, false>(grad_out, row_of, nullptr, grad_x, rows, tokens,
+                                                                 top_k, hidden, st);
+        case MOE_EPI_F16:
+            return launch_sum<MOE_EPI_F16, MOE_EPI_F16, false>(grad_out, row_of, nullptr, grad_x, rows, tokens, top_k,
+                                                               hidden, st);
+        default:
+            return launch_sum<MOE_EPI_F32, MOE_EPI_F32, false>(grad_out, row_of, nullptr, grad_x, rows, tokens, top_k,
+                                                               hidden, st);
+    }
+}
+
+extern "C" int moe_combine_weighted_fwd(const void* expert_out, int eo_dtype, const int32_t* row_of,
+                                        const float* weights, void* out, int out_dtype, int64_t rows, int64_t tokens,
+                                        int64_t top_k, int64_t hidden, void* stream) {
+    if (!dtype_ok(eo_dtype) || (out_dtype != eo_dtype && out_dtype != MOE_EPI_F32)) return MOE_EPI_ERR_BAD_DTYPE;
+    const int e = elem_bytes(eo_dtype), eo = elem_bytes(out_dtype);
+    const Sizes n(rows, tokens, top_k, hidden, e, eo);
+    if (!n.ok) return MOE_EPI_ERR_BAD_SHAPE;
+    if (tokens == 0) return MOE_EPI_SUCCESS;
+    if ((rows > 0 && !expert_out) || !row_of || !weights || !out) return MOE_EPI_ERR_NULL_POINTER;
+    if (!aligned(expert_out, e) || !aligned(out, eo) || !aligned(row_of, 4) || !aligned(weights, 4))
+        return MOE_EPI_ERR_MISALIGNED;
+    const Range ro = range_of(out, n.token_bytes);
+    if (overlaps(ro, range_of(expert_out, n.row_bytes)) || overlaps(ro, range_of(row_of, n.slot_bytes)) ||
+        overlaps(ro, range_of(weights, n.slot_bytes)))
+        return MOE_EPI_ERR_ALIAS;
+    const hipStream_t st = as_stream(stream);
+    auto go = [&](auto launch) { return launch(expert_out, row_of, weights, out, rows, tokens, top_k, hidden, st); };
+    if (eo_dtype == MOE_EPI_F32) return go(launch_sum<MOE_EPI_F32, MOE_EPI_F32, true>);
+    if (eo_dtype == MOE_EPI_BF16)
+        return out_dtype == MOE_EPI_F32 ? go(launch_sum<MOE_EPI_BF16, MOE_EPI_F32, true>)
+                                        : go(launch_sum<MOE_EPI_BF16, MOE_EPI_BF16, true>);
+    return out_dtype == MOE_EPI_F32 ? go(launch_sum<MOE_EPI_F16, MOE_EPI_F32, true>)
+                                    : go(launch_sum<MOE_EPI_F16, MOE_EPI_F16, true>);
+}
+
+extern "C" int moe_combine_weighted_bwd(const void* grad_out, int go_dtype, const void* expert_out, int eo_dtype,
+                                        const int32_t* row_of, const float* weights, void* grad_expert_out,
+                                        float* grad_weights, int64_t rows, int64_t tokens, int64_t top_k,
+                                        int64_t hidden, void* stream) {
+    if (!dtype_ok(eo_dtype) || (go_dtype != eo_dtype && go_dtype != MOE_EPI_F32)) return MOE_EPI_ERR_BAD_DTYPE;
+    const int e = elem_bytes(eo_dtype), g = elem_bytes(go_dtype);
+    const Sizes n(rows, tokens, top_k, hidden, e, g);
+    if (!n.ok) return MOE_EPI_ERR_BAD_SHAPE;
+    if (tokens == 0) return MOE_EPI_SUCCESS;
+    if (!grad_out || !row_of || !weights || (rows > 0 && !grad_expert_out) ||
+        (rows > 0 && grad_weights && !expert_out))
+        return MOE_EPI_ERR_NULL_POINTER;
+    if (!aligned(grad_out, g) || !aligned(expert_out, e) || !aligned(grad_expert_out, e) || !aligned(row_of, 4) ||
+        !aligned(weights, 4) || !aligned(grad_weights, 4))
+        return MOE_EPI_ERR_MISALIGNED;
+    const Range in[4] = {range_of(grad_out, n.token_bytes), range_of(expert_out, expert_out ? n.row_bytes : 0),
+                         range_of(row_of, n.slot_bytes), range_of(weights, n.slot_bytes)},
+                gi = range_of(grad_expert_out, n.row_bytes), gw = range_of(grad_weights, grad_weights ? n.slot_bytes : 0);
+    for (const Range& r : in)
+        if (overlaps(gi, r) || overlaps(gw, r)) return MOE_EPI_ERR_ALIAS;
+    if (overlaps(gi, gw)) return MOE_EPI_ERR_ALIAS;
+    const hipStream_t st = as_stream(stream);
+    auto go = [&](auto launch) {
+        return launch(grad_out, expert_out, row_of, weights, grad_expert_out, grad_weights, rows, tokens, top_k,
+                      hidden, st);
+    };
+    if (eo_dtype == MOE_EPI_F32) return go(launch_grad<MOE_EPI_F32, MOE_EPI_F32>);
+    if (eo_dtype == MOE_EPI_BF16)
+        return go_dtype == MOE_EPI_F32 ? go(launch_grad<MOE_EPI_F32, MOE_EPI_BF16>)
+                                       : go(launch_grad<MOE_EPI_BF16, MOE_EPI_BF16>);
+    return go_dtype == MOE_EPI_F32 ? go(launch_grad<MOE_EPI_F32, MOE_EPI_F16>)
+                                   : go(launch_grad<MOE_EPI_F16, MOE_EPI_F16>);
+}

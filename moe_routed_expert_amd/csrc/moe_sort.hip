@@ -1,0 +1,247 @@
+// Order of the routed rows (gfx950): a stable counting sort of the slots by
+// local expert.
+//
+// A slot s = t * top_k + j names an expert; with first <= expert < first +
+// experts its bucket is expert - first, otherwise it has no row. With
+//   start[b] = number of slots in buckets below b,
+//   rank[s]  = number of slots s' < s in s's own bucket,
+// the row of s is start[b] + rank[s]. Both are counts of whole numbers, so
+// the result does not depend on the order in which they are formed.
+//
+// Ranks within a wavefront come from ballots: one per bit of the bucket gives
+// each lane the mask of the lanes in its own bucket, the bits below the lane
+// are its rank, and the lowest lane of each mask adds the mask's count to the
+// wavefront's counter of that bucket. The counters are private to a
+// wavefront, so no atomic operation is needed.
+#include "epi_common.h"
+#include "moe_routed.h"
+
+namespace moe_epi {
+namespace {
+
+constexpr int kMaxExperts = 1024;
+constexpr int64_t kMaxSlotsPerToken = 1024;
+constexpr int kGroups = 4;                       // groups of 64 slots per wavefront of a tile
+constexpr int kTileThreads = 1024;
+constexpr int kTileWaves = kTileThreads / 64;
+constexpr int kTile = kTileThreads * kGroups;    // slots per block
+
+inline int bits_for(int64_t experts) {           // buckets 0 .. experts (experts: no row)
+    int n = 0;
+    while ((experts >> n) != 0) ++n;
+    return n;
+}
+
+// The bucket of slot s; `experts` for a slot without a row or past the end.
+template <class Id>
+__device__ __forceinline__ uint32_t bucket_of(const Id* __restrict__ ids, int64_t s, int64_t slots, int64_t first,
+                                              int experts) {
+    if (s >= slots) return static_cast<uint32_t>(experts);
+    const uint64_t b = static_cast<uint64_t>(static_cast<int64_t>(ids[s])) - static_cast<uint64_t>(first);
+    return b < static_cast<uint64_t>(experts) ? static_cast<uint32_t>(b) : static_cast<uint32_t>(experts);
+}
+
+// The lanes of the wavefront whose bucket equals the calling lane's.
+__device__ __forceinline__ uint64_t same_bucket(uint32_t b, int nbits) {
+    uint64_t mask = ~uint64_t{0};
+    for (int i = 0; i < nbits; ++i) {
+        const bool on = (b >> i) & 1u;
+        const uint64_t v = __ballot(on);
+        mask &= on ? v : ~v;
+    }
+    return mask;
+}
+
+__device__ __forceinline__ int rank_in(uint64_t mask) {
+    return __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                     __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0u));
+}
+
+__device__ __forceinline__ bool is_lowest(uint64_t mask) {
+    return __builtin_ctzll(mask) == static_cast<int>(threadIdx.x & 63u);
+}
+
+// Exclusive scan of n counts in LDS by the calling wavefront, in place; returns the total.
+__device__ __forceinline__ int wave_scan(int* v, int n) {
+    const int lane = static_cast<int>(threadIdx.x & 63u);
+    int carry = 0;
+    for (int i0 = 0; i0 < n; i0 += 64) {
+        const int c = i0 + lane < n ? v[i0 + lane] : 0;
+        int x = c;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int y = __shfl_up(x, d, 64);
+            if (lane >= d) x += y;
+        }
+        if (i0 + lane < n) v[i0 + lane] = carry + x - c;
+        carry += __shfl(x, 63, 64);
+    }
+    return carry;
+}
+
+// Counts of one tile's slots per bucket: hist[tile * experts + b].
+template <class Id>
+__global__ __launch_bounds__(kTileThreads) void moe_sort_count(const Id* __restrict__ ids, int* __restrict__ hist,
+                                                               int64_t slots, int64_t first, int experts) {
+    __shared__ int count[kMaxExperts];
+    for (int e = threadIdx.x; e < experts; e += kTileThreads) count[e] = 0;
+    __syncthreads();
+    const int64_t s0 = static_cast<int64_t>(blockIdx.x) * kTile + threadIdx.x;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        const uint32_t b = bucket_of(ids, s0 + g * kTileThreads, slots, first, experts);
+        if (b < static_cast<uint32_t>(experts)) atomicAdd(&count[b], 1);  // whole numbers: any order, one sum
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < experts; e += kTileThreads)
+        hist[static_cast<int64_t>(blockIdx.x) * experts + e] = count[e];
+}
+
+// Rows of one tile's slots. hist holds every tile's counts (not read when
+// there is one tile: its own counts are then the totals).
+template <class Id>
+__global__ __launch_bounds__(kTileThreads) void moe_sort_place(const Id* __restrict__ ids,
+                                                               const int* __restrict__ hist, int* __restrict__ offs,
+                                                               int* __restrict__ row_of, int* __restrict__ slot_of,
+                                                               int64_t slots, int64_t first, int experts, int nbits,
+                                                               int tiles) {
+    // counts per wavefront and bucket (a tile has 4096 slots), total and start per bucket
+    extern __shared__ uint16_t wave_count[];  // [kTileWaves][experts]
+    __shared__ int before[kMaxExperts];       // slots of the bucket in earlier tiles
+    __shared__ int start[kMaxExperts];
+    __shared__ int total_rows;
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
+    const int tile = static_cast<int>(blockIdx.x);
+
+    for (int i = tid; i < kTileWaves * experts; i += kTileThreads) wave_count[i] = 0;
+    for (int e = tid; e < experts; e += kTileThreads) before[e] = start[e] = 0;
+    __syncthreads();
+
+    const int64_t s0 = static_cast<int64_t>(tile) * kTile + wave * (64 * kGroups) + lane;
+    uint32_t b[kGroups];
+    uint64_t mask[kGroups];
+    uint16_t* mine = wave_count + wave * experts;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) b[g] = bucket_of(ids, s0 + g * 64, slots, first, experts);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        mask[g] = same_bucket(b[g], nbits);
+        if (b[g] < static_cast<uint32_t>(experts) && is_lowest(mask[g])) mine[b[g]] += __popcll(mask[g]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    if (tiles > 1) {
+        // earlier tiles' counts and all tiles' counts of each bucket
+        for (int64_t i = tid; i < static_cast<int64_t>(tiles) * experts; i += kTileThreads) {
+            const int c = hist[i], e = static_cast<int>(i % experts);
+            if (c != 0) {
+                atomicAdd(&start[e], c);
+                if (i / experts < tile) atomicAdd(&before[e], c);
+            }
+        }
+    }
+    __syncthreads();
+    // the wavefronts' counts become the slots of the bucket in the tile's earlier wavefronts
+    for (int e = tid; e < experts; e += kTileThreads) {
+        int n = 0;
+        for (int w = 0; w < kTileWaves; ++w) {
+            const int c = wave_count[w * experts + e];
+            wave_count[w * experts + e] = static_cast<uint16_t>(n);
+            n += c;
+        }
+        if (tiles == 1) start[e] = n;
+        if (tile == 0) before[e] = 0;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        const int n = wave_scan(start, experts);
+        if (lane == 0) total_rows = n;
+    }
+    __syncthreads();
+    const int rows = total_rows;
+    if (tile == 0)
+        for (int e = tid; e < experts; e += kTileThreads) offs[e] = e + 1 < experts ? start[e + 1] : rows;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        const int64_t s = s0 + g * 64;
+        int row = -1;
+        if (b[g] < static_cast<uint32_t>(experts)) {
+            row = start[b[g]] + before[b[g]] + mine[b[g]] + rank_in(mask[g]);
+            slot_of[row] = static_cast<int>(s);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (b[g] < static_cast<uint32_t>(experts) && is_lowest(mask[g])) mine[b[g]] += __popcll(mask[g]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (s < slots) {
+            row_of[s] = row;
+            if (s >= rows) slot_of[s] = -1;  // past the last row
+        }
+    }
+}
+
+__global__ void moe_sort_empty(int* __restrict__ offs, int experts) {
+    for (int e = threadIdx.x; e < experts; e += blockDim.x) offs[e] = 0;
+}
+
+bool sizes_ok(int64_t tokens, int64_t top_k, int64_t experts) {
+    return tokens >= 0 && top_k >= 1 && top_k <= kMaxSlotsPerToken && experts >= 1 && experts <= kMaxExperts &&
+           tokens <= INT32_MAX / top_k;
+}
+
+int64_t tiles_of(int64_t slots) { return (slots + kTile - 1) / kTile; }
+
+template <class Id>
+void launch_sort(const void* ids, int64_t first, int* offs, int* row_of, int* slot_of, int* hist, int64_t slots,
+                 int experts, hipStream_t st) {
+    const int tiles = static_cast<int>(tiles_of(slots));
+    const Id* p = static_cast<const Id*>(ids);
+    if (tiles > 1)
+        hipLaunchKernelGGL((moe_sort_count<Id>), dim3(tiles), dim3(kTileThreads), 0, st, p, hist, slots, first,
+                           experts);
+    hipLaunchKernelGGL((moe_sort_place<Id>), dim3(tiles), dim3(kTileThreads),
+                       kTileWaves * experts * static_cast<int>(sizeof(uint16_t)), st, p, hist, offs, row_of, slot_of,
+                       slots, first, experts, bits_for(experts), tiles);
+}
+
+}  // namespace
+}  // namespace moe_epi
+
+using namespace moe_epi;
+
+extern "C" int64_t moe_sort_workspace_bytes(int64_t tokens, int64_t top_k, int64_t experts) {
+    if (!sizes_ok(tokens, top_k, experts)) return -1;
+    const int64_t tiles = tiles_of(tokens * top_k);
+    return tiles > 1 ? tiles * experts * 4 : 0;
+}
+
+extern "C" int moe_sort_fwd(const void* expert_of, int id_bytes, int64_t first_expert, int32_t* offs, int32_t* row_of,
+                            int32_t* slot_of, void* workspace, int64_t workspace_bytes, int64_t tokens, int64_t top_k,
+                            int64_t experts, void* stream) {
+    if (id_bytes != 4 && id_bytes != 8) return MOE_EPI_ERR_BAD_DTYPE;
+    const int64_t need = moe_sort_workspace_bytes(tokens, top_k, experts);
+    if (need < 0 || workspace_bytes < need) return MOE_EPI_ERR_BAD_SHAPE;
+    const int64_t slots = tokens * top_k;
+    if (!offs || (need > 0 && !workspace)) return MOE_EPI_ERR_NULL_POINTER;
+    if (slots > 0 && (!expert_of || !row_of || !slot_of)) return MOE_EPI_ERR_NULL_POINTER;
+    if (!aligned(expert_of, id_bytes) || !aligned(offs, 4) || !aligned(row_of, 4) || !aligned(slot_of, 4) ||
+        !aligned(workspace, 4))
+        return MOE_EPI_ERR_MISALIGNED;
+    const Range in = range_of(expert_of, slots * id_bytes),
+                out[4] = {range_of(offs, experts * 4), range_of(row_of, slots * 4), range_of(slot_of, slots * 4),
+                          range_of(workspace, need)};
+    for (int i = 0; i < 4; ++i) {
+        if (overlaps(out[i], in)) return MOE_EPI_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(out[i], out[j])) return MOE_EPI_ERR_ALIAS;
+    }
+    (void)hipGetLastError();
+    const hipStream_t st = as_stream(stream);
+    if (slots == 0)
+        hipLaunchKernelGGL(moe_sort_empty, dim3(1), dim3(256), 0, st, offs, static_cast<int>(experts));
+    else if (id_bytes == 4)
+        launch_sort<int32_t>(expert_of, first_expert, offs, row_of, slot_of, static_cast<int*>(workspace), slots,
+                             static_cast<int>(experts), st);
+    else
+        launch_sort<int64_t>(expert_of, first_expert, offs, row_of, slot_of, static_cast<int*>(workspace), slots,
+                             static_cast<int>(experts), st);
+    return launch_status();
+}

@@ -1,0 +1,309 @@
+"""Python binding of the steps around the routed experts (ctypes; argument marshalling only).
+
+Names follow the C ABI (include/moe_routed.h):
+  moe_sort_fwd(expert_of, first_expert, offs, row_of, slot_of, workspace)
+  moe_dispatch_fwd(x, slot_of, top_k, out)
+  moe_dispatch_bwd(grad_out, row_of, grad_x)
+  moe_combine_weighted_fwd(expert_out, row_of, weights, out)
+  moe_combine_weighted_bwd(grad_out, expert_out, row_of, weights, grad_expert_out, grad_weights)
+  quantize_rows_int8_fwd(x, q, scale)
+  grouped_gate_up_swiglu_int8_fwd(a, a_scale, slot_of, top_k, w_gate, w_gate_scale, w_up, w_up_scale, offs, probs,
+                                  y, limit)
+  grouped_down_router_int8_fwd(h, h_scale, w_down, w_down_scale, offs, probs, out)
+plus allocating helpers (moe_sort, quantize_rows_int8) and torch.autograd.Function wrappers
+(MoeDispatch, MoeCombineWeighted). Every call writes into tensors of the caller, on the current
+stream of their device, and raises TypeError / ValueError for tensors the C ABI cannot take and
+MoeEpiError for a status other than success. There is no fallback.
+
+These calls are also made for single tokens, where a kernel runs for a few microseconds, so a
+tensor that is as expected passes one short test, and the message is formed only when it is not.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import binding
+from .binding import DTYPE_CODE, MoeEpiError
+
+_BF16, _F32, _I32, _I64, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.int8
+_fns = None
+
+
+def _lib():
+    """The library with the signatures of this module's calls set."""
+    global _fns
+    if _fns is None:
+        L = binding.lib()
+        vp, i64, f32, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int
+        L.moe_sort_fwd.argtypes = [vp, i32, i64, vp, vp, vp, vp, i64, i64, i64, i64, vp]
+        L.moe_sort_workspace_bytes.argtypes = [i64, i64, i64]
+        L.moe_dispatch_fwd.argtypes = [vp, i32, vp, vp, i64, i64, i64, i64, vp]
+        L.moe_dispatch_bwd.argtypes = [vp, i32, vp, vp, i64, i64, i64, i64, vp]
+        L.moe_combine_weighted_fwd.argtypes = [vp, i32, vp, vp, vp, i32, i64, i64, i64, i64, vp]
+        L.moe_combine_weighted_bwd.argtypes = [vp, i32, vp, i32, vp, vp, vp, vp, i64, i64, i64, i64, vp]
+        L.quantize_rows_int8_fwd.argtypes = [vp, i32, vp, vp, i64, i64, vp]
+        L.grouped_gate_up_swiglu_int8_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64,
+                                                      i64, f32, vp]
+        L.grouped_down_router_int8_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i64, i64, i64, i64, vp]
+        for name in ("moe_sort_fwd", "moe_dispatch_fwd", "moe_dispatch_bwd", "moe_combine_weighted_fwd",
+                     "moe_combine_weighted_bwd", "quantize_rows_int8_fwd", "grouped_gate_up_swiglu_int8_fwd",
+                     "grouped_down_router_int8_fwd"):
+            getattr(L, name).restype = ctypes.c_int
+        L.moe_sort_workspace_bytes.restype = i64
+        _fns = L
+    return _fns
+
+
+def _take(t, name: str, dtype, shape, device: int) -> int:
+    """The address of a contiguous tensor of this dtype and shape on this GPU; raises otherwise."""
+    if (t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == device and device >= 0
+            and t.is_contiguous()):
+        return t.data_ptr()
+    where = torch.device("cuda", device) if device >= 0 else torch.device("cuda")
+    binding._need(t, name, dtype, [shape], where)
+    raise ValueError(f"{name}: expected a tensor on {where}, got {t.device}")
+
+
+def _code(t: torch.Tensor, name: str) -> int:
+    code = DTYPE_CODE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
+    return code
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _vector(t: torch.Tensor, name: str) -> int:
+    if t.dim() != 1:
+        raise ValueError(f"{name} must be 1-D, got {tuple(t.shape)}")
+    return t.shape[0]
+
+
+def _experts(w: torch.Tensor, name: str):
+    if w.dim() != 3:
+        raise ValueError(f"{name} must be 3-D [experts, out, in], got {tuple(w.shape)}")
+    return w.shape
+
+
+def _stream(device: int, stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _check(status: int, where: str) -> None:
+    if status:
+        raise MoeEpiError(status, where)
+
+
+# ---- order of the rows ------------------------------------------------------------
+
+def moe_sort_workspace_bytes(tokens: int, top_k: int, experts: int) -> int:
+    """Bytes of workspace that moe_sort_fwd needs for these sizes (0: it may be None)."""
+    n = _lib().moe_sort_workspace_bytes(int(tokens), int(top_k), int(experts))
+    if n < 0:
+        raise ValueError(f"moe_sort_fwd takes no tokens={tokens}, top_k={top_k}, experts={experts}")
+    return n
+
+
+def moe_sort_fwd(expert_of, first_expert: int, offs, row_of, slot_of, workspace=None, stream=None) -> None:
+    """Order of the routed rows. expert_of [tokens, top_k] int32 or int64; the experts of this GPU are
+    [first_expert, first_expert + len(offs)). offs int32 [experts] cumulative row counts; row_of int32
+    [tokens, top_k] the row of each slot or -1; slot_of int32 [tokens * top_k] the slot of each row, -1
+    past the last; workspace uint8 of moe_sort_workspace_bytes, or None if that is 0."""
+    tokens, top_k = _matrix(expert_of, "expert_of")
+    dev, wide = expert_of.get_device(), expert_of.dtype is _I64
+    experts = _vector(offs, "offs")
+    ids = _take(expert_of, "expert_of", _I64 if wide else _I32, (tokens, top_k), dev)
+    ws, nbytes = None, 0
+    if workspace is not None:
+        nbytes = _vector(workspace, "workspace")
+        ws = _take(workspace, "workspace", torch.uint8, (nbytes,), dev)
+    _check(_lib().moe_sort_fwd(ids, 8 if wide else 4, first_expert, _take(offs, "offs", _I32, (experts,), dev),
+                               _take(row_of, "row_of", _I32, (tokens, top_k), dev),
+                               _take(slot_of, "slot_of", _I32, (tokens * top_k,), dev), ws, nbytes, tokens, top_k,
+                               experts, _stream(dev, stream)), "moe_sort_fwd")
+
+
+def moe_sort(expert_of, experts: int, first_expert: int = 0):
+    """(offs, row_of, slot_of) of moe_sort_fwd in new tensors."""
+    tokens, top_k = _matrix(expert_of, "expert_of")
+    dev = expert_of.device
+    offs = torch.empty(experts, dtype=_I32, device=dev)
+    row_of = torch.empty((tokens, top_k), dtype=_I32, device=dev)
+    slot_of = torch.empty(tokens * top_k, dtype=_I32, device=dev)
+    workspace = torch.empty(moe_sort_workspace_bytes(tokens, top_k, experts), dtype=torch.uint8, device=dev)
+    moe_sort_fwd(expert_of.contiguous(), first_expert, offs, row_of, slot_of, workspace)
+    return offs, row_of, slot_of
+
+
+# ---- moves of the rows ---------------------------------------------------------------
+
+def moe_dispatch_fwd(x, slot_of, top_k: int, out, stream=None) -> None:
+    """out[r] = x[slot_of[r] // top_k] for every row r whose slot is in range, zeros for the others. x [tokens,
+    hidden], out [rows, hidden] of x's dtype (bf16, fp16 or fp32); slot_of int32 [rows]."""
+    tokens, hidden = _matrix(x, "x")
+    rows, dev, dt, code = _vector(slot_of, "slot_of"), x.get_device(), x.dtype, _code(x, "x")
+    _check(_lib().moe_dispatch_fwd(_take(x, "x", dt, (tokens, hidden), dev), code,
+                                   _take(slot_of, "slot_of", _I32, (rows,), dev),
+                                   _take(out, "out", dt, (rows, hidden), dev), rows, tokens, top_k, hidden,
+                                   _stream(dev, stream)), "moe_dispatch_fwd")
+
+
+def moe_dispatch_bwd(grad_out, row_of, grad_x, stream=None) -> None:
+    """grad_x[t] = the fp32 sum of grad_out[row_of[t, j]] over the slots that have a row, rounded once.
+    grad_out [rows, hidden], grad_x [tokens, hidden] of one dtype; row_of int32 [tokens, top_k]."""
+    rows, hidden = _matrix(grad_out, "grad_out")
+    tokens, top_k = _matrix(row_of, "row_of")
+    dev, dt, code = grad_x.get_device(), grad_out.dtype, _code(grad_out, "grad_out")
+    _check(_lib().moe_dispatch_bwd(_take(grad_out, "grad_out", dt, (rows, hidden), dev), code,
+                                   _take(row_of, "row_of", _I32, (tokens, top_k), dev),
+                                   _take(grad_x, "grad_x", dt, (tokens, hidden), dev), rows, tokens, top_k, hidden,
+                                   _stream(dev, stream)), "moe_dispatch_bwd")
+
+
+def moe_combine_weighted_fwd(expert_out, row_of, weights, out, stream=None) -> None:
+    """out[t] = the fp32 sum of weights[t, j] * expert_out[row_of[t, j]] over the slots that have a row,
+    rounded once. expert_out [rows, hidden] (bf16, fp16 or fp32); row_of int32 and weights fp32
+    [tokens, top_k]; out [tokens, hidden] of expert_out's dtype or fp32."""
+    rows, hidden = _matrix(expert_out, "expert_out")
+    tokens, top_k = _matrix(row_of, "row_of")
+    dev, code, out_code = out.get_device(), _code(expert_out, "expert_out"), _code(out, "out")
+    _check(_lib().moe_combine_weighted_fwd(
+        _take(expert_out, "expert_out", expert_out.dtype, (rows, hidden), dev), code,
+        _take(row_of, "row_of", _I32, (tokens, top_k), dev), _take(weights, "weights", _F32, (tokens, top_k), dev),
+        _take(out, "out", out.dtype, (tokens, hidden), dev), out_code, rows, tokens, top_k, hidden,
+        _stream(dev, stream)), "moe_combine_weighted_fwd")
+
+
+def moe_combine_weighted_bwd(grad_out, expert_out, row_of, weights, grad_expert_out, grad_weights,
+                             stream=None) -> None:
+    """grad_expert_out[row_of[t, j]] = weights[t, j] * grad_out[t]; grad_weights[t, j] = the dot product of
+    grad_out[t] and expert_out[row_of[t, j]] (fp32), 0 for a slot without a row. grad_out of expert_out's
+    dtype or fp32. expert_out and grad_weights may both be None (weights without gradient)."""
+    tokens, hidden = _matrix(grad_out, "grad_out")
+    top_k = _matrix(row_of, "row_of")[1]
+    rows, dt, dev = _matrix(grad_expert_out, "grad_expert_out")[0], grad_expert_out.dtype, grad_out.get_device()
+    code, grad_code, eo, gw = _code(grad_expert_out, "grad_expert_out"), _code(grad_out, "grad_out"), None, None
+    if grad_weights is not None:
+        eo = _take(expert_out, "expert_out", dt, (rows, hidden), dev)
+        gw = _take(grad_weights, "grad_weights", _F32, (tokens, top_k), dev)
+    _check(_lib().moe_combine_weighted_bwd(
+        _take(grad_out, "grad_out", grad_out.dtype, (tokens, hidden), dev), grad_code, eo, code,
+        _take(row_of, "row_of", _I32, (tokens, top_k), dev),
+        _take(weights, "weights", _F32, (tokens, top_k), dev),
+        _take(grad_expert_out, "grad_expert_out", dt, (rows, hidden), dev), gw, rows, tokens, top_k, hidden,
+        _stream(dev, stream)), "moe_combine_weighted_bwd")
+
+
+class MoeDispatch(torch.autograd.Function):
+    """The tokens' rows in expert order: MoeDispatch.apply(x, row_of, slot_of). slot_of is moe_sort's
+    first `rows` entries; rows past the last one are zeros."""
+
+    @staticmethod
+    def forward(ctx, x, row_of, slot_of):
+        ctx.save_for_backward(row_of)
+        ctx.tokens = x.shape[0]
+        out = torch.empty((slot_of.shape[0], x.shape[1]), dtype=x.dtype, device=x.device)
+        moe_dispatch_fwd(x.contiguous(), slot_of, row_of.shape[1], out)
+        return out
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        row_of, = ctx.saved_tensors
+        grad_x = torch.empty((ctx.tokens, grad_out.shape[1]), dtype=grad_out.dtype, device=grad_out.device)
+        moe_dispatch_bwd(grad_out.contiguous(), row_of, grad_x)
+        return grad_x, None, None
+
+
+class MoeCombineWeighted(torch.autograd.Function):
+    """The weighted sum of each token's rows: MoeCombineWeighted.apply(expert_out, row_of, weights,
+    out_dtype=None). expert_out is kept for the backward pass only when weights need a gradient."""
+
+    @staticmethod
+    def forward(ctx, expert_out, row_of, weights, out_dtype=None):
+        expert_out, weights = expert_out.contiguous(), weights.contiguous()
+        ctx.save_for_backward(expert_out if ctx.needs_input_grad[2] else None, row_of, weights)
+        ctx.rows, ctx.dtype = expert_out.shape[0], expert_out.dtype
+        out = torch.empty((row_of.shape[0], expert_out.shape[1]), dtype=out_dtype or expert_out.dtype,
+                          device=expert_out.device)
+        moe_combine_weighted_fwd(expert_out, row_of, weights, out)
+        return out
+
+    @staticmethod
+    def backward(ctx, grad_out):
+        expert_out, row_of, weights = ctx.saved_tensors
+        # rows that belong to no slot have gradient 0
+        grad_rows = torch.zeros((ctx.rows, grad_out.shape[1]), dtype=ctx.dtype, device=grad_out.device)
+        grad_weights = torch.empty_like(weights) if ctx.needs_input_grad[2] else None
+        moe_combine_weighted_bwd(grad_out.contiguous(), expert_out, row_of, weights, grad_rows, grad_weights)
+        return grad_rows, None, grad_weights, None
+
+
+# ---- 8-bit integers ---------------------------------------------------------------------
+
+def quantize_rows_int8_fwd(x, q, scale, stream=None) -> None:
+    """scale[r] = max|x[r]| / 127, q[r] = rint(127 x[r] / max|x[r]|). x [rows, cols] (bf16, fp16 or fp32);
+    q int8 [rows, cols]; scale fp32 [rows]."""
+    rows, cols = _matrix(x, "x")
+    dev, code = x.get_device(), _code(x, "x")
+    _check(_lib().quantize_rows_int8_fwd(_take(x, "x", x.dtype, (rows, cols), dev), code,
+                                         _take(q, "q", _I8, (rows, cols), dev),
+                                         _take(scale, "scale", _F32, (rows,), dev), rows, cols,
+                                         _stream(dev, stream)), "quantize_rows_int8_fwd")
+
+
+def quantize_rows_int8(x):
+    """(q, scale) of x in new tensors. x [..., cols]: the leading dimensions are rows, so that weights
+    [experts, out, in] get a scale for each output channel."""
+    q = torch.empty(x.shape, dtype=_I8, device=x.device)
+    scale = torch.empty(x.shape[:-1], dtype=_F32, device=x.device)
+    quantize_rows_int8_fwd(x.reshape(-1, x.shape[-1]), q.view(-1, x.shape[-1]), scale.view(-1))
+    return q, scale
+
+
+def grouped_gate_up_swiglu_int8_fwd(a, a_scale, slot_of, top_k: int, w_gate, w_gate_scale, w_up, w_up_scale, offs,
+                                    probs, y, limit: float, stream=None) -> None:
+    """gate_up grouped product in 8-bit integers + clamped SwiGLU x probs. a int8 [tokens, hidden] with
+    a_scale fp32 [tokens]; slot_of int32 [rows] (row r reads token slot_of[r] // top_k) or None (row r
+    reads row r of a, top_k 1); w_gate, w_up int8 [experts, inter, hidden] with scales fp32 [experts,
+    inter]; offs int32 [experts] cumulative row counts (on the device); probs fp32 [rows] or None for 1;
+    y bf16 [rows, inter]."""
+    tokens, hidden = _matrix(a, "a")
+    experts, inter, _ = _experts(w_gate, "w_gate")
+    rows, dev = _matrix(y, "y")[0], a.get_device()
+    _check(_lib().grouped_gate_up_swiglu_int8_fwd(
+        _take(a, "a", _I8, (tokens, hidden), dev), _take(a_scale, "a_scale", _F32, (tokens,), dev),
+        None if slot_of is None else _take(slot_of, "slot_of", _I32, (rows,), dev),
+        _take(w_gate, "w_gate", _I8, (experts, inter, hidden), dev),
+        _take(w_gate_scale, "w_gate_scale", _F32, (experts, inter), dev),
+        _take(w_up, "w_up", _I8, (experts, inter, hidden), dev),
+        _take(w_up_scale, "w_up_scale", _F32, (experts, inter), dev), _take(offs, "offs", _I32, (experts,), dev),
+        None if probs is None else _take(probs, "probs", _F32, (rows,), dev),
+        _take(y, "y", _BF16, (rows, inter), dev), rows, tokens, top_k, hidden, inter, experts, limit,
+        _stream(dev, stream)), "grouped_gate_up_swiglu_int8_fwd")
+
+
+def grouped_down_router_int8_fwd(h, h_scale, w_down, w_down_scale, offs, probs, out, stream=None) -> None:
+    """Down grouped product in 8-bit integers + router multiply. h int8 [rows, inter] with h_scale fp32
+    [rows]; w_down int8 [experts, hidden, inter] with w_down_scale fp32 [experts, hidden]; offs int32
+    [experts] cumulative row counts (on the device); probs fp32 [rows] or None for 1; out [rows, hidden]
+    bf16 or fp32."""
+    rows, inter = _matrix(h, "h")
+    experts, hidden, _ = _experts(w_down, "w_down")
+    dev = h.get_device()
+    if out.dtype is not _BF16 and out.dtype is not _F32:
+        raise TypeError(f"out: expected bfloat16 or float32, got {out.dtype}")
+    _check(_lib().grouped_down_router_int8_fwd(
+        _take(h, "h", _I8, (rows, inter), dev), _take(h_scale, "h_scale", _F32, (rows,), dev),
+        _take(w_down, "w_down", _I8, (experts, hidden, inter), dev),
+        _take(w_down_scale, "w_down_scale", _F32, (experts, hidden), dev), _take(offs, "offs", _I32, (experts,), dev),
+        None if probs is None else _take(probs, "probs", _F32, (rows,), dev),
+        _take(out, "out", out.dtype, (rows, hidden), dev), DTYPE_CODE[out.dtype], rows, inter, hidden, experts,
+        _stream(dev, stream)), "grouped_down_router_int8_fwd")

@@ -83,6 +83,47 @@ __device__ __forceinline__ void stage_barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// The mt-th row tile of bm rows over all experts in order (rows == 0: there is
+// none). The whole wavefront takes 64 experts at a time: with the running
+// maximum of offs as the clamped end of each expert and the running sum of
+// their tiles, the expert is the first whose sum passes mt. One expert after
+// the other, as many dependent reads as experts, would take longer than a
+// short product.
+struct RowTile {
+    int row0, rows, expert;
+};
+__device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offs, int rows, int experts, int mt, int bm) {
+    const int lane = static_cast<int>(threadIdx.x & 63u);
+    int carry = 0, before = 0;  // end of the last expert, and tiles, of earlier groups of 64
+    for (int e0 = 0; e0 < experts; e0 += 64) {
+        int end = e0 + lane < experts ? offs[e0 + lane] : 0;
+        end = end > rows ? rows : (end < carry ? carry : end);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(end, d, 64);
+            if (lane >= d && o > end) end = o;
+        }
+        int start = __shfl_up(end, 1, 64);
+        if (lane == 0) start = carry;
+        int tiles = (end - start + bm - 1) / bm, sum = tiles;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(sum, d, 64);
+            if (lane >= d) sum += o;
+        }
+        const uint64_t past = __ballot(before + sum > mt);
+        if (past) {
+            const int hit = __builtin_ctzll(past);
+            const int row0 = __shfl(start + (mt - before - (sum - tiles)) * bm, hit, 64), last = __shfl(end, hit, 64);
+            return RowTile{__builtin_amdgcn_readfirstlane(row0),
+                           __builtin_amdgcn_readfirstlane(last - row0 < bm ? last - row0 : bm), e0 + hit};
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+        carry = __builtin_amdgcn_readlane(end, 63);
+    }
+    return RowTile{0, 0, 0};
+}
+
 template <class C, Out kOut>
 __global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
     const int8_t* __restrict__ a, Rows rows_of, const int8_t* __restrict__ w1, const float* __restrict__ s1,
@@ -97,7 +138,7 @@ __global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
 
     int64_t mt, nt;
     tile_of(blockIdx.x, n_blocks / n_tiles, n_tiles, C::GM, &mt, &nt);
-    const TileRows tr = find_row_tile(offs, rows, experts, mt, C::BM);
+    const RowTile tr = find_tile(offs, static_cast<int>(rows), static_cast<int>(experts), static_cast<int>(mt), C::BM);
     if (tr.rows == 0) return;
     const int64_t col1 = nt * (kPair ? C::BN : 2 * C::BN), col2 = kPair ? col1 : col1 + C::BN;
     const int n1 = static_cast<int>(n_dim - col1 < C::BN ? n_dim - col1 : C::BN);
@@ -108,7 +149,8 @@ __global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
     const int wm = wave / C::WN, wn = wave % C::WN;
 
     if (tid < C::BM) {
-        const int64_t r = tr.row0 + (tid < tr.rows ? tid : tr.rows - 1), u = rows_of.of(r);
+        const int r = tr.row0 + (tid < tr.rows ? tid : tr.rows - 1);
+        const int64_t u = rows_of.of(r);
         row_scale[tid] = u >= 0 ? rows_of.scale[u] : 0.0f;
         row_prob[tid] = probs ? probs[r] : 1.0f;
     }
@@ -126,8 +168,9 @@ __global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
         const int64_t u = rows_of.of(tr.row0 + (row < tr.rows ? row : tr.rows - 1));
         pa[i] = a + (u >= 0 ? u : 0) * k_dim;
     }
-    const int8_t* t1 = w1 + (tr.expert * n_dim + col1) * k_dim;
-    const int8_t* t2 = w2 + (tr.expert * n_dim + (n2 > 0 ? col2 : col1)) * k_dim;
+    const int64_t wrow = static_cast<int64_t>(tr.expert) * n_dim;
+    const int8_t* t1 = w1 + (wrow + col1) * k_dim;
+    const int8_t* t2 = w2 + (wrow + (n2 > 0 ? col2 : col1)) * k_dim;
     const int m2 = n2 > 0 ? n2 : n1;
 #pragma unroll
     for (int i = 0; i < C::kWLoads; ++i) {
@@ -203,7 +246,6 @@ __global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
 
     // Lane l holds, in register j of tile (mi, ni), row mi * 16 + l % 16 and
     // column ni * 16 + 4 * (l / 16) + j of the wavefront's part.
-    const int64_t wrow = tr.expert * n_dim;
     auto col_scale = [&](const float* s, int64_t col, int n) {
         f32x4 v;
 #pragma unroll
@@ -249,7 +291,7 @@ __global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
             for (int i = 0; i < C::BM * C::BN / 8 / C::kThreads; ++i) {
                 const int s = i * C::kThreads + tid, row = s / (C::BN / 8), c = s % (C::BN / 8) * 8;
                 if (row < tr.rows && c < n)
-                    *reinterpret_cast<u32x4*>(o + (tr.row0 + row) * n_dim + c0 + c) =
+                    *reinterpret_cast<u32x4*>(o + static_cast<int64_t>(tr.row0 + row) * n_dim + c0 + c) =
                         *reinterpret_cast<const u32x4*>(stage + row * C::kLdo + c);
             }
         }
@@ -285,11 +327,143 @@ __global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
             for (int i = 0; i < C::BM * C::BN / 4 / C::kThreads; ++i) {
                 const int s = i * C::kThreads + tid, row = s / (C::BN / 4), c = s % (C::BN / 4) * 4;
                 if (row < tr.rows && c < n)
-                    store_nt16(o + (tr.row0 + row) * n_dim + c0 + c, *reinterpret_cast<const u32x4*>(stage + at(row, c)));
+                    store_nt16(o + static_cast<int64_t>(tr.row0 + row) * n_dim + c0 + c, *reinterpret_cast<const u32x4*>(stage + at(row, c)));
             }
         }
     }
 }
+
+// ---- few rows per expert ---------------------------------------------------------------
+//
+// Bound by reading the weights of the experts that have rows, once. A block
+// takes one row tile of 16 * MT rows and 16 columns of each of two weights
+// (gate and up; two neighbouring column ranges of down); its W wavefronts
+// share the K dimension and meet in LDS at the end (whole numbers: any
+// order). Weights go from memory to registers, with no reuse to stage them
+// for; the rows' bytes come from L2, where they stay. Four wavefronts of 8
+// loads each per block and several blocks per CU keep the memory busy.
+
+constexpr int kUnroll = 4;  // 64-byte steps of K that a wavefront has in flight
+
+template <int MT, int W, Out kOut>
+__global__ __launch_bounds__(64 * W) void grouped_int8_few_kernel(
+    const int8_t* __restrict__ a, Rows rows_of, const int8_t* __restrict__ w1, const float* __restrict__ s1,
+    const int8_t* __restrict__ w2, const float* __restrict__ s2, const int32_t* __restrict__ offs,
+    const float* __restrict__ probs, void* __restrict__ out, int rows, int k_dim, int64_t n_dim, int experts,
+    float limit, int n_tiles) {
+    constexpr bool kPair = kOut == Out::kSwiglu;
+    __shared__ i32x4 part[W][MT][2][64];
+    const int lane = static_cast<int>(threadIdx.x & 63u);
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    const int mt = static_cast<int>(blockIdx.x) / n_tiles, nt = static_cast<int>(blockIdx.x) % n_tiles;
+    const RowTile tr = find_tile(offs, rows, experts, mt, 16 * MT);
+    if (tr.rows == 0) return;
+    const int64_t col1 = static_cast<int64_t>(nt) * (kPair ? 16 : 32), col2 = kPair ? col1 : col1 + 16;
+    const int64_t wrow = static_cast<int64_t>(tr.expert) * n_dim;
+
+    // Lane l holds bytes 16 * (l / 16) .. of a step, of weight row and tile row l % 16.
+    const int at = lane / 16 * 16;
+    const int64_t c1 = col1 + lane % 16 < n_dim ? col1 + lane % 16 : n_dim - 1;
+    const int64_t c2 = col2 + lane % 16 < n_dim ? col2 + lane % 16 : n_dim - 1;
+    const int8_t* p1 = w1 + (wrow + c1) * k_dim;
+    const int8_t* p2 = w2 + (wrow + c2) * k_dim;
+    const int8_t* pa[MT];
+    float sa[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int i = m * 16 + lane % 16;
+        const int64_t u = rows_of.of(tr.row0 + (i < tr.rows ? i : tr.rows - 1));
+        pa[m] = a + (u >= 0 ? u : 0) * k_dim;
+        sa[m] = u >= 0 ? rows_of.scale[u] : 0.0f;
+    }
+    i32x4 acc1[MT], acc2[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc1[m] = acc2[m] = i32x4{0, 0, 0, 0};
+
+    // Wavefronts take turns at pieces of kUnroll steps, so that the block reads
+    // W * kUnroll * 64 consecutive bytes of each weight row at a time.
+    for (int k0 = wave * (kUnroll * 64); k0 < k_dim; k0 += W * kUnroll * 64) {
+        i32x4 f1[kUnroll], f2[kUnroll], fa[kUnroll][MT];
+#pragma unroll
+        for (int s = 0; s < kUnroll; ++s) {
+            const int k = k0 + s * 64 + at;
+            const int ks = k < k_dim ? k : 0;  // past the end: any bytes, times rows of zeros
+            f1[s] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(p1 + ks));
+            f2[s] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(p2 + ks));
+#pragma unroll
+            for (int m = 0; m < MT; ++m) fa[s][m] = *reinterpret_cast<const i32x4*>(pa[m] + ks);
+        }
+#pragma unroll
+        for (int s = 0; s < kUnroll; ++s)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const i32x4 f = k0 + s * 64 + at < k_dim ? fa[s][m] : i32x4{0, 0, 0, 0};
+                acc1[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f1[s], f, acc1[m], 0, 0, 0);
+                acc2[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f2[s], f, acc2[m], 0, 0, 0);
+            }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        part[wave][m][0][lane] = acc1[m];
+        part[wave][m][1][lane] = acc2[m];
+    }
+    __syncthreads();
+    // Lane l of row tile m has row m * 16 + l % 16 and columns 4 * (l / 16) .. + 3.
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        if (m % W != wave) continue;
+        const int i = m * 16 + lane % 16;
+        if (i >= tr.rows) continue;
+        i32x4 q1{0, 0, 0, 0}, q2{0, 0, 0, 0};
+#pragma unroll
+        for (int v = 0; v < W; ++v) {
+            q1 += part[v][m][0][lane];
+            q2 += part[v][m][1][lane];
+        }
+        const int64_t r = tr.row0 + i;
+        const float p = probs ? probs[r] : 1.0f;
+#pragma unroll
+        for (int half = 0; half < (kPair ? 1 : 2); ++half) {
+            const int64_t c = (half == 0 ? col1 : col2) + 4 * (lane / 16);
+            if (c >= n_dim) continue;  // n_dim is a multiple of 8: four columns are in or out
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float t1 = s1[wrow + c + j];
+                if constexpr (kPair) {
+                    const float g = static_cast<float>(q1[j]) * sa[m] * t1;
+                    const float u = static_cast<float>(q2[j]) * sa[m] * s2[wrow + c + j];
+                    v[j] = fwd_elem(g, u, p, limit);
+                } else {
+                    v[j] = static_cast<float>(half == 0 ? q1[j] : q2[j]) * sa[m] * t1 * p;
+                }
+            }
+            if constexpr (kOut == Out::kF32)
+                *reinterpret_cast<f32x4*>(static_cast<float*>(out) + r * n_dim + c) = f32x4{v[0], v[1], v[2], v[3]};
+            else
+                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + r * n_dim + c) =
+                    u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        }
+    }
+}
+
+template <int MT, Out kOut>
+int launch_few(const int8_t* a, const Rows& rows_of, const int8_t* w1, const float* s1, const int8_t* w2,
+               const float* s2, const int32_t* offs, const float* probs, void* out, int64_t rows, int64_t k_dim,
+               int64_t n_dim, int64_t experts, float limit, hipStream_t st) {
+    constexpr int W = 4;
+    // row tiles: no more than rows, and one partial one per expert
+    const int64_t most = (rows + 16 * MT - 1) / (16 * MT) + experts, m_tiles = most < rows ? most : rows;
+    const int64_t cols = kOut == Out::kSwiglu ? 16 : 32, n_tiles = (n_dim + cols - 1) / cols;
+    if (m_tiles * n_tiles >= (int64_t{1} << 31)) return MOE_EPI_ERR_BAD_SHAPE;
+    (void)hipGetLastError();
+    hipLaunchKernelGGL((grouped_int8_few_kernel<MT, W, kOut>), dim3(static_cast<unsigned>(m_tiles * n_tiles)),
+                       dim3(64 * W), 0, st, a, rows_of, w1, s1, w2, s2, offs, probs, out, static_cast<int>(rows),
+                       static_cast<int>(k_dim), n_dim, static_cast<int>(experts), limit, static_cast<int>(n_tiles));
+    return launch_status();
+}
+
+// ---- launches ------------------------------------------------------------------------
 
 typedef Tile<256, 128, 4, 2, 2> GateUpTile;
 typedef Tile<256, 128, 4, 2, 32> DownTile;
@@ -298,6 +472,10 @@ template <class C, Out kOut>
 int launch_int8(const int8_t* a, const Rows& rows_of, const int8_t* w1, const float* s1, const int8_t* w2,
                 const float* s2, const int32_t* offs, const float* probs, void* out, int64_t rows, int64_t k_dim,
                 int64_t n_dim, int64_t experts, float limit, hipStream_t st) {
+    if (rows <= 16 * experts)
+        return launch_few<1, kOut>(a, rows_of, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim, experts, limit, st);
+    if (rows <= 64 * experts)
+        return launch_few<4, kOut>(a, rows_of, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim, experts, limit, st);
     int64_t n_tiles, n_blocks;
     const int64_t grid =
         grouped_grid(rows, n_dim, kOut == Out::kSwiglu ? C::BN : 2 * C::BN, experts, C::BM, &n_tiles, &n_blocks);
@@ -311,7 +489,7 @@ int launch_int8(const int8_t* a, const Rows& rows_of, const int8_t* w1, const fl
 
 bool shape_ok(int64_t rows, int64_t k_dim, int64_t n_dim, int64_t experts) {
     return rows >= 0 && rows <= INT32_MAX && k_dim > 0 && k_dim < kMaxK && k_dim % 16 == 0 && n_dim > 0 &&
-           n_dim % 8 == 0 && experts > 0 && experts <= INT64_MAX / 4 / n_dim;
+           n_dim % 8 == 0 && experts > 0 && experts <= INT32_MAX && n_dim <= INT64_MAX / 4 / experts;
 }
 
 }  // namespace

@@ -83,6 +83,23 @@ __device__ __forceinline__ void stage_barrier() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// Inclusive scan of one value per lane over the wavefront, by lane shifts:
+// within rows of 16 lanes by 1, 2, 4 and 8, then lane 15 of a row into the
+// next row and lane 31 into the upper half. Lanes that receive nothing get `none`.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int dpp(int none, int v) {
+    return __builtin_amdgcn_update_dpp(none, v, kCtrl, kRows, 0xF, false);
+}
+template <class F>
+__device__ __forceinline__ int scan(int v, int none, F&& op) {
+    v = op(v, dpp<0x111, 0xF>(none, v));  // row_shr 1, 2, 4, 8
+    v = op(v, dpp<0x112, 0xF>(none, v));
+    v = op(v, dpp<0x114, 0xF>(none, v));
+    v = op(v, dpp<0x118, 0xF>(none, v));
+    v = op(v, dpp<0x142, 0xA>(none, v));  // row_bcast 15, 31
+    return op(v, dpp<0x143, 0xC>(none, v));
+}
+
 // The mt-th row tile of bm rows over all experts in order (rows == 0: there is
 // none). The whole wavefront takes 64 experts at a time: with the running
 // maximum of offs as the clamped end of each expert and the running sum of
@@ -98,25 +115,16 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offs, i
     for (int e0 = 0; e0 < experts; e0 += 64) {
         int end = e0 + lane < experts ? offs[e0 + lane] : 0;
         end = end > rows ? rows : (end < carry ? carry : end);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(end, d, 64);
-            if (lane >= d && o > end) end = o;
-        }
-        int start = __shfl_up(end, 1, 64);
-        if (lane == 0) start = carry;
-        int tiles = (end - start + bm - 1) / bm, sum = tiles;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(sum, d, 64);
-            if (lane >= d) sum += o;
-        }
+        end = scan(end, 0, [](int x, int y) { return x > y ? x : y; });
+        const int start = dpp<0x138, 0xF>(carry, end);  // wave_shr 1: the expert before
+        const int n = end - start, tiles = n > 0 ? (n - 1) / bm + 1 : 0;
+        const int sum = scan(tiles, 0, [](int x, int y) { return x + y; });
         const uint64_t past = __ballot(before + sum > mt);
         if (past) {
             const int hit = __builtin_ctzll(past);
-            const int row0 = __shfl(start + (mt - before - (sum - tiles)) * bm, hit, 64), last = __shfl(end, hit, 64);
-            return RowTile{__builtin_amdgcn_readfirstlane(row0),
-                           __builtin_amdgcn_readfirstlane(last - row0 < bm ? last - row0 : bm), e0 + hit};
+            const int row0 = __builtin_amdgcn_readlane(start + (mt - before - (sum - tiles)) * bm, hit);
+            const int left = __builtin_amdgcn_readlane(end, hit) - row0;
+            return RowTile{row0, left < bm ? left : bm, e0 + hit};
         }
         before += __builtin_amdgcn_readlane(sum, 63);
         carry = __builtin_amdgcn_readlane(end, 63);
@@ -336,37 +344,53 @@ __global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
 // ---- few rows per expert ---------------------------------------------------------------
 //
 // Bound by reading the weights of the experts that have rows, once. A block
-// takes one row tile of 16 * MT rows and 16 columns of each of two weights
-// (gate and up; two neighbouring column ranges of down); its W wavefronts
-// share the K dimension and meet in LDS at the end (whole numbers: any
-// order). Weights go from memory to registers, with no reuse to stage them
-// for; the rows' bytes come from L2, where they stay. Four wavefronts of 8
-// loads each per block and several blocks per CU keep the memory busy.
+// takes one row tile of 16 * MT rows and 16 * NT columns of each of two
+// weights (gate and up; two neighbouring column ranges of down); its W
+// wavefronts share K in pieces of 256 and meet in LDS at the end (whole
+// numbers: any order).
+//
+// A load instruction takes 256 consecutive bytes of each of 4 weight rows,
+// and the wavefront passes them through its own part of LDS into the order
+// the matrix instruction wants. Loaded straight into that order, 64 bytes of
+// each of 16 rows, the same kernel ran at 4.1-4.6 TB/s of weights instead of
+// 6.4 (gate_up of 32 rows, 8 experts of 7168 -> 2 x 2048: 57.5 and 51.6 us
+// without and with the weights kept in the caches, against 36.6). The next
+// piece is on its way while the present one is multiplied; weights are read
+// once (nontemporal: 42.0 us without), the rows' bytes stay in L2.
 
-constexpr int kUnroll = 4;  // 64-byte steps of K that a wavefront has in flight
+constexpr int kPiece = 256;                 // bytes of K of a weight row that a wavefront takes at a time
+constexpr int kPieceChunks = kPiece / 16;   // 16: a load instruction covers 4 rows of 256 bytes
 
-template <int MT, int W, Out kOut>
+template <int MT, int NT, int W, Out kOut>
 __global__ __launch_bounds__(64 * W) void grouped_int8_few_kernel(
     const int8_t* __restrict__ a, Rows rows_of, const int8_t* __restrict__ w1, const float* __restrict__ s1,
     const int8_t* __restrict__ w2, const float* __restrict__ s2, const int32_t* __restrict__ offs,
     const float* __restrict__ probs, void* __restrict__ out, int rows, int k_dim, int64_t n_dim, int experts,
     float limit, int n_tiles) {
     constexpr bool kPair = kOut == Out::kSwiglu;
-    __shared__ i32x4 part[W][MT][2][64];
+    constexpr int T = 2 * NT;  // weight tiles of 16 rows: the first NT of w1, the others of w2
+    constexpr int kStageVecs = T * 16 * kPieceChunks, kPartVecs = MT * T * 64;
+    __shared__ i32x4 lds[W * (kStageVecs > kPartVecs ? kStageVecs : kPartVecs)];
     const int lane = static_cast<int>(threadIdx.x & 63u);
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
     const int mt = static_cast<int>(blockIdx.x) / n_tiles, nt = static_cast<int>(blockIdx.x) % n_tiles;
     const RowTile tr = find_tile(offs, rows, experts, mt, 16 * MT);
     if (tr.rows == 0) return;
-    const int64_t col1 = static_cast<int64_t>(nt) * (kPair ? 16 : 32), col2 = kPair ? col1 : col1 + 16;
+    const int64_t col1 = static_cast<int64_t>(nt) * (kPair ? 16 : 32) * NT, col2 = kPair ? col1 : col1 + 16 * NT;
     const int64_t wrow = static_cast<int64_t>(tr.expert) * n_dim;
 
-    // Lane l holds bytes 16 * (l / 16) .. of a step, of weight row and tile row l % 16.
+    // loads: lane l takes chunk l % 16 of rows l / 16 + 4 i
+    const int lc = lane % 16 * 16, lr = lane / 16;
+    const int8_t* pw[T][4];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            int64_t c = (t < NT ? col1 + t * 16 : col2 + (t - NT) * 16) + lr + 4 * i;
+            c = c < n_dim ? c : n_dim - 1;
+            pw[t][i] = (t < NT ? w1 : w2) + (wrow + c) * k_dim;
+        }
     const int at = lane / 16 * 16;
-    const int64_t c1 = col1 + lane % 16 < n_dim ? col1 + lane % 16 : n_dim - 1;
-    const int64_t c2 = col2 + lane % 16 < n_dim ? col2 + lane % 16 : n_dim - 1;
-    const int8_t* p1 = w1 + (wrow + c1) * k_dim;
-    const int8_t* p2 = w2 + (wrow + c2) * k_dim;
     const int8_t* pa[MT];
     float sa[MT];
 #pragma unroll
@@ -376,55 +400,83 @@ __global__ __launch_bounds__(64 * W) void grouped_int8_few_kernel(
         pa[m] = a + (u >= 0 ? u : 0) * k_dim;
         sa[m] = u >= 0 ? rows_of.scale[u] : 0.0f;
     }
-    i32x4 acc1[MT], acc2[MT];
+    i32x4 acc[MT][T];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) acc1[m] = acc2[m] = i32x4{0, 0, 0, 0};
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < T; ++t) acc[m][t] = i32x4{0, 0, 0, 0};
 
-    // Wavefronts take turns at pieces of kUnroll steps, so that the block reads
-    // W * kUnroll * 64 consecutive bytes of each weight row at a time.
-    for (int k0 = wave * (kUnroll * 64); k0 < k_dim; k0 += W * kUnroll * 64) {
-        i32x4 f1[kUnroll], f2[kUnroll], fa[kUnroll][MT];
+    // The wavefront's own part of LDS: row r's chunk c at 16 r + (c ^ r), so that the 16
+    // rows of a fragment read take 16 different bank groups. No other wavefront touches
+    // it, and a wavefront's LDS accesses stay in order, so no barrier is needed.
+    i32x4* const mine = lds + wave * (kStageVecs > kPartVecs ? kStageVecs : kPartVecs);
+    i32x4 rw[T][4], ra[MT][4];  // the next piece, on its way
+    // Past the end of K any bytes will do: the rows' are replaced by zeros below.
+    auto fetch = [&](int k0) {
+        const int k = k0 + lc < k_dim ? k0 + lc : 0;
 #pragma unroll
-        for (int s = 0; s < kUnroll; ++s) {
-            const int k = k0 + s * 64 + at;
-            const int ks = k < k_dim ? k : 0;  // past the end: any bytes, times rows of zeros
-            f1[s] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(p1 + ks));
-            f2[s] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(p2 + ks));
+        for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) fa[s][m] = *reinterpret_cast<const i32x4*>(pa[m] + ks);
+            for (int i = 0; i < 4; ++i) rw[t][i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pw[t][i] + k));
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int ka = k0 + s * 64 + at < k_dim ? k0 + s * 64 + at : 0;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) ra[m][s] = *reinterpret_cast<const i32x4*>(pa[m] + ka);
         }
+    };
+    int k0 = wave * kPiece;
+    if (k0 < k_dim) fetch(k0);
+    for (; k0 < k_dim; k0 += W * kPiece) {
 #pragma unroll
-        for (int s = 0; s < kUnroll; ++s)
+        for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const i32x4 f = k0 + s * 64 + at < k_dim ? fa[s][m] : i32x4{0, 0, 0, 0};
-                acc1[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f1[s], f, acc1[m], 0, 0, 0);
-                acc2[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f2[s], f, acc2[m], 0, 0, 0);
+            for (int i = 0; i < 4; ++i) {
+                const int row = lr + 4 * i;
+                mine[(t * 16 + row) * 16 + ((lane % 16) ^ row)] = rw[t][i];
             }
-    }
+        i32x4 fa[MT][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        part[wave][m][0][lane] = acc1[m];
-        part[wave][m][1][lane] = acc2[m];
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) fa[m][s] = k0 + s * 64 + at < k_dim ? ra[m][s] : i32x4{0, 0, 0, 0};
+        if (k0 + W * kPiece < k_dim) fetch(k0 + W * kPiece);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const i32x4 f = mine[(t * 16 + lane % 16) * 16 + ((4 * s + lane / 16) ^ (lane % 16))];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    acc[m][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f, fa[m][s], acc[m][t], 0, 0, 0);
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
+    if constexpr (W > 1) __syncthreads();  // the parts of the sum take the place of the pieces
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < T; ++t) lds[((wave * MT + m) * T + t) * 64 + lane] = acc[m][t];
     __syncthreads();
-    // Lane l of row tile m has row m * 16 + l % 16 and columns 4 * (l / 16) .. + 3.
+    // Lane l of row tile m has row m * 16 + l % 16 and columns 4 * (l / 16) .. + 3 of each weight tile.
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        if (m % W != wave) continue;
+    for (int mn = 0; mn < MT * NT; ++mn) {
+        const int m = mn / NT, n = mn % NT;
+        if (mn % W != wave) continue;
         const int i = m * 16 + lane % 16;
         if (i >= tr.rows) continue;
         i32x4 q1{0, 0, 0, 0}, q2{0, 0, 0, 0};
 #pragma unroll
         for (int v = 0; v < W; ++v) {
-            q1 += part[v][m][0][lane];
-            q2 += part[v][m][1][lane];
+            q1 += lds[((v * MT + m) * T + n) * 64 + lane];
+            q2 += lds[((v * MT + m) * T + NT + n) * 64 + lane];
         }
         const int64_t r = tr.row0 + i;
         const float p = probs ? probs[r] : 1.0f;
 #pragma unroll
         for (int half = 0; half < (kPair ? 1 : 2); ++half) {
-            const int64_t c = (half == 0 ? col1 : col2) + 4 * (lane / 16);
+            const int64_t c = (half == 0 ? col1 : col2) + n * 16 + 4 * (lane / 16);
             if (c >= n_dim) continue;  // n_dim is a multiple of 8: four columns are in or out
             float v[4];
 #pragma unroll
@@ -447,20 +499,38 @@ __global__ __launch_bounds__(64 * W) void grouped_int8_few_kernel(
     }
 }
 
+template <int MT, int W, Out kOut>
+void launch_few_waves(unsigned grid, const int8_t* a, const Rows& rows_of, const int8_t* w1, const float* s1,
+                      const int8_t* w2, const float* s2, const int32_t* offs, const float* probs, void* out,
+                      int64_t rows, int64_t k_dim, int64_t n_dim, int64_t experts, float limit, int64_t n_tiles,
+                      hipStream_t st) {
+    hipLaunchKernelGGL((grouped_int8_few_kernel<MT, 1, W, kOut>), dim3(grid), dim3(64 * W), 0, st, a, rows_of, w1, s1,
+                       w2, s2, offs, probs, out, static_cast<int>(rows), static_cast<int>(k_dim), n_dim,
+                       static_cast<int>(experts), limit, static_cast<int>(n_tiles));
+}
+
 template <int MT, Out kOut>
 int launch_few(const int8_t* a, const Rows& rows_of, const int8_t* w1, const float* s1, const int8_t* w2,
                const float* s2, const int32_t* offs, const float* probs, void* out, int64_t rows, int64_t k_dim,
                int64_t n_dim, int64_t experts, float limit, hipStream_t st) {
-    constexpr int W = 4;
     // row tiles: no more than rows, and one partial one per expert
     const int64_t most = (rows + 16 * MT - 1) / (16 * MT) + experts, m_tiles = most < rows ? most : rows;
     const int64_t cols = kOut == Out::kSwiglu ? 16 : 32, n_tiles = (n_dim + cols - 1) / cols;
-    if (m_tiles * n_tiles >= (int64_t{1} << 31)) return MOE_EPI_ERR_BAD_SHAPE;
-    (void)hipGetLastError();
-    hipLaunchKernelGGL((grouped_int8_few_kernel<MT, W, kOut>), dim3(static_cast<unsigned>(m_tiles * n_tiles)),
-                       dim3(64 * W), 0, st, a, rows_of, w1, s1, w2, s2, offs, probs, out, static_cast<int>(rows),
-                       static_cast<int>(k_dim), n_dim, static_cast<int>(experts), limit, static_cast<int>(n_tiles));
-    return launch_status();
+    const int64_t blocks = m_tiles * n_tiles;
+    if (blocks >= (int64_t{1} << 31)) return MOE_EPI_ERR_BAD_SHAPE;
+    // Wavefronts that share K: as many as keep the grid near 4096 wavefronts, 16
+    // per CU. One GPU, us with 1 / 2 / 4: 32 rows 2048 -> 7168 on 8 experts (1792
+    // blocks) 19.7 / 19.6 / 21.0; 8 rows 2048 -> 2 x 768 on 64 (384 blocks)
+    // 9.8 / 8.3 / 7.4.
+    auto go = [&](auto launch) {
+        (void)hipGetLastError();
+        launch(static_cast<unsigned>(blocks), a, rows_of, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim,
+               experts, limit, n_tiles, st);
+        return launch_status();
+    };
+    if (blocks <= 1024) return go(launch_few_waves<MT, 4, kOut>);
+    if (blocks <= 2048) return go(launch_few_waves<MT, 2, kOut>);
+    return go(launch_few_waves<MT, 1, kOut>);
 }
 
 // ---- launches ------------------------------------------------------------------------
@@ -472,10 +542,10 @@ template <class C, Out kOut>
 int launch_int8(const int8_t* a, const Rows& rows_of, const int8_t* w1, const float* s1, const int8_t* w2,
                 const float* s2, const int32_t* offs, const float* probs, void* out, int64_t rows, int64_t k_dim,
                 int64_t n_dim, int64_t experts, float limit, hipStream_t st) {
-    if (rows <= 16 * experts)
+    if (rows <= 8 * experts)
         return launch_few<1, kOut>(a, rows_of, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim, experts, limit, st);
-    if (rows <= 64 * experts)
-        return launch_few<4, kOut>(a, rows_of, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim, experts, limit, st);
+    if (rows <= 24 * experts)
+        return launch_few<2, kOut>(a, rows_of, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim, experts, limit, st);
     int64_t n_tiles, n_blocks;
     const int64_t grid =
         grouped_grid(rows, n_dim, kOut == Out::kSwiglu ? C::BN : 2 * C::BN, experts, C::BM, &n_tiles, &n_blocks);

@@ -322,7 +322,8 @@ def scales(rng, shape, size):
 # rows per expert, K, N: single rows, tiles of one row more or less, empty experts, short and odd K and N
 PRODUCTS = [([1], 16, 8), ([1], 128, 128), ([1, 0, 3], 48, 24), ([0, 16, 17, 0], 112, 136), ([5, 40, 2], 144, 264),
             ([64, 65, 1, 63], 256, 128), ([255, 256, 257], 272, 72), ([700], 128, 520), ([3, 130, 0, 200], 1040, 200),
-            ([2] * 33, 400, 40), ([0, 0, 0], 64, 16), ([129, 31, 33, 500], 2064, 48)]
+            ([2] * 33, 400, 40), ([0, 0, 0], 64, 16), ([129, 31, 33, 500], 2064, 48), ([0] * 30 + [100] + [3] * 70, 528, 56),
+            ([1, 90, 0, 2, 7], 7184, 40)]
 
 
 @pytest.mark.parametrize("counts,k,n", PRODUCTS)

@@ -11,14 +11,31 @@
 // The integer sums carry no rounding, so their order is free: tiles, steps
 // and wavefronts may be arranged at will without changing a bit.
 //
-// Tile kernel: a block covers 256 rows of one expert and 128 columns of each
-// of two weight tiles (gate and up of the same columns; two neighbouring
-// column ranges of the down weights), eight wavefronts of 64 x 64 x 2, 128
-// accumulators per lane. Steps of 128 along K: a row of a tile is then 128
-// bytes, eight 16-byte chunks, XOR-swizzled so that a fragment read (one
-// chunk of each of 16 rows) takes 16 different bank groups. Global memory
-// goes straight to LDS in two stages; the next stage's loads are in flight
-// while this one's products run.
+// Three kernels, by the mean number of rows of an expert (launch_int8):
+//   few rows    the weights are read once and set the time (below);
+//   tiles       a block covers BM rows of one expert and BN columns of each of
+//               two weight tiles (gate and up of the same columns; two
+//               neighbouring column ranges of the down weights). Steps of 128
+//               along K: a row of a tile is then 128 bytes, eight 16-byte
+//               chunks, XOR-swizzled so that a fragment read (one chunk of each
+//               of 16 rows) takes 16 different bank groups. Memory goes
+//               straight to LDS in two stages; the next stage's loads are in
+//               flight while this one's products run. 64 x 64 and 128 x 64
+//               tiles share a CU and fill each other's waits;
+//   large tiles 256 x 128 x 2, eight wavefronts of 64 x 64 x 2, 128
+//               accumulators a lane, one block per CU, with the loop written
+//               out so that fragment reads and loads go between the matrix
+//               instructions in a fixed order. A step of it reads 192 KiB from
+//               LDS and writes 64 KiB, 2048 cycles at 128 bytes a cycle, beside
+//               2048 cycles of matrix instructions: the two bound it together.
+//               65536 rows over 8 experts: gate_up (7168 -> 2 x 2048) 1609 us,
+//               2392 TOP/s (the plain loop 1695 us), down (2048 -> 7168, bf16
+//               out) 972 us, 1980 TOP/s, its shorter K giving the output's
+//               stores a larger share; a library product of 16384^3 in int8
+//               runs at 2341 TOP/s on this part. Eight loading wavefronts
+//               against four: gate_up 1609 / 1641 us, down 1002 / 983; row
+//               tiles per group: gate_up 1: 1691, 2: 1641, 4: 1648, 8: 1689;
+//               down 8: 977, 16: 972, 32: 983, 128: 1002.
 #include "epi_common.h"
 #include "grouped_map.h"
 #include "moe_routed.h"
@@ -50,19 +67,29 @@ struct Rows {
 
 enum class Out { kSwiglu, kBf16, kF32 };
 
-template <int BM_, int BN_, int WM_, int WN_, int GM_>
+// BM rows and BN columns of each weight by WM x WN wavefronts; GM row tiles to
+// a group of the tile order; kLoadWaves wavefronts load; kRoll: the main loop
+// that keeps one block per CU busy (below), otherwise the plain one.
+template <int BM_, int BN_, int WM_, int WN_, int GM_, int LW_, bool kRoll_>
 struct Tile {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, GM = GM_;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, GM = GM_, kLoadWaves = LW_;
+    static constexpr bool kRoll = kRoll_;
     static constexpr int kThreads = 64 * WM * WN;
     static constexpr int MI = BM / (16 * WM), NI = BN / (16 * WN);
     static constexpr int kABytes = BM * kStep, kWBytes = BN * kStep, kStage = kABytes + 2 * kWBytes;
-    static constexpr int kALoads = BM * kChunks / kThreads, kWLoads = BN * kChunks / kThreads;
+    static constexpr int kLoadThreads = 64 * kLoadWaves;
+    static constexpr int kALoads = BM * kChunks / kLoadThreads, kWLoads = BN * kChunks / kLoadThreads;
+    static constexpr int kLoads = kALoads + 2 * kWLoads;  // of a step, per loading wavefront
+    static constexpr int kMfmas = 2 * MI * NI;            // of a sub-step of 64
+    static constexpr int kEvery = kMfmas / kLoads;        // matrix instructions per load
     static constexpr int kLds = 2 * kStage;
     static constexpr int kLdo = BN + 8;  // elements per row of a staged bf16 tile
     static_assert(BM * kLdo * 2 <= kLds && BM * BN * 4 <= kLds, "a staged output tile fits");
-    static_assert(kALoads >= 1 && kWLoads >= 1 && BM * kChunks % kThreads == 0 && BN * kChunks % kThreads == 0,
+    static_assert(kALoads >= 1 && kWLoads >= 1 && BM * kChunks % kLoadThreads == 0 && BN * kChunks % kLoadThreads == 0,
                   "whole chunks per lane");
+    static_assert(kEvery >= 1, "a load per matrix instruction at most");
     static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && BM <= kThreads, "whole MFMA tiles");
+    static_assert(WM * WN >= kLoadWaves && BM * BN % (8 * kThreads) == 0, "loading wavefronts; whole output chunks");
 };
 
 __device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
@@ -132,21 +159,20 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offs, i
     return RowTile{0, 0, 0};
 }
 
-template <class C, Out kOut>
-__global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
-    const int8_t* __restrict__ a, Rows rows_of, const int8_t* __restrict__ w1, const float* __restrict__ s1,
-    const int8_t* __restrict__ w2, const float* __restrict__ s2, const int32_t* __restrict__ offs,
-    const float* __restrict__ probs, void* __restrict__ out, int64_t rows, int64_t k_dim, int64_t n_dim,
-    int64_t experts, float limit, int64_t n_tiles, int64_t n_blocks) {
+template <class C, Out kOut, bool kWide>
+__device__ __forceinline__ void grouped_int8_tile(
+    uint8_t* lds, const int8_t* __restrict__ a, const Rows& rows_of, const int8_t* __restrict__ w1,
+    const float* __restrict__ s1, const int8_t* __restrict__ w2, const float* __restrict__ s2,
+    const int32_t* __restrict__ offs, const float* __restrict__ probs, void* __restrict__ out, int rows, int k_dim,
+    int64_t n_dim, int experts, float limit, int64_t n_tiles, int64_t n_blocks) {
     constexpr bool kPair = kOut == Out::kSwiglu;  // two weights of the same columns
     constexpr int MI = C::MI, NI = C::NI;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds + C::BM * 8];
     float* const row_scale = reinterpret_cast<float*>(lds + C::kLds);
     float* const row_prob = row_scale + C::BM;
 
     int64_t mt, nt;
     tile_of(blockIdx.x, n_blocks / n_tiles, n_tiles, C::GM, &mt, &nt);
-    const RowTile tr = find_tile(offs, static_cast<int>(rows), static_cast<int>(experts), static_cast<int>(mt), C::BM);
+    const RowTile tr = find_tile(offs, rows, experts, static_cast<int>(mt), C::BM);
     if (tr.rows == 0) return;
     const int64_t col1 = nt * (kPair ? C::BN : 2 * C::BN), col2 = kPair ? col1 : col1 + C::BN;
     const int n1 = static_cast<int>(n_dim - col1 < C::BN ? n_dim - col1 : C::BN);
@@ -155,6 +181,7 @@ __global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
     const int tid = static_cast<int>(threadIdx.x), lane = tid % 64;
     const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int wm = wave / C::WN, wn = wave % C::WN;
+    const bool loads = wave < C::kLoadWaves;
 
     if (tid < C::BM) {
         const int r = tr.row0 + (tid < tr.rows ? tid : tr.rows - 1);
@@ -163,30 +190,94 @@ __global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
         row_prob[tid] = probs ? probs[r] : 1.0f;
     }
 
-    // This lane's chunks of a stage: slot row * 8 + (chunk ^ swizzle(row)) holds
-    // chunk `chunk` of tile row `row`. Rows past the tile repeat its last one.
-    const int8_t* pa[C::kALoads];
-    const int8_t* pw1[C::kWLoads];
-    const int8_t* pw2[C::kWLoads];
-    int kq[C::kALoads > C::kWLoads ? C::kALoads : C::kWLoads];
-#pragma unroll
-    for (int i = 0; i < C::kALoads; ++i) {
-        const int s = i * C::kThreads + tid, row = s / kChunks;
-        kq[i] = ((s % kChunks) ^ swizzle(row)) * 16;
-        const int64_t u = rows_of.of(tr.row0 + (row < tr.rows ? row : tr.rows - 1));
-        pa[i] = a + (u >= 0 ? u : 0) * k_dim;
-    }
+    // This lane's 16-byte chunks of a stage: slot row * 8 + (chunk ^ swizzle(row))
+    // holds chunk `chunk` of tile row `row`. The rows of a lane's loads are a
+    // multiple of 16 apart, so all of them take the same chunk of their row. Rows
+    // past the tile repeat its last one. Loads go by a base in scalar registers,
+    // the lane's 32-bit offset from it, and the step's offset in a scalar; only
+    // the rows of a tensor of 2 GiB and more, read in place, need 64-bit addresses.
+    constexpr int kFlags = 0x00020000;  // raw buffer, 32-bit data format
     const int64_t wrow = static_cast<int64_t>(tr.expert) * n_dim;
-    const int8_t* t1 = w1 + (wrow + col1) * k_dim;
-    const int8_t* t2 = w2 + (wrow + (n2 > 0 ? col2 : col1)) * k_dim;
-    const int m2 = n2 > 0 ? n2 : n1;
+    const int lrow = (wave % C::kLoadWaves * 64 + lane) / kChunks;
+    const int kq = ((lane % kChunks) ^ swizzle(lrow)) * 16;
+    const int8_t* const abase = rows_of.slot_of ? a : a + static_cast<int64_t>(tr.row0) * k_dim;
+    const int8_t* const t1 = w1 + (wrow + col1) * k_dim;
+    const int8_t* const t2 = w2 + (wrow + (n2 > 0 ? col2 : col1)) * k_dim;
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(abase), 0, 0x7FFFFFFF, kFlags),
+                                 r1 = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(t1), 0, 0x7FFFFFFF, kFlags),
+                                 r2 = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(t2), 0, 0x7FFFFFFF, kFlags);
+    int va[C::kALoads], v1[C::kWLoads], v2[C::kWLoads];
+    const int8_t* pa[kWide ? C::kALoads : 1];
+    if (loads) {
 #pragma unroll
-    for (int i = 0; i < C::kWLoads; ++i) {
-        const int s = i * C::kThreads + tid, row = s / kChunks;
-        kq[i] = ((s % kChunks) ^ swizzle(row)) * 16;
-        pw1[i] = t1 + static_cast<int64_t>(row < n1 ? row : n1 - 1) * k_dim;
-        pw2[i] = t2 + static_cast<int64_t>(row < m2 ? row : m2 - 1) * k_dim;
+        for (int i = 0; i < C::kALoads; ++i) {
+            const int row = i * (C::kLoadThreads / kChunks) + lrow, r = row < tr.rows ? row : tr.rows - 1;
+            int64_t u = r;
+            if (rows_of.slot_of) {
+                u = rows_of.of(tr.row0 + r);
+                u = u >= 0 ? u : 0;
+            }
+            if constexpr (kWide)
+                pa[i] = abase + u * k_dim + kq;
+            else
+                va[i] = static_cast<int>(u * k_dim) + kq;
+        }
+        const int m2 = n2 > 0 ? n2 : n1;
+#pragma unroll
+        for (int i = 0; i < C::kWLoads; ++i) {
+            const int row = i * (C::kLoadThreads / kChunks) + lrow;
+            v1[i] = (row < n1 ? row : n1 - 1) * k_dim + kq;
+            v2[i] = (row < m2 ? row : m2 - 1) * k_dim + kq;
+        }
     }
+    // Load number i of step kt: the rows' chunks first, then the weights' in
+    // pairs. A step that crosses the end of K takes the start of the row for
+    // the chunks past it.
+    const int nk = (k_dim + kStep - 1) / kStep, last = k_dim % kStep ? nk - 1 : nk;  // the step that crosses, if one does
+    auto issue_one = [&](int kt, int i) {
+        uint8_t* st = lds + (kt & 1) * C::kStage;
+        int k = kt * kStep, more = 0;
+        if (kt == last) {
+            more = k + kq < k_dim ? k : -kq;
+            k = 0;
+        }
+        auto bl = [&](__amdgpu_buffer_rsrc_t r, int v, uint8_t* dst) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, v + more, k, 0, 0);
+        };
+        if (i < C::kALoads) {
+            uint8_t* dst = st + (i * C::kLoadThreads + wave * 64) * 16;
+            if constexpr (kWide)
+                __builtin_amdgcn_global_load_lds(pa[i] + k + more, (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+            else
+                bl(ra, va[i], dst);
+        } else {
+            const int j = (i - C::kALoads) / 2;
+            uint8_t* dst = st + C::kABytes + (j * C::kLoadThreads + wave * 64) * 16;
+            if ((i - C::kALoads) % 2 == 0)
+                bl(r1, v1[j], dst);
+            else
+                bl(r2, v2[j], dst + C::kWBytes);
+        }
+    };
+    auto issue = [&](int kt) {
+        if (loads)
+#pragma unroll
+            for (int i = 0; i < C::kLoads; ++i) issue_one(kt, i);
+    };
+    // Step kt has landed and nobody reads the other stage any more. In the step
+    // that crosses the end of K the rows' chunks past it are cleared, so that
+    // whatever the weights hold there counts 0.
+    auto meet = [&](int kt) {
+        stage_barrier();
+        if (kt == last) {
+            if (loads && kt * kStep + kq >= k_dim)
+#pragma unroll
+                for (int i = 0; i < C::kALoads; ++i)
+                    *reinterpret_cast<i32x4*>(lds + (kt & 1) * C::kStage + (i * C::kLoadThreads + tid) * 16) = i32x4{0, 0, 0, 0};
+            lds_barrier();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
 
     i32x4 acc1[MI][NI], acc2[MI][NI];
 #pragma unroll
@@ -194,60 +285,87 @@ __global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
 #pragma unroll
         for (int ni = 0; ni < NI; ++ni) acc1[mi][ni] = acc2[mi][ni] = i32x4{0, 0, 0, 0};
 
-    auto load = [&](const int8_t* src, uint8_t* dst) {
-        __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+    // Fragments of one sub-step of 64: 16 rows, a 16-byte chunk of each per group
+    // of 16 lanes. Which group takes which chunk is free as long as rows and
+    // weights agree; lanes l and l + 32 on neighbouring chunks keep the LDS less
+    // busy than lanes l and l + 16. Each fragment is read again for the next
+    // sub-step right after the last matrix instruction that uses it.
+    i32x4 fa[MI], f1[NI], f2[NI];
+    const int chunk0 = ((lane / 16) & 1) * 2 + lane / 32;
+    auto fragment = [&](const uint8_t* tile, int row, int kk) {
+        return *reinterpret_cast<const i32x4*>(tile + (row * kChunks + ((4 * kk + chunk0) ^ swizzle(row))) * 16);
     };
-    // Chunks past the end of K load the start of their row instead; the rows
-    // of a are then cleared there, so that whatever the weights hold counts 0.
-    auto issue = [&](int64_t kt) {
-        uint8_t* st = lds + (kt & 1) * C::kStage;
-        const int64_t k0 = kt * kStep;
+    auto read_a = [&](const uint8_t* st, int kk, int mi) {
+        fa[mi] = fragment(st, wm * (C::BM / C::WM) + mi * 16 + lane % 16, kk);
+    };
+    auto read_w = [&](const uint8_t* st, int kk, int ni) {
+        const int row = wn * (C::BN / C::WN) + ni * 16 + lane % 16;
+        f1[ni] = fragment(st + C::kABytes, row, kk);
+        f2[ni] = fragment(st + C::kABytes + C::kWBytes, row, kk);
+    };
+    auto mfma = [&](int i) {
+        const int ni = i / (2 * MI), mi = i / 2 % MI;
+        if (i % 2 == 0)
+            acc1[mi][ni] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f1[ni], fa[mi], acc1[mi][ni], 0, 0, 0);
+        else
+            acc2[mi][ni] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f2[ni], fa[mi], acc2[mi][ni], 0, 0, 0);
+    };
+    auto reads_after = [&](int i, const uint8_t* st, int kk) {
+        if (i >= 2 * MI * (NI - 1) && i % 2 == 1) read_a(st, kk, i / 2 % MI);
+        if (i % (2 * MI) == 2 * MI - 1) read_w(st, kk, i / (2 * MI));
+    };
+    auto substep = [&](const uint8_t* next, int kk) {  // with the reads of `next`, sub-step kk, in this order
 #pragma unroll
-        for (int i = 0; i < C::kALoads; ++i)
-            load(pa[i] + (k0 + kq[i] < k_dim ? k0 + kq[i] : 0), st + (i * C::kThreads + wave * 64) * 16);
-#pragma unroll
-        for (int i = 0; i < C::kWLoads; ++i) {
-            const int64_t k = k0 + kq[i] < k_dim ? k0 + kq[i] : 0;
-            load(pw1[i] + k, st + C::kABytes + (i * C::kThreads + wave * 64) * 16);
-            load(pw2[i] + k, st + C::kABytes + C::kWBytes + (i * C::kThreads + wave * 64) * 16);
+        for (int i = 0; i < C::kMfmas; ++i) {
+            mfma(i);
+            reads_after(i, next, kk);
+            __builtin_amdgcn_sched_barrier(0);
         }
-    };
-    auto fragment = [&](const uint8_t* tile, int row, int chunk) {
-        return *reinterpret_cast<const i32x4*>(tile + (row * kChunks + (chunk ^ swizzle(row))) * 16);
     };
 
-    const int64_t nk = (k_dim + kStep - 1) / kStep;
-    issue(0);
-    for (int64_t kt = 0; kt < nk; ++kt) {
-        uint8_t* st = lds + (kt & 1) * C::kStage;
-        stage_barrier();  // step kt has landed, and nobody reads the other stage any more
-        if (kt + 1 < nk) issue(kt + 1);
-        if (kt + 1 == nk && k_dim % kStep != 0) {
-            const int64_t k0 = kt * kStep;
+    if constexpr (C::kRoll) {
+        // From the middle of one step to the middle of the next: after the barrier the
+        // next step is complete and this one's stage is free, so the step after next
+        // is loaded into it, a load after every kEvery-th matrix instruction.
+        issue(0);
+        meet(0);
+        if (nk > 1) issue(1);
 #pragma unroll
-            for (int i = 0; i < C::kALoads; ++i)
-                if (k0 + kq[i] >= k_dim) *reinterpret_cast<i32x4*>(st + (i * C::kThreads + tid) * 16) = i32x4{0, 0, 0, 0};
-            lds_barrier();
+        for (int i = 0; i < C::kMfmas; ++i) reads_after(i, lds, 0);
+        substep(lds, 1);
+        meet(1);
+        for (int kt = 0; kt + 1 < nk; ++kt) {
+            const uint8_t* next = lds + ((kt + 1) & 1) * C::kStage;
+#pragma unroll
+            for (int i = 0; i < C::kMfmas; ++i) {
+                mfma(i);
+                if (i % C::kEvery == 0 && i / C::kEvery < C::kLoads && loads && kt + 2 < nk)
+                    issue_one(kt + 2, i / C::kEvery);
+                reads_after(i, next, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            substep(next, 1);
+            meet(kt + 2);
         }
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            i32x4 fa[MI], f1[NI], f2[NI];
-            const int chunk = 4 * kk + lane / 16;
+        for (int i = 0; i < C::kMfmas; ++i) mfma(i);
+        __builtin_amdgcn_sched_barrier(0);
+    } else {
+        // Several blocks share a CU and fill each other's waits.
+        issue(0);
+        for (int kt = 0; kt < nk; ++kt) {
+            meet(kt);
+            if (kt + 1 < nk) issue(kt + 1);
 #pragma unroll
-            for (int mi = 0; mi < MI; ++mi) fa[mi] = fragment(st, wm * (C::BM / C::WM) + mi * 16 + lane % 16, chunk);
+            for (int kk = 0; kk < 2; ++kk) {
+                const uint8_t* st = lds + (kt & 1) * C::kStage;
 #pragma unroll
-            for (int ni = 0; ni < NI; ++ni) {
-                const int row = wn * (C::BN / C::WN) + ni * 16 + lane % 16;
-                f1[ni] = fragment(st + C::kABytes, row, chunk);
-                f2[ni] = fragment(st + C::kABytes + C::kWBytes, row, chunk);
+                for (int mi = 0; mi < MI; ++mi) read_a(st, kk, mi);
+#pragma unroll
+                for (int ni = 0; ni < NI; ++ni) read_w(st, kk, ni);
+#pragma unroll
+                for (int i = 0; i < C::kMfmas; ++i) mfma(i);
             }
-#pragma unroll
-            for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-                for (int mi = 0; mi < MI; ++mi) {
-                    acc1[mi][ni] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f1[ni], fa[mi], acc1[mi][ni], 0, 0, 0);
-                    acc2[mi][ni] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f2[ni], fa[mi], acc2[mi][ni], 0, 0, 0);
-                }
         }
     }
     lds_barrier();  // all fragment reads done before the stages become the output tile
@@ -339,6 +457,17 @@ __global__ __launch_bounds__(C::kThreads) void grouped_int8_kernel(
             }
         }
     }
+}
+
+template <class C, Out kOut, bool kWide>
+__global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(2))) void grouped_int8_kernel(
+    const int8_t* __restrict__ a, Rows rows_of, const int8_t* __restrict__ w1, const float* __restrict__ s1,
+    const int8_t* __restrict__ w2, const float* __restrict__ s2, const int32_t* __restrict__ offs,
+    const float* __restrict__ probs, void* __restrict__ out, int rows, int k_dim, int64_t n_dim, int experts,
+    float limit, int64_t n_tiles, int64_t n_blocks) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds + C::BM * 8];
+    grouped_int8_tile<C, kOut, kWide>(lds, a, rows_of, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim, experts,
+                                      limit, n_tiles, n_blocks);
 }
 
 // ---- few rows per expert ---------------------------------------------------------------
@@ -535,26 +664,77 @@ int launch_few(const int8_t* a, const Rows& rows_of, const int8_t* w1, const flo
 
 // ---- launches ------------------------------------------------------------------------
 
-typedef Tile<256, 128, 4, 2, 2> GateUpTile;
-typedef Tile<256, 128, 4, 2, 32> DownTile;
+// Three tile sizes. The large one has the fewest bytes per product and takes a
+// CU by itself; the smaller ones give few rows more blocks, several to a CU.
+template <Out kOut> struct Tiles {
+    typedef Tile<256, 128, 4, 2, 16, 4, true> Large;
+    typedef Tile<128, 64, 2, 2, 16, 4, false> Middle;
+    typedef Tile<64, 64, 2, 2, 16, 4, false> Small;
+};
+template <> struct Tiles<Out::kSwiglu> {
+    typedef Tile<256, 128, 4, 2, 2, 8, true> Large;
+    typedef Tile<128, 64, 2, 2, 2, 4, false> Middle;
+    typedef Tile<64, 64, 2, 2, 2, 4, false> Small;
+};
 
 template <class C, Out kOut>
-int launch_int8(const int8_t* a, const Rows& rows_of, const int8_t* w1, const float* s1, const int8_t* w2,
-                const float* s2, const int32_t* offs, const float* probs, void* out, int64_t rows, int64_t k_dim,
-                int64_t n_dim, int64_t experts, float limit, hipStream_t st) {
-    if (rows <= 8 * experts)
-        return launch_few<1, kOut>(a, rows_of, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim, experts, limit, st);
-    if (rows <= 24 * experts)
-        return launch_few<2, kOut>(a, rows_of, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim, experts, limit, st);
+int launch_tiles(const int8_t* a, const Rows& rows_of, int64_t tokens, const int8_t* w1, const float* s1, const int8_t* w2,
+                 const float* s2, const int32_t* offs, const float* probs, void* out, int64_t rows, int64_t k_dim,
+                 int64_t n_dim, int64_t experts, float limit, hipStream_t st) {
     int64_t n_tiles, n_blocks;
     const int64_t grid =
         grouped_grid(rows, n_dim, kOut == Out::kSwiglu ? C::BN : 2 * C::BN, experts, C::BM, &n_tiles, &n_blocks);
     if (grid == 0) return MOE_EPI_ERR_BAD_SHAPE;
-    (void)hipGetLastError();
-    hipLaunchKernelGGL((grouped_int8_kernel<C, kOut>), dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), 0, st, a,
-                       rows_of, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim, experts, limit, n_tiles,
-                       n_blocks);
-    return launch_status();
+    auto go = [&](auto kernel) {
+        (void)hipGetLastError();
+        hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), 0, st, a, rows_of, w1, s1, w2,
+                           s2, offs, probs, out, static_cast<int>(rows), static_cast<int>(k_dim), n_dim,
+                           static_cast<int>(experts), limit, n_tiles, n_blocks);
+        return launch_status();
+    };
+    if constexpr (kOut == Out::kSwiglu) {
+        // the rows of a are read in place: their offsets pass 31 bits in a large enough tensor
+        if (rows_of.slot_of && tokens * k_dim > INT32_MAX) return go(grouped_int8_kernel<C, kOut, true>);
+    }
+    return go(grouped_int8_kernel<C, kOut, false>);
+}
+
+template <Out kOut>
+int launch_int8(const int8_t* a, const Rows& rows_of, int64_t tokens, const int8_t* w1, const float* s1,
+                const int8_t* w2, const float* s2, const int32_t* offs, const float* probs, void* out, int64_t rows,
+                int64_t k_dim, int64_t n_dim, int64_t experts, float limit, hipStream_t st) {
+    auto few = [&](auto launch) {
+        return launch(a, rows_of, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim, experts, limit, st);
+    };
+    auto tiles = [&](auto launch) {
+        return launch(a, rows_of, tokens, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim, experts, limit, st);
+    };
+    // By the mean number of rows of an expert (offs is on the device): a larger
+    // tile reads the weights fewer times, a smaller one wastes fewer rows of a
+    // partial tile; and a tile size is taken only where it gives half of the CUs
+    // a block. Measured (us, 8 experts, gate_up 7168 -> 2 x 2048 / down 2048 ->
+    // 7168, few rows by 16 / by 32, small, middle, large tiles):
+    //   8 rows an expert   39.2/19.8  41.1/20.9  64.3/25.5  68.5/26.8  96.0/36.6
+    //   24                 71.6/32.4  49.8/25.5  64.7/29.7  68.6/28.9  95.5/36.8
+    //   48                            96.4/47.5  60.3/32.7  64.1/29.5  96.0/37.6
+    //   96                             169/77.5  71.6/49.6  65.5/33.5  96.1/64.4
+    //   192                            291/140    121/76.4  81.2/51.1   101/42.3
+    //   256                            378/185    125/89.0   126/73.7   108/72.7
+    // and where the grid is small (4 experts, 1024 -> 2 x 512):
+    //   100                6.6        6.7         9.8        10.1       19.7
+    //   400                15.6       15.4       10.2        12.1       20.9
+    //   1500               43.1       37.5       15.9        15.1       21.5
+    auto fills = [&](int bm, int cols) { return (rows / bm + experts / 2) * ((n_dim + cols - 1) / cols) >= 128; };
+    constexpr int kCols = kOut == Out::kSwiglu ? 1 : 2;  // column ranges of a tile
+    typedef typename Tiles<kOut>::Large Large;
+    typedef typename Tiles<kOut>::Middle Middle;
+    typedef typename Tiles<kOut>::Small Small;
+    if (rows <= 10 * experts) return few(launch_few<1, kOut>);
+    if (rows <= 24 * experts || !fills(Small::BM, kCols * Small::BN)) return few(launch_few<2, kOut>);
+    if (rows <= 56 * experts || !fills(Middle::BM, kCols * Middle::BN)) return tiles(launch_tiles<Small, kOut>);
+    if (rows <= (kCols == 1 ? 192 : 112) * experts || !fills(Large::BM, kCols * Large::BN))
+        return tiles(launch_tiles<Middle, kOut>);
+    return tiles(launch_tiles<Large, kOut>);
 }
 
 bool shape_ok(int64_t rows, int64_t k_dim, int64_t n_dim, int64_t experts) {
@@ -595,7 +775,7 @@ extern "C" int grouped_gate_up_swiglu_int8_fwd(const int8_t* a, const float* a_s
                            range_of(w_up_scale, sb), range_of(offs, ob), range_of(probs, probs ? rb : 0)})
         if (overlaps(ry, r)) return MOE_EPI_ERR_ALIAS;
     const Rows rows_of{a_scale, slot_of, static_cast<uint32_t>(top_k), tokens * top_k};
-    return launch_int8<GateUpTile, Out::kSwiglu>(a, rows_of, w_gate, w_gate_scale, w_up, w_up_scale, offs, probs, y,
+    return launch_int8<Out::kSwiglu>(a, rows_of, tokens, w_gate, w_gate_scale, w_up, w_up_scale, offs, probs, y,
                                                  rows, hidden, inter, experts, limit, as_stream(stream));
 }
 
@@ -622,8 +802,8 @@ extern "C" int grouped_down_router_int8_fwd(const int8_t* h, const float* h_scal
     const Rows rows_of{h_scale, nullptr, 1u, rows};
     const hipStream_t st = as_stream(stream);
     if (out_dtype == MOE_EPI_F32)
-        return launch_int8<DownTile, Out::kF32>(h, rows_of, w_down, w_down_scale, w_down, w_down_scale, offs, probs,
+        return launch_int8<Out::kF32>(h, rows_of, rows, w_down, w_down_scale, w_down, w_down_scale, offs, probs,
                                                 out, rows, inter, hidden, experts, 1.0f, st);
-    return launch_int8<DownTile, Out::kBf16>(h, rows_of, w_down, w_down_scale, w_down, w_down_scale, offs, probs, out,
+    return launch_int8<Out::kBf16>(h, rows_of, rows, w_down, w_down_scale, w_down, w_down_scale, offs, probs, out,
                                              rows, inter, hidden, experts, 1.0f, st);
 }

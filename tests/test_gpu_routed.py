@@ -324,6 +324,10 @@ PRODUCTS = [([1], 16, 8), ([1], 128, 128), ([1, 0, 3], 48, 24), ([0, 16, 17, 0],
             ([64, 65, 1, 63], 256, 128), ([255, 256, 257], 272, 72), ([700], 128, 520), ([3, 130, 0, 200], 1040, 200),
             ([2] * 33, 400, 40), ([0, 0, 0], 64, 16), ([129, 31, 33, 500], 2064, 48), ([0] * 30 + [100] + [3] * 70, 528, 56),
             ([1, 90, 0, 2, 7], 7184, 40)]
+# enough rows and columns for the small, the middle and the large tiles, partial ones among them; K below,
+# at and past one step and with odd numbers of steps
+PRODUCTS += [(counts * 7, k, n) for counts, n in (([30, 0, 25, 31, 64, 17], 520), ([100, 128, 1, 0, 140, 129], 520),
+                                                  ([300, 256, 257, 1, 512, 0], 776)) for k in (16, 112, 128, 272, 384)]
 
 
 @pytest.mark.parametrize("counts,k,n", PRODUCTS)
@@ -423,22 +427,26 @@ def test_offs_out_of_order_or_past_the_rows_are_clamped():
 
 
 def test_tokens_past_two_and_four_gigabytes():
-    """Rows read in place from a tensor whose byte offsets pass 2^31 and 2^32, moved and multiplied."""
-    tokens, k, n = 600_000, 7200, 16
+    """Rows read in place from a tensor whose byte offsets pass 2^31 and 2^32, moved and multiplied, with
+    few rows and with small, middle and large tiles."""
+    tokens, k = 600_000, 7200
     a = torch.zeros((tokens, k), dtype=torch.int8, device="cuda")
-    picks = [0, 1, 298_261, 298_262, 596_523, 596_524, tokens - 1]
+    picks = np.array([0, 1, 298_261, 298_262, 596_523, 596_524, tokens - 1])
     rng = np.random.default_rng(6)
     values = int8_of(rng, (len(picks), k))
-    a[torch.tensor(picks, device="cuda")] = values
-    w = int8_of(rng, (1, n, k))
+    a[torch.from_numpy(picks).cuda()] = values
     one = torch.ones(tokens, device="cuda")
-    y = sentinel((len(picks), n), torch.bfloat16)
-    epi.grouped_gate_up_swiglu_int8_fwd(a, one * 1e-4, ints(picks), 1, w, one[:n].view(1, n) * 0.01, w,
-                                        one[:n].view(1, n) * 0.01, ints([len(picks)]), None, y, 7.0)
-    want, slack = ref.gate_up(values.cpu().numpy(), np.full(len(picks), 1e-4, np.float32), np.arange(len(picks)),
-                              w.cpu().numpy(), np.full((1, n), 0.01, np.float32), w.cpu().numpy(),
-                              np.full((1, n), 0.01, np.float32), [len(picks)], np.ones(len(picks), np.float32), 7.0)
-    check(y, want, slack, torch.bfloat16, "gate_up")
+    for rows, n in ((7, 16), (2048, 264), (4096, 264), (8192, 776)):
+        w = int8_of(rng, (1, n, k))
+        y = sentinel((rows, n), torch.bfloat16)
+        which = np.arange(rows) % len(picks)
+        epi.grouped_gate_up_swiglu_int8_fwd(a, one * 1e-4, ints(picks[which]), 1, w, one[:n].view(1, n) * 0.01, w,
+                                            one[:n].view(1, n) * 0.01, ints([rows]), None, y, 7.0)
+        s = np.full((1, n), 0.01, np.float32)
+        want, slack = ref.gate_up(values.cpu().numpy(), np.full(len(picks), 1e-4, np.float32), np.arange(len(picks)),
+                                  w.cpu().numpy(), s, w.cpu().numpy(), s, [len(picks)],
+                                  np.ones(len(picks), np.float32), 7.0)
+        check(y, want[which], slack[which], torch.bfloat16, "gate_up")
     x = a.view(torch.bfloat16)                    # the same bytes, moved as 16-bit rows
     out = sentinel((len(picks), k // 2), torch.bfloat16)
     epi.moe_dispatch_fwd(x, ints(picks), 1, out)

@@ -18,6 +18,8 @@
 // accesses of a wavefront are one contiguous run on both sides. Rows of odd
 // width or address are moved by the same vectors at the element's alignment
 // (the hardware takes any), with the last few elements one per lane.
+#include <type_traits>
+
 #include "epi_common.h"
 #include "moe_routed.h"
 
@@ -47,9 +49,16 @@ MOE_WORD(8, u32x2, 4)
 MOE_WORD(8, u32x2, 2)
 #undef MOE_WORD
 
+// Aligned words are streamed (nontemporal); words at the element's alignment
+// share cache lines with their neighbours, whose loads should find them: a
+// weighted sum of 30021 rows of 1001 float16 22.2 -> 19.8 us.
 template <int kBytes, int kAlign>
 __device__ __forceinline__ typename Word<kBytes, kAlign>::plain load_word(const void* p) {
-    return __builtin_nontemporal_load(static_cast<const typename Word<kBytes, kAlign>::type*>(p));
+    const typename Word<kBytes, kAlign>::type* w = static_cast<const typename Word<kBytes, kAlign>::type*>(p);
+    if constexpr (kAlign == kBytes)
+        return __builtin_nontemporal_load(w);
+    else
+        return *w;
 }
 template <int kBytes, int kAlign>
 __device__ __forceinline__ void store_word(void* p, typename Word<kBytes, kAlign>::plain v) {
@@ -106,12 +115,17 @@ struct Vec {
 
 // ---- dispatch ------------------------------------------------------------------------
 
-constexpr int kCopyLanes = 128;
-constexpr int kCopyVecs = 4;  // 16-byte pieces per lane
+constexpr int kCopyLanes = 64;
 
-// One block per (row, segment of kCopyLanes * kCopyVecs pieces): bytes are
-// copied, whatever they stand for. kAlign: of every row on both sides.
-template <int kAlign>
+// One wavefront per (row, segment of kCopyLanes * V 16-byte pieces): bytes are
+// copied, whatever they stand for. kAlign: of every row on both sides. Tokens
+// are read with the caches' default policy, since a token with several rows
+// here is read again. One piece a lane streams best (131072 rows of 7168 bf16,
+// about one a token: 592 us, 6.3 TB/s moved; 2 pieces 634, 4 with 128 lanes
+// 687; a residency limit on the latter 652 to 675); where tokens have many
+// rows, which come from the Infinity Cache, two pieces do (262144 rows of 2048,
+// 8 a token: 299 us against 330).
+template <int kAlign, int V>
 __global__ __launch_bounds__(kCopyLanes) void moe_dispatch_kernel(const char* __restrict__ x,
                                                                   const int32_t* __restrict__ slot_of,
                                                                   char* __restrict__ out, int64_t rows, int64_t slots,
@@ -125,15 +139,16 @@ __global__ __launch_bounds__(kCopyLanes) void moe_dispatch_kernel(const char* __
         const bool has = slot >= 0 && slot < slots;  // a row without a slot is zeros
         const char* src = x + (has ? static_cast<int64_t>(static_cast<uint32_t>(slot) / top_k) * row_bytes : 0);
         char* dst = out + r * row_bytes;
-        const uint32_t c0 = seg * (kCopyLanes * kCopyVecs) + threadIdx.x;
-        u32x4 v[kCopyVecs];
+        const uint32_t c0 = seg * (kCopyLanes * V) + threadIdx.x;
+        u32x4 v[V];
 #pragma unroll
-        for (int k = 0; k < kCopyVecs; ++k) {
+        for (int k = 0; k < V; ++k) {
             v[k] = u32x4{0u, 0u, 0u, 0u};
-            if (has && c0 + k * kCopyLanes < pieces) v[k] = load_word<16, kAlign>(src + (c0 + k * kCopyLanes) * 16u);
+            if (has && c0 + k * kCopyLanes < pieces)
+                v[k] = *reinterpret_cast<const typename Word<16, kAlign>::type*>(src + (c0 + k * kCopyLanes) * 16u);
         }
 #pragma unroll
-        for (int k = 0; k < kCopyVecs; ++k)
+        for (int k = 0; k < V; ++k)
             if (c0 + k * kCopyLanes < pieces) store_word<16, kAlign>(dst + (c0 + k * kCopyLanes) * 16u, v[k]);
         if constexpr (kAlign < 16) {  // the row's last bytes, two at a time
             const uint32_t done = pieces * 16, left = static_cast<uint32_t>(row_bytes) - done;
@@ -146,11 +161,14 @@ __global__ __launch_bounds__(kCopyLanes) void moe_dispatch_kernel(const char* __
 
 // ---- sums over a token's rows ------------------------------------------------------
 
-constexpr int kSumLanes = 128;
+constexpr int kSumLanes = 64;
 constexpr int kSumVecs = 2;  // vectors per lane of a segment
 constexpr int kSumRows = 4;  // rows whose loads are in flight together
 
-// One block per (token, segment). The slots' rows and weights are the same
+// One wavefront per (token, segment). Measured (us): 8 rows a token, 32768
+// tokens of 2048 bf16 206, 5.9 TB/s (128 lanes 214; one vector a lane with 8
+// rows in flight 203); about one row a token, 131072 of 7168 bf16 610, 6.2
+// TB/s (637; 964); float32 rows, 65536 of 7168, 600 (606; 953). The slots' rows and weights are the same
 // for the whole block (scalar loads); those with a row are kept as a bit mask
 // and taken in ascending order, kSumRows at a time.
 template <int TI, int TO, int N, bool kWeighted, bool kAligned>
@@ -246,20 +264,24 @@ __global__ __launch_bounds__(kSumLanes) void moe_row_sum_kernel(const char* __re
 
 // ---- gradients of the weighted combine -----------------------------------------------
 
-constexpr int kGradLanes = 256;
-constexpr int kGradWaves = kGradLanes / 64;
+constexpr int kGradVecs = 4;  // vectors per lane and pass over the row
+constexpr int kGradRows = 2;  // rows whose loads are in flight together
 
-// One block per token: its gradient is read once for up to kSlotChunk slots,
+// L lanes per token: its gradient is read once for up to kSlotChunk slots,
 // each of their rows is read and its gradient written in the same pass, and
-// the products' partial sums stay in one register per slot.
-template <int TG, int TE, int N, bool kDot, bool kAligned>
-__global__ __launch_bounds__(kGradLanes) void moe_combine_grad_kernel(
+// the products' partial sums stay in one register per slot. Rows of up to 256
+// vectors take a wavefront, wider ones four. 65536 tokens of 7168 bf16, about
+// one row each: 432 us, 5.8 TB/s (one vector at a time 450; 2 vectors a lane
+// 445; 448 lanes of 2, an exact fit, 483; default-policy stores 448).
+template <int TG, int TE, int N, int L, bool kDot, bool kAligned>
+__global__ __launch_bounds__(L) void moe_combine_grad_kernel(
     const char* __restrict__ grad, const char* __restrict__ in, const int32_t* __restrict__ row_of,
     const float* __restrict__ weights, char* __restrict__ grad_in, float* __restrict__ grad_w, int64_t rows,
     int64_t tokens, int64_t top_k, int64_t hidden) {
     typedef Vec<TG, N, kAligned> G;
     typedef Vec<TE, N, kAligned> E;
-    __shared__ float part[kGradWaves][kSlotChunk];
+    constexpr int kWaves = L / 64;
+    __shared__ float part[kWaves][kSlotChunk];
     const uint32_t nvec = static_cast<uint32_t>(hidden / N), done = nvec * N;
     const uint32_t left = static_cast<uint32_t>(hidden) - done;
     for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
@@ -280,22 +302,41 @@ __global__ __launch_bounds__(kGradLanes) void moe_combine_grad_kernel(
                 }
             }
             if (mask) {
-                for (uint32_t c = threadIdx.x; c < nvec; c += kGradLanes) {
-                    float g[N];
-                    G::widen(G::load(grow, c * N), g);
+                for (uint32_t c0 = threadIdx.x; c0 < nvec; c0 += L * kGradVecs) {
+                    typename G::Raw gr[kGradVecs];
 #pragma unroll
-                    for (int j = 0; j < kSlotChunk; ++j) {
-                        if (!(mask >> j & 1u)) continue;
-                        float o[N];
+                    for (int u = 0; u < kGradVecs; ++u)
+                        gr[u] = c0 + u * L < nvec ? G::load(grow, (c0 + u * L) * N) : typename G::Raw{};
+#pragma unroll
+                    for (int jj = 0; jj < kSlotChunk; jj += kGradRows) {
+                        typename E::Raw er[kGradRows][kGradVecs];
                         if constexpr (kDot) {
-                            float f[N];
-                            E::widen(E::load(in + at[j], c * N), f);
 #pragma unroll
-                            for (int i = 0; i < N; ++i) dot[j] = __fmaf_rn(g[i], f[i], dot[j]);
+                            for (int q = 0; q < kGradRows; ++q) {
+                                if (!(mask >> (jj + q) & 1u)) continue;
+#pragma unroll
+                                for (int u = 0; u < kGradVecs; ++u)
+                                    er[q][u] = c0 + u * L < nvec ? E::load(in + at[jj + q], (c0 + u * L) * N) : typename E::Raw{};
+                            }
                         }
 #pragma unroll
-                        for (int i = 0; i < N; ++i) o[i] = w[j] * g[i];
-                        E::store(grad_in + at[j], c * N, o);
+                        for (int q = 0; q < kGradRows; ++q) {
+                            if (!(mask >> (jj + q) & 1u)) continue;
+#pragma unroll
+                            for (int u = 0; u < kGradVecs; ++u) {
+                                float g[N], o[N];
+                                G::widen(gr[u], g);
+                                if constexpr (kDot) {
+                                    float f[N];
+                                    E::widen(er[q][u], f);
+#pragma unroll
+                                    for (int i = 0; i < N; ++i) dot[jj + q] = __fmaf_rn(g[i], f[i], dot[jj + q]);
+                                }
+#pragma unroll
+                                for (int i = 0; i < N; ++i) o[i] = w[jj + q] * g[i];
+                                if (c0 + u * L < nvec) E::store(grad_in + at[jj + q], (c0 + u * L) * N, o);
+                            }
+                        }
                     }
                 }
                 if (!kAligned && threadIdx.x < left) {
@@ -320,7 +361,7 @@ __global__ __launch_bounds__(kGradLanes) void moe_combine_grad_kernel(
                 if (threadIdx.x < kSlotChunk && j0 + threadIdx.x < top_k) {
                     float s = 0.0f;
 #pragma unroll
-                    for (int v = 0; v < kGradWaves; ++v) s += part[v][threadIdx.x];
+                    for (int v = 0; v < kWaves; ++v) s += part[v][threadIdx.x];
                     grad_w[t * top_k + j0 + threadIdx.x] = s;
                 }
                 __syncthreads();
@@ -357,20 +398,29 @@ int launch_grad(const void* grad, const void* in, const int32_t* row_of, const f
     constexpr int N = TG == MOE_EPI_F32 || TE == MOE_EPI_F32 ? 4 : 8;
     const bool fit = hidden % N == 0 && aligned(grad, N * kBytesOf<TG>) && aligned(in, N * kBytesOf<TE>) &&
                      aligned(grad_in, N * kBytesOf<TE>);
-    const dim3 grid(grid_for_rows(tokens, 1)), block(kGradLanes);
-    auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, block, 0, st, static_cast<const char*>(grad), static_cast<const char*>(in),
-                           row_of, weights, static_cast<char*>(grad_in), grad_w, rows, tokens, top_k, hidden);
+    const bool wide = hidden / N > 64 * kGradVecs;
+    const dim3 grid(grid_for_rows(tokens, 1));
+    auto go = [&](int lanes, auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(lanes), 0, st, static_cast<const char*>(grad),
+                           static_cast<const char*>(in), row_of, weights, static_cast<char*>(grad_in), grad_w, rows,
+                           tokens, top_k, hidden);
+    };
+    auto pick = [&](auto lanes) {
+        constexpr int L = decltype(lanes)::value;
+        if (fit && grad_w)
+            go(L, moe_combine_grad_kernel<TG, TE, N, L, true, true>);
+        else if (fit)
+            go(L, moe_combine_grad_kernel<TG, TE, N, L, false, true>);
+        else if (grad_w)
+            go(L, moe_combine_grad_kernel<TG, TE, N, L, true, false>);
+        else
+            go(L, moe_combine_grad_kernel<TG, TE, N, L, false, false>);
     };
     (void)hipGetLastError();
-    if (fit && grad_w)
-        go(moe_combine_grad_kernel<TG, TE, N, true, true>);
-    else if (fit)
-        go(moe_combine_grad_kernel<TG, TE, N, false, true>);
-    else if (grad_w)
-        go(moe_combine_grad_kernel<TG, TE, N, true, false>);
+    if (wide)
+        pick(std::integral_constant<int, 256>());
     else
-        go(moe_combine_grad_kernel<TG, TE, N, false, false>);
+        pick(std::integral_constant<int, 64>());
     return launch_status();
 }
 
@@ -402,7 +452,8 @@ extern "C" int moe_dispatch_fwd(const void* x, int dtype, const int32_t* slot_of
     if (!aligned(x, e) || !aligned(out, e) || !aligned(slot_of, 4)) return MOE_EPI_ERR_MISALIGNED;
     const Range ro = range_of(out, n.row_bytes);
     if (overlaps(ro, range_of(x, n.token_bytes)) || overlaps(ro, range_of(slot_of, rows * 4))) return MOE_EPI_ERR_ALIAS;
-    const int64_t bytes = hidden * e, per = kCopyLanes * kCopyVecs;
+    const bool again = rows > 2 * tokens;  // tokens have several rows each
+    const int64_t bytes = hidden * e, per = kCopyLanes * (again ? 2 : 1);
     const int64_t nseg = bytes / 16 <= per ? 1 : (bytes / 16 + per - 1) / per;
     const dim3 grid(grid_for_rows(rows * nseg, 1)), block(kCopyLanes);
     auto go = [&](auto kernel) {
@@ -412,11 +463,11 @@ extern "C" int moe_dispatch_fwd(const void* x, int dtype, const int32_t* slot_of
     };
     (void)hipGetLastError();
     if (bytes % 16 == 0 && aligned(x, 16) && aligned(out, 16))
-        go(moe_dispatch_kernel<16>);
+        again ? go(moe_dispatch_kernel<16, 2>) : go(moe_dispatch_kernel<16, 1>);
     else if (bytes % 4 == 0 && aligned(x, 4) && aligned(out, 4))
-        go(moe_dispatch_kernel<4>);
+        again ? go(moe_dispatch_kernel<4, 2>) : go(moe_dispatch_kernel<4, 1>);
     else
-        go(moe_dispatch_kernel<2>);
+        again ? go(moe_dispatch_kernel<2, 2>) : go(moe_dispatch_kernel<2, 1>);
     return launch_status();
 }
 

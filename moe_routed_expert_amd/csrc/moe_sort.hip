@@ -13,6 +13,15 @@
 // are its rank, and the lowest lane of each mask adds the mask's count to the
 // wavefront's counter of that bucket. The counters are private to a
 // wavefront, so no atomic operation is needed.
+//
+// Short calls are bound by their chain of reads, counts and writes, and a call
+// of up to 1024 or 4096 slots is one block (32 x 8 slots over 64 experts: 4.6
+// us, 5.1 with a block of 1024 threads; 1 x 8 over 256: 4.9). Longer ones
+// count tiles of 4096 slots first: two launches, 131072 x 8 slots over 8 local
+// experts 10.1 us, of which the 12 MB that are read and written need 2; with
+// more than 8192 counts a third launch sums them, since every block would
+// read them all (131072 x 8 over 256 experts 20.3 us against 40.2; 32768 x 8
+// over 128 experts, 8192 counts, 12.7 without it against 14.8).
 #include "epi_common.h"
 #include "moe_routed.h"
 
@@ -25,6 +34,7 @@ constexpr int kGroups = 4;                       // groups of 64 slots per wavef
 constexpr int kTileThreads = 1024;
 constexpr int kTileWaves = kTileThreads / 64;
 constexpr int kTile = kTileThreads * kGroups;    // slots per block
+constexpr int kDirect = 8;                       // counts per thread that a block reads of all tiles
 
 inline int bits_for(int64_t experts) {           // buckets 0 .. experts (experts: no row)
     int n = 0;
@@ -97,59 +107,102 @@ __global__ __launch_bounds__(kTileThreads) void moe_sort_count(const Id* __restr
         hist[static_cast<int64_t>(blockIdx.x) * experts + e] = count[e];
 }
 
-// Rows of one tile's slots. hist holds every tile's counts (not read when
-// there is one tile: its own counts are then the totals).
-template <class Id>
-__global__ __launch_bounds__(kTileThreads) void moe_sort_place(const Id* __restrict__ ids,
-                                                               const int* __restrict__ hist, int* __restrict__ offs,
-                                                               int* __restrict__ row_of, int* __restrict__ slot_of,
-                                                               int64_t slots, int64_t first, int experts, int nbits,
-                                                               int tiles) {
-    // counts per wavefront and bucket (a tile has 4096 slots), total and start per bucket
-    extern __shared__ uint16_t wave_count[];  // [kTileWaves][experts]
-    __shared__ int before[kMaxExperts];       // slots of the bucket in earlier tiles
+// The counts of 64 experts (one a lane) become the slots of earlier tiles, and
+// their totals go to totals[e]: each wavefront sums a run of tiles, then
+// replaces its counts from the sum of the runs before.
+__global__ __launch_bounds__(kTileThreads) void moe_sort_scan(int* __restrict__ hist, int* __restrict__ totals,
+                                                              int64_t tiles, int experts) {
+    __shared__ int run[kTileWaves][64];
+    const int lane = static_cast<int>(threadIdx.x & 63u), wave = static_cast<int>(threadIdx.x >> 6);
+    const int e = static_cast<int>(blockIdx.x) * 64 + lane;
+    const int64_t per = (tiles + kTileWaves - 1) / kTileWaves, t0 = wave * per;
+    const int64_t t1 = t0 + per < tiles ? t0 + per : tiles;
+    int n = 0;
+    if (e < experts)
+#pragma unroll 8
+        for (int64_t t = t0; t < t1; ++t) n += hist[t * experts + e];
+    run[wave][lane] = n;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < wave; ++w) before += run[w][lane];
+    if (e >= experts) return;
+#pragma unroll 8
+    for (int64_t t = t0; t < t1; ++t) {
+        const int c = hist[t * experts + e];
+        hist[t * experts + e] = before;
+        before += c;
+    }
+    if (wave == kTileWaves - 1) totals[e] = before;
+}
+
+// Rows of one tile's slots, kThreads * kGroups of them. A single tile's own
+// counts are the totals (kMany false: hist and totals are not read); of many,
+// hist holds every tile's counts, or, where totals are given, the slots of
+// earlier tiles (moe_sort_scan).
+template <class Id, int kThreads, bool kMany>
+__global__ __launch_bounds__(kThreads) void moe_sort_place(const Id* __restrict__ ids,
+                                                           const int* __restrict__ hist,
+                                                           const int* __restrict__ totals, int* __restrict__ offs,
+                                                           int* __restrict__ row_of, int* __restrict__ slot_of,
+                                                           int64_t slots, int64_t first, int experts, int nbits,
+                                                           int tiles) {
+    // counts per wavefront and bucket (a tile has 4096 slots), earlier tiles' slots and start per bucket
+    constexpr int kWaves = kThreads / 64;
+    extern __shared__ uint16_t wave_count[];  // [kWaves][experts]
+    __shared__ int before[kMaxExperts];
     __shared__ int start[kMaxExperts];
     __shared__ int total_rows;
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     const int tile = static_cast<int>(blockIdx.x);
 
-    for (int i = tid; i < kTileWaves * experts; i += kTileThreads) wave_count[i] = 0;
-    for (int e = tid; e < experts; e += kTileThreads) before[e] = start[e] = 0;
-    __syncthreads();
-
-    const int64_t s0 = static_cast<int64_t>(tile) * kTile + wave * (64 * kGroups) + lane;
+    const int64_t s0 = static_cast<int64_t>(tile) * (kThreads * kGroups) + wave * (64 * kGroups) + lane;
     uint32_t b[kGroups];
     uint64_t mask[kGroups];
     uint16_t* mine = wave_count + wave * experts;
+    // everything that is read is asked for at once
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) b[g] = bucket_of(ids, s0 + g * 64, slots, first, experts);
+    int count[kMany ? kDirect : 1];
+    if constexpr (kMany) {
+#pragma unroll
+        for (int k = 0; k < kDirect; ++k) {
+            const int i = tid + k * kThreads;
+            count[k] = !totals && i < tiles * experts ? hist[i] : 0;
+        }
+    }
+    for (int i = lane; i < experts; i += 64) mine[i] = 0;
+    for (int e = tid; e < experts; e += kThreads) {
+        start[e] = kMany && totals ? totals[e] : 0;
+        before[e] = kMany && totals ? hist[static_cast<int64_t>(tile) * experts + e] : 0;
+    }
+    if constexpr (kMany) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kDirect; ++k) {
+            if (count[k] == 0) continue;
+            const uint32_t i = tid + k * kThreads, t = i / static_cast<uint32_t>(experts), e = i - t * experts;
+            atomicAdd(&start[e], count[k]);  // whole numbers: any order, one sum
+            if (static_cast<int>(t) < tile) atomicAdd(&before[e], count[k]);
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
         mask[g] = same_bucket(b[g], nbits);
         if (b[g] < static_cast<uint32_t>(experts) && is_lowest(mask[g])) mine[b[g]] += __popcll(mask[g]);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-    if (tiles > 1) {
-        // earlier tiles' counts and all tiles' counts of each bucket
-        for (int64_t i = tid; i < static_cast<int64_t>(tiles) * experts; i += kTileThreads) {
-            const int c = hist[i], e = static_cast<int>(i % experts);
-            if (c != 0) {
-                atomicAdd(&start[e], c);
-                if (i / experts < tile) atomicAdd(&before[e], c);
-            }
-        }
-    }
     __syncthreads();
     // the wavefronts' counts become the slots of the bucket in the tile's earlier wavefronts
-    for (int e = tid; e < experts; e += kTileThreads) {
+    for (int e = tid; e < experts; e += kThreads) {
         int n = 0;
-        for (int w = 0; w < kTileWaves; ++w) {
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
             const int c = wave_count[w * experts + e];
             wave_count[w * experts + e] = static_cast<uint16_t>(n);
             n += c;
         }
-        if (tiles == 1) start[e] = n;
-        if (tile == 0) before[e] = 0;
+        if constexpr (!kMany) start[e] = n;
     }
     __syncthreads();
     if (wave == 0) {
@@ -159,7 +212,7 @@ __global__ __launch_bounds__(kTileThreads) void moe_sort_place(const Id* __restr
     __syncthreads();
     const int rows = total_rows;
     if (tile == 0)
-        for (int e = tid; e < experts; e += kTileThreads) offs[e] = e + 1 < experts ? start[e + 1] : rows;
+        for (int e = tid; e < experts; e += kThreads) offs[e] = e + 1 < experts ? start[e + 1] : rows;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
         const int64_t s = s0 + g * 64;
@@ -189,17 +242,29 @@ bool sizes_ok(int64_t tokens, int64_t top_k, int64_t experts) {
 
 int64_t tiles_of(int64_t slots) { return (slots + kTile - 1) / kTile; }
 
+// Every block of moe_sort_place reads all counts, kDirect a thread, while they
+// are that few; beyond that a third launch sums them first.
+bool scans(int64_t tiles, int64_t experts) { return tiles * experts > kDirect * kTileThreads; }
+
 template <class Id>
 void launch_sort(const void* ids, int64_t first, int* offs, int* row_of, int* slot_of, int* hist, int64_t slots,
                  int experts, hipStream_t st) {
     const int tiles = static_cast<int>(tiles_of(slots));
     const Id* p = static_cast<const Id*>(ids);
-    if (tiles > 1)
-        hipLaunchKernelGGL((moe_sort_count<Id>), dim3(tiles), dim3(kTileThreads), 0, st, p, hist, slots, first,
+    int* totals = nullptr;
+    auto place = [&](int threads, auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(tiles), dim3(threads), threads / 64 * experts * static_cast<int>(sizeof(uint16_t)),
+                           st, p, hist, totals, offs, row_of, slot_of, slots, first, experts, bits_for(experts), tiles);
+    };
+    if (slots <= 256 * kGroups) return place(256, moe_sort_place<Id, 256, false>);
+    if (tiles == 1) return place(kTileThreads, moe_sort_place<Id, kTileThreads, false>);
+    hipLaunchKernelGGL((moe_sort_count<Id>), dim3(tiles), dim3(kTileThreads), 0, st, p, hist, slots, first, experts);
+    if (scans(tiles, experts)) {
+        totals = hist + static_cast<int64_t>(tiles) * experts;
+        hipLaunchKernelGGL(moe_sort_scan, dim3((experts + 63) / 64), dim3(kTileThreads), 0, st, hist, totals, tiles,
                            experts);
-    hipLaunchKernelGGL((moe_sort_place<Id>), dim3(tiles), dim3(kTileThreads),
-                       kTileWaves * experts * static_cast<int>(sizeof(uint16_t)), st, p, hist, offs, row_of, slot_of,
-                       slots, first, experts, bits_for(experts), tiles);
+    }
+    place(kTileThreads, moe_sort_place<Id, kTileThreads, true>);
 }
 
 }  // namespace
@@ -210,7 +275,7 @@ using namespace moe_epi;
 extern "C" int64_t moe_sort_workspace_bytes(int64_t tokens, int64_t top_k, int64_t experts) {
     if (!sizes_ok(tokens, top_k, experts)) return -1;
     const int64_t tiles = tiles_of(tokens * top_k);
-    return tiles > 1 ? tiles * experts * 4 : 0;
+    return tiles > 1 ? (tiles + 1) * experts * 4 : 0;
 }
 
 extern "C" int moe_sort_fwd(const void* expert_of, int id_bytes, int64_t first_expert, int32_t* offs, int32_t* row_of,

@@ -28,14 +28,19 @@
 //               instructions in a fixed order. A step of it reads 192 KiB from
 //               LDS and writes 64 KiB, 2048 cycles at 128 bytes a cycle, beside
 //               2048 cycles of matrix instructions: the two bound it together.
-//               65536 rows over 8 experts: gate_up (7168 -> 2 x 2048) 1609 us,
-//               2392 TOP/s (the plain loop 1695 us), down (2048 -> 7168, bf16
-//               out) 972 us, 1980 TOP/s, its shorter K giving the output's
-//               stores a larger share; a library product of 16384^3 in int8
-//               runs at 2341 TOP/s on this part. Eight loading wavefronts
-//               against four: gate_up 1609 / 1641 us, down 1002 / 983; row
-//               tiles per group: gate_up 1: 1691, 2: 1641, 4: 1648, 8: 1689;
-//               down 8: 977, 16: 972, 32: 983, 128: 1002.
+//               65536 rows over 8 experts: gate_up (7168 -> 2 x 2048) 1570 us,
+//               2452 TOP/s, down (2048 -> 7168, bf16 out) 927 us, 2076 TOP/s,
+//               float32 out 1029 us: its shorter K gives the output a larger
+//               share; a library product of 16384^3 in int8 runs at 2341 TOP/s
+//               on this part. On the way there, gate_up / down: the plain loop
+//               1695 / 1010; the loop written out 1609 / 960; the first two
+//               steps' loads issued together, the scales asked for at the start
+//               and the output staged in one piece 1590 / 940; nontemporal
+//               stores of the output 1570 / 927. Eight loading wavefronts
+//               against four: gate_up 1609 / 1641, down 947 / 940; row tiles
+//               per group: gate_up 1: 1691, 2: 1641, 4: 1648, 8: 1689; down 8:
+//               977, 16: 972, 32: 983, 128: 1002; steps of 64 with two blocks
+//               per CU (128 x 128 x 2 or 256 x 64 x 2): gate_up 1935, down 1099.
 #include "epi_common.h"
 #include "grouped_map.h"
 #include "moe_routed.h"
@@ -83,8 +88,8 @@ struct Tile {
     static constexpr int kMfmas = 2 * MI * NI;            // of a sub-step of 64
     static constexpr int kEvery = kMfmas / kLoads;        // matrix instructions per load
     static constexpr int kLds = 2 * kStage;
-    static constexpr int kLdo = BN + 8;  // elements per row of a staged bf16 tile
-    static_assert(BM * kLdo * 2 <= kLds && BM * BN * 4 <= kLds, "a staged output tile fits");
+    static_assert(BM * BN * 4 <= kLds, "a staged output tile fits: both halves in bf16, one in float32");
+    static_assert(BM + 2 * BN <= kThreads, "a thread per row and per column of the scales");
     static_assert(kALoads >= 1 && kWLoads >= 1 && BM * kChunks % kLoadThreads == 0 && BN * kChunks % kLoadThreads == 0,
                   "whole chunks per lane");
     static_assert(kEvery >= 1, "a load per matrix instruction at most");
@@ -169,6 +174,7 @@ __device__ __forceinline__ void grouped_int8_tile(
     constexpr int MI = C::MI, NI = C::NI;
     float* const row_scale = reinterpret_cast<float*>(lds + C::kLds);
     float* const row_prob = row_scale + C::BM;
+    float* const col_scale = row_prob + C::BM;  // of the two weight tiles
 
     int64_t mt, nt;
     tile_of(blockIdx.x, n_blocks / n_tiles, n_tiles, C::GM, &mt, &nt);
@@ -183,11 +189,19 @@ __device__ __forceinline__ void grouped_int8_tile(
     const int wm = wave / C::WN, wn = wave % C::WN;
     const bool loads = wave < C::kLoadWaves;
 
+    // The scales of a row and its probability, or of a column, one thread each:
+    // asked for now, kept in LDS once the products are done.
+    const int64_t wrow = static_cast<int64_t>(tr.expert) * n_dim;
+    float scale = 0.0f, prob = 1.0f;
     if (tid < C::BM) {
         const int r = tr.row0 + (tid < tr.rows ? tid : tr.rows - 1);
         const int64_t u = rows_of.of(r);
-        row_scale[tid] = u >= 0 ? rows_of.scale[u] : 0.0f;
-        row_prob[tid] = probs ? probs[r] : 1.0f;
+        if (u >= 0) scale = rows_of.scale[u];
+        if (probs) prob = probs[r];
+    } else if (tid < C::BM + 2 * C::BN) {
+        const int c = tid - C::BM, second = c >= C::BN;
+        if (c - second * C::BN < (second ? n2 : n1))
+            scale = (second ? s2 : s1)[wrow + (second ? col2 - C::BN : col1) + c];
     }
 
     // This lane's 16-byte chunks of a stage: slot row * 8 + (chunk ^ swizzle(row))
@@ -197,7 +211,6 @@ __device__ __forceinline__ void grouped_int8_tile(
     // the lane's 32-bit offset from it, and the step's offset in a scalar; only
     // the rows of a tensor of 2 GiB and more, read in place, need 64-bit addresses.
     constexpr int kFlags = 0x00020000;  // raw buffer, 32-bit data format
-    const int64_t wrow = static_cast<int64_t>(tr.expert) * n_dim;
     const int lrow = (wave % C::kLoadWaves * 64 + lane) / kChunks;
     const int kq = ((lane % kChunks) ^ swizzle(lrow)) * 16;
     const int8_t* const abase = rows_of.slot_of ? a : a + static_cast<int64_t>(tr.row0) * k_dim;
@@ -328,8 +341,16 @@ __device__ __forceinline__ void grouped_int8_tile(
         // next step is complete and this one's stage is free, so the step after next
         // is loaded into it, a load after every kEvery-th matrix instruction.
         issue(0);
-        meet(0);
-        if (nk > 1) issue(1);
+        if (nk > 1) {
+            issue(1);
+            __builtin_amdgcn_s_waitcnt((C::kLoads & 0xF) | 0x0070 | (C::kLoads >> 4) << 14);  // step 0 has landed
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        } else {
+            meet(0);
+        }
 #pragma unroll
         for (int i = 0; i < C::kMfmas; ++i) reads_after(i, lds, 0);
         substep(lds, 1);
@@ -368,33 +389,37 @@ __device__ __forceinline__ void grouped_int8_tile(
             }
         }
     }
+    if (tid < C::BM) {
+        row_scale[tid] = scale;
+        row_prob[tid] = prob;
+    } else if (tid < C::BM + 2 * C::BN) {
+        col_scale[tid - C::BM] = scale;
+    }
     lds_barrier();  // all fragment reads done before the stages become the output tile
 
     // Lane l holds, in register j of tile (mi, ni), row mi * 16 + l % 16 and
     // column ni * 16 + 4 * (l / 16) + j of the wavefront's part.
-    auto col_scale = [&](const float* s, int64_t col, int n) {
-        f32x4 v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = n > j ? s[wrow + col + j] : 0.0f;
-        return v;
-    };
+    auto col_of = [&](int ni) { return wn * (C::BN / C::WN) + ni * 16 + 4 * (lane / 16); };
+    auto row_of = [&](int mi) { return wm * (C::BM / C::WM) + mi * 16 + lane % 16; };
     if constexpr (kOut != Out::kF32) {
-        uint16_t* stage = reinterpret_cast<uint16_t*>(lds);
-        uint16_t* o = static_cast<uint16_t*>(out);
+        // The whole output tile in bf16, the two column ranges of down side by side,
+        // so that a row is stored in one run. 16-byte chunks of a row are swizzled by
+        // the row: 16 rows of one chunk take 16 different bank groups.
+        constexpr int kCols = kPair ? C::BN : 2 * C::BN, kRowChunks = kCols / 8;
+        constexpr int kWrap = kRowChunks < 16 ? kRowChunks : 16, kEach = 16 / kWrap;
+        uint8_t* const stage = lds;
+        auto at = [](int row, int c) { return (row * kRowChunks + ((c / 8) ^ (row / kEach % kWrap))) * 16 + c % 8 * 2; };
 #pragma unroll
-        for (int half = 0; half < (kPair ? 1 : 2); ++half) {
-            const int64_t c0 = half == 0 ? col1 : col2;
-            const int n = half == 0 ? n1 : n2;
-            if (half == 1) lds_barrier();
+        for (int half = 0; half < (kPair ? 1 : 2); ++half)
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni) {
-                const int c = wn * (C::BN / C::WN) + ni * 16 + 4 * (lane / 16);
-                const f32x4 sc1 = col_scale(half == 0 ? s1 : s2, c0 + c, n - c);
+                const int c = half * C::BN + col_of(ni);
+                const f32x4 sc1 = *reinterpret_cast<const f32x4*>(col_scale + c);
                 f32x4 sc2{};
-                if constexpr (kPair) sc2 = col_scale(s2, c0 + c, n - c);
+                if constexpr (kPair) sc2 = *reinterpret_cast<const f32x4*>(col_scale + C::BN + c);
 #pragma unroll
                 for (int mi = 0; mi < MI; ++mi) {
-                    const int r = wm * (C::BM / C::WM) + mi * 16 + lane % 16;
+                    const int r = row_of(mi);
                     const float sa = row_scale[r], p = row_prob[r];
                     float v[4];
 #pragma unroll
@@ -408,18 +433,18 @@ __device__ __forceinline__ void grouped_int8_tile(
                             v[j] = static_cast<float>(q) * sa * sc1[j] * p;
                         }
                     }
-                    *reinterpret_cast<u32x2*>(stage + r * C::kLdo + c) =
-                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    *reinterpret_cast<u32x2*>(stage + at(r, c)) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
                 }
             }
-            lds_barrier();
+        lds_barrier();
+        uint16_t* o = static_cast<uint16_t*>(out) + col1;
+        const int n = kPair ? n1 : n1 + n2;
 #pragma unroll
-            for (int i = 0; i < C::BM * C::BN / 8 / C::kThreads; ++i) {
-                const int s = i * C::kThreads + tid, row = s / (C::BN / 8), c = s % (C::BN / 8) * 8;
-                if (row < tr.rows && c < n)
-                    *reinterpret_cast<u32x4*>(o + static_cast<int64_t>(tr.row0 + row) * n_dim + c0 + c) =
-                        *reinterpret_cast<const u32x4*>(stage + row * C::kLdo + c);
-            }
+        for (int i = 0; i < C::BM * kRowChunks / C::kThreads; ++i) {
+            const int s = i * C::kThreads + tid, row = s / kRowChunks, c = s % kRowChunks * 8;
+            if (row < tr.rows && c < n)
+                store_nt16(o + static_cast<int64_t>(tr.row0 + row) * n_dim + c,
+                           *reinterpret_cast<const u32x4*>(stage + at(row, c)));
         }
     } else {
         // float32, one weight tile at a time; 16-byte chunks of a row swizzled by the row
@@ -433,11 +458,11 @@ __device__ __forceinline__ void grouped_int8_tile(
             if (half == 1) lds_barrier();
 #pragma unroll
             for (int ni = 0; ni < NI; ++ni) {
-                const int c = wn * (C::BN / C::WN) + ni * 16 + 4 * (lane / 16);
-                const f32x4 sc = col_scale(half == 0 ? s1 : s2, c0 + c, n - c);
+                const int c = col_of(ni);
+                const f32x4 sc = *reinterpret_cast<const f32x4*>(col_scale + half * C::BN + c);
 #pragma unroll
                 for (int mi = 0; mi < MI; ++mi) {
-                    const int r = wm * (C::BM / C::WM) + mi * 16 + lane % 16;
+                    const int r = row_of(mi);
                     const float sa = row_scale[r], p = row_prob[r];
                     f32x4 v;
 #pragma unroll
@@ -465,7 +490,7 @@ __global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(2))
     const int8_t* __restrict__ w2, const float* __restrict__ s2, const int32_t* __restrict__ offs,
     const float* __restrict__ probs, void* __restrict__ out, int rows, int k_dim, int64_t n_dim, int experts,
     float limit, int64_t n_tiles, int64_t n_blocks) {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds + C::BM * 8];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[C::kLds + 8 * (C::BM + C::BN)];
     grouped_int8_tile<C, kOut, kWide>(lds, a, rows_of, w1, s1, w2, s2, offs, probs, out, rows, k_dim, n_dim, experts,
                                       limit, n_tiles, n_blocks);
 }

@@ -28,6 +28,7 @@ from . import binding
 from .binding import DTYPE_CODE, MoeEpiError
 
 _BF16, _F32, _I32, _I64, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.int8
+_raw_stream = torch._C._cuda_getCurrentRawStream
 _fns = None
 
 
@@ -57,12 +58,14 @@ def _lib():
 
 
 def _take(t, name: str, dtype, shape, device: int) -> int:
-    """The address of a contiguous tensor of this dtype and shape on this GPU; raises otherwise."""
-    if (t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == device and device >= 0
-            and t.is_contiguous()):
+    """The address of a contiguous tensor of this dtype and shape (None: any) on this device; raises otherwise."""
+    if (t is not None and t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
         return t.data_ptr()
+    if t is None:
+        raise ValueError(f"{name} is required")
     where = torch.device("cuda", device) if device >= 0 else torch.device("cuda")
-    binding._need(t, name, dtype, [shape], where)
+    binding._need(t, name, dtype, [t.shape if shape is None else shape], where)
     raise ValueError(f"{name}: expected a tensor on {where}, got {t.device}")
 
 
@@ -74,32 +77,36 @@ def _code(t: torch.Tensor, name: str) -> int:
 
 
 def _matrix(t: torch.Tensor, name: str):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(shape)}")
+    return shape
 
 
 def _vector(t: torch.Tensor, name: str) -> int:
-    if t.dim() != 1:
-        raise ValueError(f"{name} must be 1-D, got {tuple(t.shape)}")
-    return t.shape[0]
+    shape = t.shape
+    if len(shape) != 1:
+        raise ValueError(f"{name} must be 1-D, got {tuple(shape)}")
+    return shape[0]
 
 
 def _experts(w: torch.Tensor, name: str):
-    if w.dim() != 3:
-        raise ValueError(f"{name} must be 3-D [experts, out, in], got {tuple(w.shape)}")
-    return w.shape
+    shape = w.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be 3-D [experts, out, in], got {tuple(shape)}")
+    return shape
 
 
 def _stream(device: int, stream) -> int:
+    if device < 0:
+        raise ValueError("expected tensors on a GPU")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
+        return _raw_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _check(status: int, where: str) -> None:
-    if status:
-        raise MoeEpiError(status, where)
+def _fail(status: int, where: str) -> None:
+    raise MoeEpiError(status, where)
 
 
 # ---- order of the rows ------------------------------------------------------------
@@ -120,15 +127,17 @@ def moe_sort_fwd(expert_of, first_expert: int, offs, row_of, slot_of, workspace=
     tokens, top_k = _matrix(expert_of, "expert_of")
     dev, wide = expert_of.get_device(), expert_of.dtype is _I64
     experts = _vector(offs, "offs")
-    ids = _take(expert_of, "expert_of", _I64 if wide else _I32, (tokens, top_k), dev)
+    ids = _take(expert_of, "expert_of", _I64 if wide else _I32, None, dev)
     ws, nbytes = None, 0
     if workspace is not None:
         nbytes = _vector(workspace, "workspace")
-        ws = _take(workspace, "workspace", torch.uint8, (nbytes,), dev)
-    _check(_lib().moe_sort_fwd(ids, 8 if wide else 4, first_expert, _take(offs, "offs", _I32, (experts,), dev),
-                               _take(row_of, "row_of", _I32, (tokens, top_k), dev),
-                               _take(slot_of, "slot_of", _I32, (tokens * top_k,), dev), ws, nbytes, tokens, top_k,
-                               experts, _stream(dev, stream)), "moe_sort_fwd")
+        ws = _take(workspace, "workspace", torch.uint8, None, dev)
+    status = (_fns or _lib()).moe_sort_fwd(
+        ids, 8 if wide else 4, first_expert, _take(offs, "offs", _I32, None, dev),
+        _take(row_of, "row_of", _I32, (tokens, top_k), dev), _take(slot_of, "slot_of", _I32, (tokens * top_k,), dev), ws,
+        nbytes, tokens, top_k, experts, _stream(dev, stream))
+    if status:
+        _fail(status, "moe_sort_fwd")
 
 
 def moe_sort(expert_of, experts: int, first_expert: int = 0):
@@ -150,10 +159,11 @@ def moe_dispatch_fwd(x, slot_of, top_k: int, out, stream=None) -> None:
     hidden], out [rows, hidden] of x's dtype (bf16, fp16 or fp32); slot_of int32 [rows]."""
     tokens, hidden = _matrix(x, "x")
     rows, dev, dt, code = _vector(slot_of, "slot_of"), x.get_device(), x.dtype, _code(x, "x")
-    _check(_lib().moe_dispatch_fwd(_take(x, "x", dt, (tokens, hidden), dev), code,
-                                   _take(slot_of, "slot_of", _I32, (rows,), dev),
-                                   _take(out, "out", dt, (rows, hidden), dev), rows, tokens, top_k, hidden,
-                                   _stream(dev, stream)), "moe_dispatch_fwd")
+    status = (_fns or _lib()).moe_dispatch_fwd(
+        _take(x, "x", dt, None, dev), code, _take(slot_of, "slot_of", _I32, None, dev),
+        _take(out, "out", dt, (rows, hidden), dev), rows, tokens, top_k, hidden, _stream(dev, stream))
+    if status:
+        _fail(status, "moe_dispatch_fwd")
 
 
 def moe_dispatch_bwd(grad_out, row_of, grad_x, stream=None) -> None:
@@ -162,10 +172,11 @@ def moe_dispatch_bwd(grad_out, row_of, grad_x, stream=None) -> None:
     rows, hidden = _matrix(grad_out, "grad_out")
     tokens, top_k = _matrix(row_of, "row_of")
     dev, dt, code = grad_x.get_device(), grad_out.dtype, _code(grad_out, "grad_out")
-    _check(_lib().moe_dispatch_bwd(_take(grad_out, "grad_out", dt, (rows, hidden), dev), code,
-                                   _take(row_of, "row_of", _I32, (tokens, top_k), dev),
-                                   _take(grad_x, "grad_x", dt, (tokens, hidden), dev), rows, tokens, top_k, hidden,
-                                   _stream(dev, stream)), "moe_dispatch_bwd")
+    status = (_fns or _lib()).moe_dispatch_bwd(
+        _take(grad_out, "grad_out", dt, None, dev), code, _take(row_of, "row_of", _I32, None, dev),
+        _take(grad_x, "grad_x", dt, (tokens, hidden), dev), rows, tokens, top_k, hidden, _stream(dev, stream))
+    if status:
+        _fail(status, "moe_dispatch_bwd")
 
 
 def moe_combine_weighted_fwd(expert_out, row_of, weights, out, stream=None) -> None:
@@ -175,11 +186,13 @@ def moe_combine_weighted_fwd(expert_out, row_of, weights, out, stream=None) -> N
     rows, hidden = _matrix(expert_out, "expert_out")
     tokens, top_k = _matrix(row_of, "row_of")
     dev, code, out_code = out.get_device(), _code(expert_out, "expert_out"), _code(out, "out")
-    _check(_lib().moe_combine_weighted_fwd(
-        _take(expert_out, "expert_out", expert_out.dtype, (rows, hidden), dev), code,
-        _take(row_of, "row_of", _I32, (tokens, top_k), dev), _take(weights, "weights", _F32, (tokens, top_k), dev),
+    status = (_fns or _lib()).moe_combine_weighted_fwd(
+        _take(expert_out, "expert_out", expert_out.dtype, None, dev), code,
+        _take(row_of, "row_of", _I32, None, dev), _take(weights, "weights", _F32, (tokens, top_k), dev),
         _take(out, "out", out.dtype, (tokens, hidden), dev), out_code, rows, tokens, top_k, hidden,
-        _stream(dev, stream)), "moe_combine_weighted_fwd")
+        _stream(dev, stream))
+    if status:
+        _fail(status, "moe_combine_weighted_fwd")
 
 
 def moe_combine_weighted_bwd(grad_out, expert_out, row_of, weights, grad_expert_out, grad_weights,
@@ -194,12 +207,14 @@ def moe_combine_weighted_bwd(grad_out, expert_out, row_of, weights, grad_expert_
     if grad_weights is not None:
         eo = _take(expert_out, "expert_out", dt, (rows, hidden), dev)
         gw = _take(grad_weights, "grad_weights", _F32, (tokens, top_k), dev)
-    _check(_lib().moe_combine_weighted_bwd(
-        _take(grad_out, "grad_out", grad_out.dtype, (tokens, hidden), dev), grad_code, eo, code,
+    status = (_fns or _lib()).moe_combine_weighted_bwd(
+        _take(grad_out, "grad_out", grad_out.dtype, None, dev), grad_code, eo, code,
         _take(row_of, "row_of", _I32, (tokens, top_k), dev),
         _take(weights, "weights", _F32, (tokens, top_k), dev),
         _take(grad_expert_out, "grad_expert_out", dt, (rows, hidden), dev), gw, rows, tokens, top_k, hidden,
-        _stream(dev, stream)), "moe_combine_weighted_bwd")
+        _stream(dev, stream))
+    if status:
+        _fail(status, "moe_combine_weighted_bwd")
 
 
 class MoeDispatch(torch.autograd.Function):
@@ -253,10 +268,11 @@ def quantize_rows_int8_fwd(x, q, scale, stream=None) -> None:
     q int8 [rows, cols]; scale fp32 [rows]."""
     rows, cols = _matrix(x, "x")
     dev, code = x.get_device(), _code(x, "x")
-    _check(_lib().quantize_rows_int8_fwd(_take(x, "x", x.dtype, (rows, cols), dev), code,
-                                         _take(q, "q", _I8, (rows, cols), dev),
-                                         _take(scale, "scale", _F32, (rows,), dev), rows, cols,
-                                         _stream(dev, stream)), "quantize_rows_int8_fwd")
+    status = (_fns or _lib()).quantize_rows_int8_fwd(
+        _take(x, "x", x.dtype, None, dev), code, _take(q, "q", _I8, (rows, cols), dev),
+        _take(scale, "scale", _F32, (rows,), dev), rows, cols, _stream(dev, stream))
+    if status:
+        _fail(status, "quantize_rows_int8_fwd")
 
 
 def quantize_rows_int8(x):
@@ -278,8 +294,8 @@ def grouped_gate_up_swiglu_int8_fwd(a, a_scale, slot_of, top_k: int, w_gate, w_g
     tokens, hidden = _matrix(a, "a")
     experts, inter, _ = _experts(w_gate, "w_gate")
     rows, dev = _matrix(y, "y")[0], a.get_device()
-    _check(_lib().grouped_gate_up_swiglu_int8_fwd(
-        _take(a, "a", _I8, (tokens, hidden), dev), _take(a_scale, "a_scale", _F32, (tokens,), dev),
+    status = (_fns or _lib()).grouped_gate_up_swiglu_int8_fwd(
+        _take(a, "a", _I8, None, dev), _take(a_scale, "a_scale", _F32, (tokens,), dev),
         None if slot_of is None else _take(slot_of, "slot_of", _I32, (rows,), dev),
         _take(w_gate, "w_gate", _I8, (experts, inter, hidden), dev),
         _take(w_gate_scale, "w_gate_scale", _F32, (experts, inter), dev),
@@ -287,7 +303,9 @@ def grouped_gate_up_swiglu_int8_fwd(a, a_scale, slot_of, top_k: int, w_gate, w_g
         _take(w_up_scale, "w_up_scale", _F32, (experts, inter), dev), _take(offs, "offs", _I32, (experts,), dev),
         None if probs is None else _take(probs, "probs", _F32, (rows,), dev),
         _take(y, "y", _BF16, (rows, inter), dev), rows, tokens, top_k, hidden, inter, experts, limit,
-        _stream(dev, stream)), "grouped_gate_up_swiglu_int8_fwd")
+        _stream(dev, stream))
+    if status:
+        _fail(status, "grouped_gate_up_swiglu_int8_fwd")
 
 
 def grouped_down_router_int8_fwd(h, h_scale, w_down, w_down_scale, offs, probs, out, stream=None) -> None:
@@ -300,10 +318,12 @@ def grouped_down_router_int8_fwd(h, h_scale, w_down, w_down_scale, offs, probs, 
     dev = h.get_device()
     if out.dtype is not _BF16 and out.dtype is not _F32:
         raise TypeError(f"out: expected bfloat16 or float32, got {out.dtype}")
-    _check(_lib().grouped_down_router_int8_fwd(
-        _take(h, "h", _I8, (rows, inter), dev), _take(h_scale, "h_scale", _F32, (rows,), dev),
+    status = (_fns or _lib()).grouped_down_router_int8_fwd(
+        _take(h, "h", _I8, None, dev), _take(h_scale, "h_scale", _F32, (rows,), dev),
         _take(w_down, "w_down", _I8, (experts, hidden, inter), dev),
         _take(w_down_scale, "w_down_scale", _F32, (experts, hidden), dev), _take(offs, "offs", _I32, (experts,), dev),
         None if probs is None else _take(probs, "probs", _F32, (rows,), dev),
         _take(out, "out", out.dtype, (rows, hidden), dev), DTYPE_CODE[out.dtype], rows, inter, hidden, experts,
-        _stream(dev, stream)), "grouped_down_router_int8_fwd")
+        _stream(dev, stream))
+    if status:
+        _fail(status, "grouped_down_router_int8_fwd")

@@ -216,9 +216,10 @@ __device__ __forceinline__ void grouped_int8_tile(
     const int8_t* const abase = rows_of.slot_of ? a : a + static_cast<int64_t>(tr.row0) * k_dim;
     const int8_t* const t1 = w1 + (wrow + col1) * k_dim;
     const int8_t* const t2 = w2 + (wrow + (n2 > 0 ? col2 : col1)) * k_dim;
-    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(abase), 0, 0x7FFFFFFF, kFlags),
-                                 r1 = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(t1), 0, 0x7FFFFFFF, kFlags),
-                                 r2 = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(t2), 0, 0x7FFFFFFF, kFlags);
+    auto buffer = [](const int8_t* p) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(p), 0, 0x7FFFFFFF, kFlags);
+    };
+    const __amdgpu_buffer_rsrc_t ra = buffer(abase), r1 = buffer(t1), r2 = buffer(t2);
     int va[C::kALoads], v1[C::kWLoads], v2[C::kWLoads];
     const int8_t* pa[kWide ? C::kALoads : 1];
     if (loads) {
@@ -246,7 +247,8 @@ __device__ __forceinline__ void grouped_int8_tile(
     // Load number i of step kt: the rows' chunks first, then the weights' in
     // pairs. A step that crosses the end of K takes the start of the row for
     // the chunks past it.
-    const int nk = (k_dim + kStep - 1) / kStep, last = k_dim % kStep ? nk - 1 : nk;  // the step that crosses, if one does
+    const int nk = (k_dim + kStep - 1) / kStep;
+    const int last = k_dim % kStep ? nk - 1 : -1;  // the step that crosses, if one does
     auto issue_one = [&](int kt, int i) {
         uint8_t* st = lds + (kt & 1) * C::kStage;
         int k = kt * kStep, more = 0;
@@ -255,12 +257,14 @@ __device__ __forceinline__ void grouped_int8_tile(
             k = 0;
         }
         auto bl = [&](__amdgpu_buffer_rsrc_t r, int v, uint8_t* dst) {
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, v + more, k, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, v + more, k,
+                                                     0, 0);
         };
         if (i < C::kALoads) {
             uint8_t* dst = st + (i * C::kLoadThreads + wave * 64) * 16;
             if constexpr (kWide)
-                __builtin_amdgcn_global_load_lds(pa[i] + k + more, (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+                __builtin_amdgcn_global_load_lds(pa[i] + k + more, (__attribute__((address_space(3))) void*)dst, 16, 0,
+                                                 0);
             else
                 bl(ra, va[i], dst);
         } else {
@@ -286,7 +290,8 @@ __device__ __forceinline__ void grouped_int8_tile(
             if (loads && kt * kStep + kq >= k_dim)
 #pragma unroll
                 for (int i = 0; i < C::kALoads; ++i)
-                    *reinterpret_cast<i32x4*>(lds + (kt & 1) * C::kStage + (i * C::kLoadThreads + tid) * 16) = i32x4{0, 0, 0, 0};
+                    *reinterpret_cast<i32x4*>(lds + (kt & 1) * C::kStage + (i * C::kLoadThreads + tid) * 16) =
+                        i32x4{0, 0, 0, 0};
             lds_barrier();
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -408,7 +413,9 @@ __device__ __forceinline__ void grouped_int8_tile(
         constexpr int kCols = kPair ? C::BN : 2 * C::BN, kRowChunks = kCols / 8;
         constexpr int kWrap = kRowChunks < 16 ? kRowChunks : 16, kEach = 16 / kWrap;
         uint8_t* const stage = lds;
-        auto at = [](int row, int c) { return (row * kRowChunks + ((c / 8) ^ (row / kEach % kWrap))) * 16 + c % 8 * 2; };
+        auto at = [](int row, int c) {
+            return (row * kRowChunks + ((c / 8) ^ (row / kEach % kWrap))) * 16 + c % 8 * 2;
+        };
 #pragma unroll
         for (int half = 0; half < (kPair ? 1 : 2); ++half)
 #pragma unroll
@@ -433,7 +440,8 @@ __device__ __forceinline__ void grouped_int8_tile(
                             v[j] = static_cast<float>(q) * sa * sc1[j] * p;
                         }
                     }
-                    *reinterpret_cast<u32x2*>(stage + at(r, c)) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    *reinterpret_cast<u32x2*>(stage + at(r, c)) =
+                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
                 }
             }
         lds_barrier();
@@ -478,7 +486,8 @@ __device__ __forceinline__ void grouped_int8_tile(
             for (int i = 0; i < C::BM * C::BN / 4 / C::kThreads; ++i) {
                 const int s = i * C::kThreads + tid, row = s / (C::BN / 4), c = s % (C::BN / 4) * 4;
                 if (row < tr.rows && c < n)
-                    store_nt16(o + static_cast<int64_t>(tr.row0 + row) * n_dim + c0 + c, *reinterpret_cast<const u32x4*>(stage + at(row, c)));
+                    store_nt16(o + static_cast<int64_t>(tr.row0 + row) * n_dim + c0 + c,
+                               *reinterpret_cast<const u32x4*>(stage + at(row, c)));
             }
         }
     }
@@ -571,7 +580,8 @@ __global__ __launch_bounds__(64 * W) void grouped_int8_few_kernel(
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) rw[t][i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pw[t][i] + k));
+            for (int i = 0; i < 4; ++i)
+                rw[t][i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(pw[t][i] + k));
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const int ka = k0 + s * 64 + at < k_dim ? k0 + s * 64 + at : 0;
@@ -703,9 +713,9 @@ template <> struct Tiles<Out::kSwiglu> {
 };
 
 template <class C, Out kOut>
-int launch_tiles(const int8_t* a, const Rows& rows_of, int64_t tokens, const int8_t* w1, const float* s1, const int8_t* w2,
-                 const float* s2, const int32_t* offs, const float* probs, void* out, int64_t rows, int64_t k_dim,
-                 int64_t n_dim, int64_t experts, float limit, hipStream_t st) {
+int launch_tiles(const int8_t* a, const Rows& rows_of, int64_t tokens, const int8_t* w1, const float* s1,
+                 const int8_t* w2, const float* s2, const int32_t* offs, const float* probs, void* out, int64_t rows,
+                 int64_t k_dim, int64_t n_dim, int64_t experts, float limit, hipStream_t st) {
     int64_t n_tiles, n_blocks;
     const int64_t grid =
         grouped_grid(rows, n_dim, kOut == Out::kSwiglu ? C::BN : 2 * C::BN, experts, C::BM, &n_tiles, &n_blocks);

@@ -316,7 +316,8 @@ __global__ __launch_bounds__(L) void moe_combine_grad_kernel(
                                 if (!(mask >> (jj + q) & 1u)) continue;
 #pragma unroll
                                 for (int u = 0; u < kGradVecs; ++u)
-                                    er[q][u] = c0 + u * L < nvec ? E::load(in + at[jj + q], (c0 + u * L) * N) : typename E::Raw{};
+                                    er[q][u] = c0 + u * L < nvec ? E::load(in + at[jj + q], (c0 + u * L) * N)
+                                                                 : typename E::Raw{};
                             }
                         }
 #pragma unroll
@@ -539,7 +540,8 @@ extern "C" int moe_combine_weighted_bwd(const void* grad_out, int go_dtype, cons
         return MOE_EPI_ERR_MISALIGNED;
     const Range in[4] = {range_of(grad_out, n.token_bytes), range_of(expert_out, expert_out ? n.row_bytes : 0),
                          range_of(row_of, n.slot_bytes), range_of(weights, n.slot_bytes)},
-                gi = range_of(grad_expert_out, n.row_bytes), gw = range_of(grad_weights, grad_weights ? n.slot_bytes : 0);
+                gi = range_of(grad_expert_out, n.row_bytes),
+                gw = range_of(grad_weights, grad_weights ? n.slot_bytes : 0);
     for (const Range& r : in)
         if (overlaps(gi, r) || overlaps(gw, r)) return MOE_EPI_ERR_ALIAS;
     if (overlaps(gi, gw)) return MOE_EPI_ERR_ALIAS;

@@ -253,8 +253,9 @@ void launch_sort(const void* ids, int64_t first, int* offs, int* row_of, int* sl
     const Id* p = static_cast<const Id*>(ids);
     int* totals = nullptr;
     auto place = [&](int threads, auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(tiles), dim3(threads), threads / 64 * experts * static_cast<int>(sizeof(uint16_t)),
-                           st, p, hist, totals, offs, row_of, slot_of, slots, first, experts, bits_for(experts), tiles);
+        const int lds = threads / 64 * experts * static_cast<int>(sizeof(uint16_t));
+        hipLaunchKernelGGL(kernel, dim3(tiles), dim3(threads), lds, st, p, hist, totals, offs, row_of, slot_of,
+                           slots, first, experts, bits_for(experts), tiles);
     };
     if (slots <= 256 * kGroups) return place(256, moe_sort_place<Id, 256, false>);
     if (tiles == 1) return place(kTileThreads, moe_sort_place<Id, kTileThreads, false>);

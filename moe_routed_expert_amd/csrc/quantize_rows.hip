@@ -96,9 +96,10 @@ __device__ __forceinline__ u32x2 quantize8(const RowScale& s, const float (&x)[8
     u32x2 w;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const uint32_t a = __builtin_amdgcn_perm(__float_as_uint(t[4 * h + 1]), __float_as_uint(t[4 * h]), 0x0c0c0400u),
-                       b = __builtin_amdgcn_perm(__float_as_uint(t[4 * h + 3]), __float_as_uint(t[4 * h + 2]), 0x04000c0cu);
-        w[h] = a | b;
+        // the low byte of each, two at a time
+        auto bits = [&](int i) { return __float_as_uint(t[4 * h + i]); };
+        w[h] = __builtin_amdgcn_perm(bits(1), bits(0), 0x0c0c0400u) |
+               __builtin_amdgcn_perm(bits(3), bits(2), 0x04000c0cu);
     }
     return w;
 }
@@ -150,7 +151,8 @@ __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(const char* __res
             }
         };
 #pragma unroll
-        for (int k = 0; k < kVecs; ++k) raw[k] = lane + k * L < nvec ? X::load(row, (lane + k * L) * 8) : typename X::Raw{};
+        for (int k = 0; k < kVecs; ++k)
+            raw[k] = lane + k * L < nvec ? X::load(row, (lane + k * L) * 8) : typename X::Raw{};
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) grow(raw[k]);
         for (uint32_t c = lane + kVecs * L; c < nvec; c += L) grow(X::load(row, c * 8));

@@ -134,8 +134,9 @@ def moe_sort_fwd(expert_of, first_expert: int, offs, row_of, slot_of, workspace=
         ws = _take(workspace, "workspace", torch.uint8, None, dev)
     status = (_fns or _lib()).moe_sort_fwd(
         ids, 8 if wide else 4, first_expert, _take(offs, "offs", _I32, None, dev),
-        _take(row_of, "row_of", _I32, (tokens, top_k), dev), _take(slot_of, "slot_of", _I32, (tokens * top_k,), dev), ws,
-        nbytes, tokens, top_k, experts, _stream(dev, stream))
+        _take(row_of, "row_of", _I32, (tokens, top_k), dev),
+        _take(slot_of, "slot_of", _I32, (tokens * top_k,), dev), ws, nbytes, tokens, top_k, experts,
+        _stream(dev, stream))
     if status:
         _fail(status, "moe_sort_fwd")
 

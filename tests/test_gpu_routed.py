@@ -81,7 +81,8 @@ def check(got, want, slack, dtype, what):
     ok = np.isfinite(want)
     err = np.abs(got[ok] - want[ok])
     bound = slack[ok] + ref.rounding(dtype, np.abs(want[ok]) + slack[ok])
-    assert (err <= bound).all(), f"{what}: {int((err > bound).sum())} beyond the bound, worst {float((err / bound).max()):.3g}"
+    bad = int((err > bound).sum())
+    assert bad == 0, f"{what}: {bad} beyond the bound, worst {float((err / bound).max()):.3g}"
 
 
 # ---- order of the rows --------------------------------------------------------------
@@ -141,7 +142,8 @@ WIDTHS = [1, 2, 3, 7, 8, 12, 40, 1000, 1001, 1024, 2052, 4100, 7168, 9001, 16384
 @pytest.mark.parametrize("hidden", WIDTHS)
 def test_dispatch_and_its_gradient(dtype, hidden):
     rng = np.random.default_rng(hidden)
-    for tokens, top_k, experts, local, offset in ((1, 1, 1, 1, 0), (5, 3, 4, 4, 1), (37, 8, 16, 4, 0), (20, 2, 6, 3, 3)):
+    for tokens, top_k, experts, local, offset in ((1, 1, 1, 1, 0), (5, 3, 4, 4, 1), (37, 8, 16, 4, 0),
+                                                  (20, 2, 6, 3, 3)):
         _, offs, row_of, slot_of = route(rng, tokens, top_k, experts, local)
         rows = int(offs[-1])
         capacity = rows + 2                       # two rows without a slot
@@ -185,7 +187,8 @@ def test_dispatch_leaves_out_wrong_indices():
 @pytest.mark.parametrize("hidden", WIDTHS)
 def test_combine_and_its_gradients(dtype, out_dtype, hidden):
     rng = np.random.default_rng(hidden + 1)
-    for tokens, top_k, experts, local, offset in ((1, 1, 1, 1, 0), (9, 3, 4, 4, 1), (40, 8, 16, 4, 0), (6, 20, 24, 24, 0)):
+    for tokens, top_k, experts, local, offset in ((1, 1, 1, 1, 0), (9, 3, 4, 4, 1), (40, 8, 16, 4, 0),
+                                                  (6, 20, 24, 24, 0)):
         _, offs, row_of, _ = route(rng, tokens, top_k, experts, local)
         rows = int(offs[-1])
         x = placed(normal(rng, (rows, hidden), dtype), offset)
@@ -206,7 +209,8 @@ def test_combine_and_its_gradients(dtype, out_dtype, hidden):
         r = torch.from_numpy(row_of[t_of, j_of].astype(np.int64))
         product = w.cpu()[t_of, j_of][:, None] * g.float().cpu()[t_of]   # binary32
         assert torch.equal(bits(gr)[r], bits(product.to(dtype)))
-        assert np.abs(ref.f64(gr) - gr_w).max() <= ref.rounding(dtype, np.abs(gr_w).max() * (1 + 2 * ref.EPS)) + ref.EPS * np.abs(gr_w).max()
+        most = np.abs(gr_w).max()
+        assert np.abs(ref.f64(gr) - gr_w).max() <= ref.rounding(dtype, most * (1 + 2 * ref.EPS)) + ref.EPS * most
         check(gw, gw_w, (hidden + 8) * ref.EPS * scale, torch.float32, "grad_weights")
         # without a gradient of the weights: the same rows
         gr2 = sentinel((rows, hidden), dtype, offset)
@@ -304,7 +308,8 @@ def test_quantize_rows(dtype, cols):
 def test_quantize_ties_to_even_and_rows_that_are_not_finite():
     # 127 * 0.5 / 1 = 63.5 and its like: the integer is the even neighbour
     x = torch.tensor([[1.0, 0.5, -0.5, 0.25], [2.0, 1.0, -1.0, 0.0], [float("inf"), 1, 2, 3],
-                      [1, float("nan"), 2, 3], [-float("inf"), float("nan"), 0, 0]], device="cuda", dtype=torch.bfloat16)
+                      [1, float("nan"), 2, 3], [-float("inf"), float("nan"), 0, 0]], device="cuda",
+                     dtype=torch.bfloat16)
     q, scale = epi.quantize_rows_int8(x)
     assert q[0].tolist() == [127, 64, -64, 32] and q[1].tolist() == [127, 64, -64, 0]
     assert q[2:].abs().max() == 0 and bool(torch.isnan(scale[2:]).all()) and bool(torch.isfinite(scale[:2]).all())
@@ -323,7 +328,8 @@ def scales(rng, shape, size):
 # rows per expert, K, N: single rows, tiles of one row more or less, empty experts, short and odd K and N
 PRODUCTS = [([1], 16, 8), ([1], 128, 128), ([1, 0, 3], 48, 24), ([0, 16, 17, 0], 112, 136), ([5, 40, 2], 144, 264),
             ([64, 65, 1, 63], 256, 128), ([255, 256, 257], 272, 72), ([700], 128, 520), ([3, 130, 0, 200], 1040, 200),
-            ([2] * 33, 400, 40), ([0, 0, 0], 64, 16), ([129, 31, 33, 500], 2064, 48), ([0] * 30 + [100] + [3] * 70, 528, 56),
+            ([2] * 33, 400, 40), ([0, 0, 0], 64, 16), ([129, 31, 33, 500], 2064, 48),
+            ([0] * 30 + [100] + [3] * 70, 528, 56),
             ([1, 90, 0, 2, 7], 7184, 40)]
 # enough rows and columns for the small, the middle and the large tiles, partial ones among them; K below,
 # at and past one step and with odd numbers of steps
@@ -423,7 +429,8 @@ def test_offs_out_of_order_or_past_the_rows_are_clamped():
     for offs in ([20, 10, 500, 600], [-5, 0, 30, 50], [2 ** 31 - 1, 0, 0, 0]):
         out = sentinel((50, 16), torch.float32)
         epi.grouped_down_router_int8_fwd(h, sh, w, sw, ints(offs), None, out)
-        want, slack = ref.down(h.cpu().numpy(), sh.cpu().numpy(), w.cpu().numpy(), sw.cpu().numpy(), offs, np.ones(50, np.float32))
+        want, slack = ref.down(h.cpu().numpy(), sh.cpu().numpy(), w.cpu().numpy(), sw.cpu().numpy(), offs,
+                               np.ones(50, np.float32))
         check(out, want, slack, torch.float32, "down")
 
 

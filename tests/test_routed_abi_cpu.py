@@ -104,7 +104,8 @@ def test_combine(L):
     for g in (f, b):
         expect(g, SHAPE, *shapes)
     expect(f, NULLP, {"eo": None}, {"row": None}, {"w": None}, {"out": None})
-    expect(f, MISAL, {"eo": P[0] + 1}, {"row": P[1] + 2}, {"w": P[2] + 2}, {"out": P[3] + 1}, {"odt": 2, "out": P[3] + 2})
+    expect(f, MISAL, {"eo": P[0] + 1}, {"row": P[1] + 2}, {"w": P[2] + 2}, {"out": P[3] + 1},
+           {"odt": 2, "out": P[3] + 2})
     expect(f, ALIAS, {"out": P[0]}, {"out": P[1]}, {"out": P[2] + 4})
     expect(f, OK, {"tokens": 0})
     expect(b, NULLP, {"go": None}, {"eo": None}, {"row": None}, {"w": None}, {"ge": None})

@@ -15,13 +15,14 @@
 // wavefront, so no atomic operation is needed.
 //
 // Short calls are bound by their chain of reads, counts and writes, and a call
-// of up to 1024 or 4096 slots is one block (32 x 8 slots over 64 experts: 4.6
-// us, 5.1 with a block of 1024 threads; 1 x 8 over 256: 4.9). Longer ones
-// count tiles of 4096 slots first: two launches, 131072 x 8 slots over 8 local
-// experts 10.1 us, of which the 12 MB that are read and written need 2; with
-// more than 8192 counts a third launch sums them, since every block would
-// read them all (131072 x 8 over 256 experts 20.3 us against 40.2; 32768 x 8
-// over 128 experts, 8192 counts, 12.7 without it against 14.8).
+// of up to 1024 slots is one block (32 x 8 slots over 64 experts 2.9 us, 1 x 8
+// over 256 experts 3.8). Longer ones count tiles of slots first: two launches,
+// 131072 x 8 slots over 8 local experts 10.0 us, of which the 12 MB that are
+// read and written need 2; with more than 8192 counts a third launch sums them,
+// since every block would read them all (131072 x 8 over 256 experts 20.3 us
+// against 40.2; 32768 x 8 over 128, 8192 counts, 12.7 without it against 14.8).
+#include <type_traits>
+
 #include "epi_common.h"
 #include "moe_routed.h"
 
@@ -30,10 +31,10 @@ namespace {
 
 constexpr int kMaxExperts = 1024;
 constexpr int64_t kMaxSlotsPerToken = 1024;
-constexpr int kGroups = 4;                       // groups of 64 slots per wavefront of a tile
 constexpr int kTileThreads = 1024;
 constexpr int kTileWaves = kTileThreads / 64;
-constexpr int kTile = kTileThreads * kGroups;    // slots per block
+constexpr int kMostGroups = 4;                   // groups of 64 slots per wavefront of a tile, at most
+constexpr int64_t kTiles = 256;                  // tiles that a call aims at: one per CU
 constexpr int kDirect = 8;                       // counts per thread that a block reads of all tiles
 
 inline int bits_for(int64_t experts) {           // buckets 0 .. experts (experts: no row)
@@ -90,13 +91,13 @@ __device__ __forceinline__ int wave_scan(int* v, int n) {
 }
 
 // Counts of one tile's slots per bucket: hist[tile * experts + b].
-template <class Id>
+template <class Id, int kGroups>
 __global__ __launch_bounds__(kTileThreads) void moe_sort_count(const Id* __restrict__ ids, int* __restrict__ hist,
                                                                int64_t slots, int64_t first, int experts) {
     __shared__ int count[kMaxExperts];
     for (int e = threadIdx.x; e < experts; e += kTileThreads) count[e] = 0;
     __syncthreads();
-    const int64_t s0 = static_cast<int64_t>(blockIdx.x) * kTile + threadIdx.x;
+    const int64_t s0 = static_cast<int64_t>(blockIdx.x) * (kTileThreads * kGroups) + threadIdx.x;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
         const uint32_t b = bucket_of(ids, s0 + g * kTileThreads, slots, first, experts);
@@ -139,14 +140,14 @@ __global__ __launch_bounds__(kTileThreads) void moe_sort_scan(int* __restrict__ 
 // counts are the totals (kMany false: hist and totals are not read); of many,
 // hist holds every tile's counts, or, where totals are given, the slots of
 // earlier tiles (moe_sort_scan).
-template <class Id, int kThreads, bool kMany>
+template <class Id, int kThreads, int kGroups, bool kMany>
 __global__ __launch_bounds__(kThreads) void moe_sort_place(const Id* __restrict__ ids,
                                                            const int* __restrict__ hist,
                                                            const int* __restrict__ totals, int* __restrict__ offs,
                                                            int* __restrict__ row_of, int* __restrict__ slot_of,
                                                            int64_t slots, int64_t first, int experts, int nbits,
                                                            int tiles) {
-    // counts per wavefront and bucket (a tile has 4096 slots), earlier tiles' slots and start per bucket
+    // counts per wavefront and bucket (a tile has up to 4096 slots), earlier tiles' slots and start per bucket
     constexpr int kWaves = kThreads / 64;
     extern __shared__ uint16_t wave_count[];  // [kWaves][experts]
     __shared__ int before[kMaxExperts];
@@ -240,16 +241,32 @@ bool sizes_ok(int64_t tokens, int64_t top_k, int64_t experts) {
            tokens <= INT32_MAX / top_k;
 }
 
-int64_t tiles_of(int64_t slots) { return (slots + kTile - 1) / kTile; }
-
+// Groups per wavefront: the fewest that make no more than kTiles tiles. Each
+// group of a wavefront comes after the one before (32 x 8 slots over 64 experts
+// 2.9 us with one, 3.4 with two, 4.5 with four; 4096 x 8 slots 6.6, 7.7, 9.7),
+// but every tile adds counts that all others read (131072 x 8 slots over 8 local
+// experts 16.8, 10.8, 10.0).
+// Two groups give way to four where that spares the third launch (40000 x 8 slots
+// over 64 experts 13.2, 11.3).
+int64_t tiles_of(int64_t slots, int groups) {
+    const int64_t tile = kTileThreads * groups;
+    return (slots + tile - 1) / tile;
+}
 // Every block of moe_sort_place reads all counts, kDirect a thread, while they
 // are that few; beyond that a third launch sums them first.
 bool scans(int64_t tiles, int64_t experts) { return tiles * experts > kDirect * kTileThreads; }
 
+int groups_of(int64_t slots, int64_t experts) {
+    int g = 1;
+    while (g < kMostGroups && tiles_of(slots, g) > kTiles) g *= 2;
+    if (g == 2 && scans(tiles_of(slots, 2), experts) && !scans(tiles_of(slots, 4), experts)) g = 4;
+    return g;
+}
+
 template <class Id>
 void launch_sort(const void* ids, int64_t first, int* offs, int* row_of, int* slot_of, int* hist, int64_t slots,
                  int experts, hipStream_t st) {
-    const int tiles = static_cast<int>(tiles_of(slots));
+    const int groups = groups_of(slots, experts), tiles = static_cast<int>(tiles_of(slots, groups));
     const Id* p = static_cast<const Id*>(ids);
     int* totals = nullptr;
     auto place = [&](int threads, auto kernel) {
@@ -257,15 +274,24 @@ void launch_sort(const void* ids, int64_t first, int* offs, int* row_of, int* sl
         hipLaunchKernelGGL(kernel, dim3(tiles), dim3(threads), lds, st, p, hist, totals, offs, row_of, slot_of,
                            slots, first, experts, bits_for(experts), tiles);
     };
-    if (slots <= 256 * kGroups) return place(256, moe_sort_place<Id, 256, false>);
-    if (tiles == 1) return place(kTileThreads, moe_sort_place<Id, kTileThreads, false>);
-    hipLaunchKernelGGL((moe_sort_count<Id>), dim3(tiles), dim3(kTileThreads), 0, st, p, hist, slots, first, experts);
-    if (scans(tiles, experts)) {
-        totals = hist + static_cast<int64_t>(tiles) * experts;
-        hipLaunchKernelGGL(moe_sort_scan, dim3((experts + 63) / 64), dim3(kTileThreads), 0, st, hist, totals, tiles,
+    if (slots <= 256) return place(256, moe_sort_place<Id, 256, 1, false>);
+    if (tiles == 1) return place(kTileThreads, moe_sort_place<Id, kTileThreads, 1, false>);
+    auto many = [&](auto groups) {
+        constexpr int G = decltype(groups)::value;
+        hipLaunchKernelGGL((moe_sort_count<Id, G>), dim3(tiles), dim3(kTileThreads), 0, st, p, hist, slots, first,
                            experts);
+        if (scans(tiles, experts)) {
+            totals = hist + static_cast<int64_t>(tiles) * experts;
+            hipLaunchKernelGGL(moe_sort_scan, dim3((experts + 63) / 64), dim3(kTileThreads), 0, st, hist, totals,
+                               tiles, experts);
+        }
+        place(kTileThreads, moe_sort_place<Id, kTileThreads, G, true>);
+    };
+    switch (groups) {
+        case 1: return many(std::integral_constant<int, 1>());
+        case 2: return many(std::integral_constant<int, 2>());
+        default: return many(std::integral_constant<int, kMostGroups>());
     }
-    place(kTileThreads, moe_sort_place<Id, kTileThreads, true>);
 }
 
 }  // namespace
@@ -275,7 +301,7 @@ using namespace moe_epi;
 
 extern "C" int64_t moe_sort_workspace_bytes(int64_t tokens, int64_t top_k, int64_t experts) {
     if (!sizes_ok(tokens, top_k, experts)) return -1;
-    const int64_t tiles = tiles_of(tokens * top_k);
+    const int64_t slots = tokens * top_k, tiles = tiles_of(slots, groups_of(slots, experts));
     return tiles > 1 ? (tiles + 1) * experts * 4 : 0;
 }
 

@@ -15,8 +15,8 @@ plus allocating helpers (moe_sort, quantize_rows_int8) and torch.autograd.Functi
 stream of their device, and raises TypeError / ValueError for tensors the C ABI cannot take and
 MoeEpiError for a status other than success. There is no fallback.
 
-These calls are also made for single tokens, where a kernel runs for a few microseconds, so a
-tensor that is as expected passes one short test, and the message is formed only when it is not.
+These calls are also made for single tokens, where a kernel runs for a few microseconds, so each
+call tests all its tensors in one expression, and looks for the one to name only when that fails.
 """
 from __future__ import annotations
 
@@ -57,16 +57,13 @@ def _lib():
     return _fns
 
 
-def _take(t, name: str, dtype, shape, device: int) -> int:
-    """The address of a contiguous tensor of this dtype and shape (None: any) on this device; raises otherwise."""
-    if (t is not None and t.dtype is dtype and t.get_device() == device and t.is_contiguous()
-            and (shape is None or t.shape == shape)):
-        return t.data_ptr()
-    if t is None:
-        raise ValueError(f"{name} is required")
+def _refuse(device: int, *tensors) -> None:
+    """Say which of (tensor, name, dtype, shape) is not contiguous, of this dtype and shape (None: any) and on this
+    GPU. Called when a call's own short test of all its tensors has failed."""
     where = torch.device("cuda", device) if device >= 0 else torch.device("cuda")
-    binding._need(t, name, dtype, [t.shape if shape is None else shape], where)
-    raise ValueError(f"{name}: expected a tensor on {where}, got {t.device}")
+    for t, name, dtype, shape in tensors:
+        binding._need(t, name, dtype, [() if t is None else t.shape if shape is None else shape], where)
+    raise ValueError(f"expected tensors on {where}")
 
 
 def _code(t: torch.Tensor, name: str) -> int:
@@ -97,9 +94,16 @@ def _experts(w: torch.Tensor, name: str):
     return shape
 
 
+def _optional(t, name: str, dtype, rows: int, device: int):
+    """The address of a vector of `rows` values that may be left out (None)."""
+    if t is None:
+        return None
+    if not (t.dtype is dtype and t.get_device() == device and t.shape == (rows,) and t.is_contiguous()):
+        _refuse(device, (t, name, dtype, (rows,)))
+    return t.data_ptr()
+
+
 def _stream(device: int, stream) -> int:
-    if device < 0:
-        raise ValueError("expected tensors on a GPU")
     if stream is None:
         return _raw_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
@@ -125,18 +129,24 @@ def moe_sort_fwd(expert_of, first_expert: int, offs, row_of, slot_of, workspace=
     [tokens, top_k] the row of each slot or -1; slot_of int32 [tokens * top_k] the slot of each row, -1
     past the last; workspace uint8 of moe_sort_workspace_bytes, or None if that is 0."""
     tokens, top_k = _matrix(expert_of, "expert_of")
-    dev, wide = expert_of.get_device(), expert_of.dtype is _I64
-    experts = _vector(offs, "offs")
-    ids = _take(expert_of, "expert_of", _I64 if wide else _I32, None, dev)
+    dev, dt, experts = expert_of.get_device(), expert_of.dtype, _vector(offs, "offs")
+    if not (dev >= 0 and (dt is _I32 or dt is _I64) and expert_of.is_contiguous()
+            and offs.dtype is _I32 and offs.get_device() == dev and offs.is_contiguous()
+            and row_of is not None and row_of.dtype is _I32 and row_of.get_device() == dev
+            and row_of.shape == (tokens, top_k) and row_of.is_contiguous()
+            and slot_of is not None and slot_of.dtype is _I32 and slot_of.get_device() == dev
+            and slot_of.shape == (tokens * top_k,) and slot_of.is_contiguous()):
+        _refuse(dev, (expert_of, "expert_of", _I64 if dt is _I64 else _I32, None), (offs, "offs", _I32, None),
+                (row_of, "row_of", _I32, (tokens, top_k)), (slot_of, "slot_of", _I32, (tokens * top_k,)))
     ws, nbytes = None, 0
     if workspace is not None:
         nbytes = _vector(workspace, "workspace")
-        ws = _take(workspace, "workspace", torch.uint8, None, dev)
+        if not (workspace.dtype is torch.uint8 and workspace.get_device() == dev and workspace.is_contiguous()):
+            _refuse(dev, (workspace, "workspace", torch.uint8, None))
+        ws = workspace.data_ptr()
     status = (_fns or _lib()).moe_sort_fwd(
-        ids, 8 if wide else 4, first_expert, _take(offs, "offs", _I32, None, dev),
-        _take(row_of, "row_of", _I32, (tokens, top_k), dev),
-        _take(slot_of, "slot_of", _I32, (tokens * top_k,), dev), ws, nbytes, tokens, top_k, experts,
-        _stream(dev, stream))
+        expert_of.data_ptr(), 8 if dt is _I64 else 4, first_expert, offs.data_ptr(), row_of.data_ptr(),
+        slot_of.data_ptr(), ws, nbytes, tokens, top_k, experts, _stream(dev, stream))
     if status:
         _fail(status, "moe_sort_fwd")
 
@@ -160,9 +170,13 @@ def moe_dispatch_fwd(x, slot_of, top_k: int, out, stream=None) -> None:
     hidden], out [rows, hidden] of x's dtype (bf16, fp16 or fp32); slot_of int32 [rows]."""
     tokens, hidden = _matrix(x, "x")
     rows, dev, dt, code = _vector(slot_of, "slot_of"), x.get_device(), x.dtype, _code(x, "x")
-    status = (_fns or _lib()).moe_dispatch_fwd(
-        _take(x, "x", dt, None, dev), code, _take(slot_of, "slot_of", _I32, None, dev),
-        _take(out, "out", dt, (rows, hidden), dev), rows, tokens, top_k, hidden, _stream(dev, stream))
+    if not (dev >= 0 and x.is_contiguous()
+            and slot_of.dtype is _I32 and slot_of.get_device() == dev and slot_of.is_contiguous()
+            and out is not None and out.dtype is dt and out.get_device() == dev and out.shape == (rows, hidden)
+            and out.is_contiguous()):
+        _refuse(dev, (x, "x", dt, None), (slot_of, "slot_of", _I32, None), (out, "out", dt, (rows, hidden)))
+    status = (_fns or _lib()).moe_dispatch_fwd(x.data_ptr(), code, slot_of.data_ptr(), out.data_ptr(), rows, tokens,
+                                               top_k, hidden, _stream(dev, stream))
     if status:
         _fail(status, "moe_dispatch_fwd")
 
@@ -172,10 +186,15 @@ def moe_dispatch_bwd(grad_out, row_of, grad_x, stream=None) -> None:
     grad_out [rows, hidden], grad_x [tokens, hidden] of one dtype; row_of int32 [tokens, top_k]."""
     rows, hidden = _matrix(grad_out, "grad_out")
     tokens, top_k = _matrix(row_of, "row_of")
-    dev, dt, code = grad_x.get_device(), grad_out.dtype, _code(grad_out, "grad_out")
-    status = (_fns or _lib()).moe_dispatch_bwd(
-        _take(grad_out, "grad_out", dt, None, dev), code, _take(row_of, "row_of", _I32, None, dev),
-        _take(grad_x, "grad_x", dt, (tokens, hidden), dev), rows, tokens, top_k, hidden, _stream(dev, stream))
+    dev, dt, code = grad_out.get_device(), grad_out.dtype, _code(grad_out, "grad_out")
+    if not (dev >= 0 and grad_out.is_contiguous()
+            and row_of.dtype is _I32 and row_of.get_device() == dev and row_of.is_contiguous()
+            and grad_x is not None and grad_x.dtype is dt and grad_x.get_device() == dev
+            and grad_x.shape == (tokens, hidden) and grad_x.is_contiguous()):
+        _refuse(dev, (grad_out, "grad_out", dt, None), (row_of, "row_of", _I32, None),
+                (grad_x, "grad_x", dt, (tokens, hidden)))
+    status = (_fns or _lib()).moe_dispatch_bwd(grad_out.data_ptr(), code, row_of.data_ptr(), grad_x.data_ptr(), rows,
+                                               tokens, top_k, hidden, _stream(dev, stream))
     if status:
         _fail(status, "moe_dispatch_bwd")
 
@@ -186,12 +205,17 @@ def moe_combine_weighted_fwd(expert_out, row_of, weights, out, stream=None) -> N
     [tokens, top_k]; out [tokens, hidden] of expert_out's dtype or fp32."""
     rows, hidden = _matrix(expert_out, "expert_out")
     tokens, top_k = _matrix(row_of, "row_of")
-    dev, code, out_code = out.get_device(), _code(expert_out, "expert_out"), _code(out, "out")
+    dev, code, out_code = expert_out.get_device(), _code(expert_out, "expert_out"), _code(out, "out")
+    if not (dev >= 0 and expert_out.is_contiguous()
+            and row_of.dtype is _I32 and row_of.get_device() == dev and row_of.is_contiguous()
+            and weights is not None and weights.dtype is _F32 and weights.get_device() == dev
+            and weights.shape == (tokens, top_k) and weights.is_contiguous()
+            and out.get_device() == dev and out.shape == (tokens, hidden) and out.is_contiguous()):
+        _refuse(dev, (expert_out, "expert_out", expert_out.dtype, None), (row_of, "row_of", _I32, None),
+                (weights, "weights", _F32, (tokens, top_k)), (out, "out", out.dtype, (tokens, hidden)))
     status = (_fns or _lib()).moe_combine_weighted_fwd(
-        _take(expert_out, "expert_out", expert_out.dtype, None, dev), code,
-        _take(row_of, "row_of", _I32, None, dev), _take(weights, "weights", _F32, (tokens, top_k), dev),
-        _take(out, "out", out.dtype, (tokens, hidden), dev), out_code, rows, tokens, top_k, hidden,
-        _stream(dev, stream))
+        expert_out.data_ptr(), code, row_of.data_ptr(), weights.data_ptr(), out.data_ptr(), out_code, rows, tokens,
+        top_k, hidden, _stream(dev, stream))
     if status:
         _fail(status, "moe_combine_weighted_fwd")
 
@@ -204,16 +228,27 @@ def moe_combine_weighted_bwd(grad_out, expert_out, row_of, weights, grad_expert_
     tokens, hidden = _matrix(grad_out, "grad_out")
     top_k = _matrix(row_of, "row_of")[1]
     rows, dt, dev = _matrix(grad_expert_out, "grad_expert_out")[0], grad_expert_out.dtype, grad_out.get_device()
-    code, grad_code, eo, gw = _code(grad_expert_out, "grad_expert_out"), _code(grad_out, "grad_out"), None, None
+    code, grad_code, slots = _code(grad_expert_out, "grad_expert_out"), _code(grad_out, "grad_out"), (tokens, top_k)
+    if not (dev >= 0 and grad_out.is_contiguous()
+            and row_of.dtype is _I32 and row_of.get_device() == dev and row_of.shape == slots
+            and row_of.is_contiguous()
+            and weights is not None and weights.dtype is _F32 and weights.get_device() == dev
+            and weights.shape == slots and weights.is_contiguous()
+            and grad_expert_out.get_device() == dev and grad_expert_out.shape == (rows, hidden)
+            and grad_expert_out.is_contiguous()):
+        _refuse(dev, (grad_out, "grad_out", grad_out.dtype, None), (row_of, "row_of", _I32, slots),
+                (weights, "weights", _F32, slots), (grad_expert_out, "grad_expert_out", dt, (rows, hidden)))
+    eo = gw = None
     if grad_weights is not None:
-        eo = _take(expert_out, "expert_out", dt, (rows, hidden), dev)
-        gw = _take(grad_weights, "grad_weights", _F32, (tokens, top_k), dev)
+        if not (expert_out is not None and expert_out.dtype is dt and expert_out.get_device() == dev
+                and expert_out.shape == (rows, hidden) and expert_out.is_contiguous()
+                and grad_weights.dtype is _F32 and grad_weights.get_device() == dev
+                and grad_weights.shape == slots and grad_weights.is_contiguous()):
+            _refuse(dev, (expert_out, "expert_out", dt, (rows, hidden)), (grad_weights, "grad_weights", _F32, slots))
+        eo, gw = expert_out.data_ptr(), grad_weights.data_ptr()
     status = (_fns or _lib()).moe_combine_weighted_bwd(
-        _take(grad_out, "grad_out", grad_out.dtype, None, dev), grad_code, eo, code,
-        _take(row_of, "row_of", _I32, (tokens, top_k), dev),
-        _take(weights, "weights", _F32, (tokens, top_k), dev),
-        _take(grad_expert_out, "grad_expert_out", dt, (rows, hidden), dev), gw, rows, tokens, top_k, hidden,
-        _stream(dev, stream))
+        grad_out.data_ptr(), grad_code, eo, code, row_of.data_ptr(), weights.data_ptr(), grad_expert_out.data_ptr(),
+        gw, rows, tokens, top_k, hidden, _stream(dev, stream))
     if status:
         _fail(status, "moe_combine_weighted_bwd")
 
@@ -269,9 +304,14 @@ def quantize_rows_int8_fwd(x, q, scale, stream=None) -> None:
     q int8 [rows, cols]; scale fp32 [rows]."""
     rows, cols = _matrix(x, "x")
     dev, code = x.get_device(), _code(x, "x")
-    status = (_fns or _lib()).quantize_rows_int8_fwd(
-        _take(x, "x", x.dtype, None, dev), code, _take(q, "q", _I8, (rows, cols), dev),
-        _take(scale, "scale", _F32, (rows,), dev), rows, cols, _stream(dev, stream))
+    if not (dev >= 0 and x.is_contiguous()
+            and q is not None and q.dtype is _I8 and q.get_device() == dev and q.shape == (rows, cols)
+            and q.is_contiguous()
+            and scale is not None and scale.dtype is _F32 and scale.get_device() == dev and scale.shape == (rows,)
+            and scale.is_contiguous()):
+        _refuse(dev, (x, "x", x.dtype, None), (q, "q", _I8, (rows, cols)), (scale, "scale", _F32, (rows,)))
+    status = (_fns or _lib()).quantize_rows_int8_fwd(x.data_ptr(), code, q.data_ptr(), scale.data_ptr(), rows, cols,
+                                                     _stream(dev, stream))
     if status:
         _fail(status, "quantize_rows_int8_fwd")
 
@@ -293,17 +333,30 @@ def grouped_gate_up_swiglu_int8_fwd(a, a_scale, slot_of, top_k: int, w_gate, w_g
     inter]; offs int32 [experts] cumulative row counts (on the device); probs fp32 [rows] or None for 1;
     y bf16 [rows, inter]."""
     tokens, hidden = _matrix(a, "a")
-    experts, inter, _ = _experts(w_gate, "w_gate")
-    rows, dev = _matrix(y, "y")[0], a.get_device()
+    weight = experts, inter, _ = _experts(w_gate, "w_gate")
+    rows, dev, channels = _matrix(y, "y")[0], a.get_device(), (experts, inter)
+    if not (dev >= 0 and a.dtype is _I8 and a.is_contiguous()
+            and a_scale is not None and a_scale.dtype is _F32 and a_scale.get_device() == dev
+            and a_scale.shape == (tokens,) and a_scale.is_contiguous()
+            and w_gate.dtype is _I8 and w_gate.get_device() == dev and weight[2] == hidden and w_gate.is_contiguous()
+            and w_up is not None and w_up.dtype is _I8 and w_up.get_device() == dev and w_up.shape == weight
+            and w_up.is_contiguous()
+            and w_gate_scale is not None and w_gate_scale.dtype is _F32 and w_gate_scale.get_device() == dev
+            and w_gate_scale.shape == channels and w_gate_scale.is_contiguous()
+            and w_up_scale is not None and w_up_scale.dtype is _F32 and w_up_scale.get_device() == dev
+            and w_up_scale.shape == channels and w_up_scale.is_contiguous()
+            and offs is not None and offs.dtype is _I32 and offs.get_device() == dev and offs.shape == (experts,)
+            and offs.is_contiguous()
+            and y.dtype is _BF16 and y.get_device() == dev and y.shape == (rows, inter) and y.is_contiguous()):
+        weight = (experts, inter, hidden)
+        _refuse(dev, (a, "a", _I8, None), (a_scale, "a_scale", _F32, (tokens,)), (w_gate, "w_gate", _I8, weight),
+                (w_gate_scale, "w_gate_scale", _F32, channels), (w_up, "w_up", _I8, weight),
+                (w_up_scale, "w_up_scale", _F32, channels), (offs, "offs", _I32, (experts,)),
+                (y, "y", _BF16, (rows, inter)))
     status = (_fns or _lib()).grouped_gate_up_swiglu_int8_fwd(
-        _take(a, "a", _I8, None, dev), _take(a_scale, "a_scale", _F32, (tokens,), dev),
-        None if slot_of is None else _take(slot_of, "slot_of", _I32, (rows,), dev),
-        _take(w_gate, "w_gate", _I8, (experts, inter, hidden), dev),
-        _take(w_gate_scale, "w_gate_scale", _F32, (experts, inter), dev),
-        _take(w_up, "w_up", _I8, (experts, inter, hidden), dev),
-        _take(w_up_scale, "w_up_scale", _F32, (experts, inter), dev), _take(offs, "offs", _I32, (experts,), dev),
-        None if probs is None else _take(probs, "probs", _F32, (rows,), dev),
-        _take(y, "y", _BF16, (rows, inter), dev), rows, tokens, top_k, hidden, inter, experts, limit,
+        a.data_ptr(), a_scale.data_ptr(), _optional(slot_of, "slot_of", _I32, rows, dev), w_gate.data_ptr(),
+        w_gate_scale.data_ptr(), w_up.data_ptr(), w_up_scale.data_ptr(), offs.data_ptr(),
+        _optional(probs, "probs", _F32, rows, dev), y.data_ptr(), rows, tokens, top_k, hidden, inter, experts, limit,
         _stream(dev, stream))
     if status:
         _fail(status, "grouped_gate_up_swiglu_int8_fwd")
@@ -315,16 +368,26 @@ def grouped_down_router_int8_fwd(h, h_scale, w_down, w_down_scale, offs, probs, 
     [experts] cumulative row counts (on the device); probs fp32 [rows] or None for 1; out [rows, hidden]
     bf16 or fp32."""
     rows, inter = _matrix(h, "h")
-    experts, hidden, _ = _experts(w_down, "w_down")
+    weight = experts, hidden, _ = _experts(w_down, "w_down")
     dev = h.get_device()
     if out.dtype is not _BF16 and out.dtype is not _F32:
         raise TypeError(f"out: expected bfloat16 or float32, got {out.dtype}")
+    if not (dev >= 0 and h.dtype is _I8 and h.is_contiguous()
+            and h_scale is not None and h_scale.dtype is _F32 and h_scale.get_device() == dev
+            and h_scale.shape == (rows,) and h_scale.is_contiguous()
+            and w_down.dtype is _I8 and w_down.get_device() == dev and weight[2] == inter and w_down.is_contiguous()
+            and w_down_scale is not None and w_down_scale.dtype is _F32 and w_down_scale.get_device() == dev
+            and w_down_scale.shape == (experts, hidden) and w_down_scale.is_contiguous()
+            and offs is not None and offs.dtype is _I32 and offs.get_device() == dev and offs.shape == (experts,)
+            and offs.is_contiguous()
+            and out.get_device() == dev and out.shape == (rows, hidden) and out.is_contiguous()):
+        _refuse(dev, (h, "h", _I8, None), (h_scale, "h_scale", _F32, (rows,)),
+                (w_down, "w_down", _I8, (experts, hidden, inter)),
+                (w_down_scale, "w_down_scale", _F32, (experts, hidden)), (offs, "offs", _I32, (experts,)),
+                (out, "out", out.dtype, (rows, hidden)))
     status = (_fns or _lib()).grouped_down_router_int8_fwd(
-        _take(h, "h", _I8, None, dev), _take(h_scale, "h_scale", _F32, (rows,), dev),
-        _take(w_down, "w_down", _I8, (experts, hidden, inter), dev),
-        _take(w_down_scale, "w_down_scale", _F32, (experts, hidden), dev), _take(offs, "offs", _I32, (experts,), dev),
-        None if probs is None else _take(probs, "probs", _F32, (rows,), dev),
-        _take(out, "out", out.dtype, (rows, hidden), dev), DTYPE_CODE[out.dtype], rows, inter, hidden, experts,
-        _stream(dev, stream))
+        h.data_ptr(), h_scale.data_ptr(), w_down.data_ptr(), w_down_scale.data_ptr(), offs.data_ptr(),
+        _optional(probs, "probs", _F32, rows, dev), out.data_ptr(), DTYPE_CODE[out.dtype], rows, inter, hidden,
+        experts, _stream(dev, stream))
     if status:
         _fail(status, "grouped_down_router_int8_fwd")

@@ -189,3 +189,90 @@ def test_header_and_binding_name_the_same_calls(L):
     assert len(names) == 9
     for name in names:
         assert getattr(L, name).argtypes is not None and hasattr(routed, name)
+
+
+class Tensor:
+    """What the binding asks of a tensor, on GPU 0 unless told otherwise."""
+
+    def __init__(self, shape, dtype, device=0, contiguous=True):
+        self.shape, self.dtype, self.index, self.contiguous = torch.Size(shape), dtype, device, contiguous
+
+    device = property(lambda self: torch.device("cuda", self.index) if self.index >= 0 else torch.device("cpu"))
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def data_ptr(self):
+        return 4096
+
+
+I32, F32, I8, BF16 = torch.int32, torch.float32, torch.int8, torch.bfloat16
+# call -> (its tensors, in order, and the other arguments by position)
+TENSORS = {
+    "moe_sort_fwd": ([((6, 2), I32), ((4,), I32), ((6, 2), I32), ((12,), I32), ((64,), torch.uint8)], {1: 0}),
+    "moe_dispatch_fwd": ([((6, 16), BF16), ((12,), I32), ((12, 16), BF16)], {2: 2}),
+    "moe_dispatch_bwd": ([((12, 16), BF16), ((6, 2), I32), ((6, 16), BF16)], {}),
+    "moe_combine_weighted_fwd": ([((12, 16), BF16), ((6, 2), I32), ((6, 2), F32), ((6, 16), BF16)], {}),
+    "moe_combine_weighted_bwd": ([((6, 16), BF16), ((12, 16), BF16), ((6, 2), I32), ((6, 2), F32), ((12, 16), BF16),
+                                  ((6, 2), F32)], {}),
+    "quantize_rows_int8_fwd": ([((6, 16), BF16), ((6, 16), I8), ((6,), F32)], {}),
+    "grouped_gate_up_swiglu_int8_fwd": ([((6, 16), I8), ((6,), F32), ((12,), I32), ((4, 8, 16), I8), ((4, 8), F32),
+                                         ((4, 8, 16), I8), ((4, 8), F32), ((4,), I32), ((12,), F32), ((12, 8), BF16)],
+                                        {3: 2, 11: 7.0}),
+    "grouped_down_router_int8_fwd": ([((12, 8), I8), ((12,), F32), ((4, 16, 8), I8), ((4, 16), F32), ((4,), I32),
+                                      ((12,), F32), ((12, 16), BF16)], {}),
+}
+# sizes that only the tensor itself has: experts and workspace of the sort, tokens that rows are taken from, rows
+# that are summed, slots of a token
+FREE = {("moe_sort_fwd", 1, 0), ("moe_sort_fwd", 4, 0), ("moe_dispatch_fwd", 0, 0), ("moe_dispatch_bwd", 0, 0),
+        ("moe_dispatch_bwd", 1, 1), ("moe_combine_weighted_fwd", 0, 0)}
+
+
+@pytest.mark.parametrize("name", sorted(TENSORS))
+def test_binding_passes_only_tensors_that_fit(name, monkeypatch):
+    reached = []
+
+    class Library:
+        def __getattr__(self, call):
+            return lambda *args: reached.append((call, args)) or 0
+
+    monkeypatch.setattr(routed, "_fns", Library())
+    monkeypatch.setattr(routed, "_raw_stream", lambda device: 0)
+    specs, others = TENSORS[name]
+
+    def call(tensors):
+        args = list(tensors)
+        for at in sorted(others):
+            args.insert(at, others[at])
+        getattr(routed, name)(*args)
+
+    def made():
+        return [Tensor(*s) for s in specs]
+
+    call(made())
+    assert [c for c, _ in reached] == [name]
+    assert all(a == 4096 for a in reached[0][1] if isinstance(a, int) and a > 1000)
+    for i, (shape, dtype) in enumerate(specs):
+        wrong = [Tensor(shape, torch.float64), Tensor(shape, dtype, device=1), Tensor(shape, dtype, device=-1),
+                 Tensor(shape, dtype, contiguous=False), Tensor(shape + (1,), dtype)]
+        wrong += [Tensor(shape[:d] + (shape[d] + 1,) + shape[d + 1:], dtype) for d in range(len(shape))
+                  if (name, i, d) not in FREE]
+        for bad in wrong:
+            tensors = made()
+            tensors[i] = bad
+            with pytest.raises((TypeError, ValueError)):
+                call(tensors)
+                raise AssertionError(f"{name}: tensor {i} passed with {bad.shape} {bad.dtype} {bad.device} "
+                                     f"contiguous={bad.contiguous}")
+    tensors = made()
+    for t in tensors:
+        t.index = -1                               # all of them on the CPU
+    with pytest.raises((TypeError, ValueError)):
+        call(tensors)
+    assert len(reached) == 1                       # the library was never reached again

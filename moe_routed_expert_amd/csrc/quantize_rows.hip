@@ -72,6 +72,7 @@ struct RowScale {
         mul = 127.0f * m;
         den = most == 0 ? 1.0f : __uint_as_float(most) * m;
         near = mul / den;
+        if (!(near < __uint_as_float(0x7F800000u))) near = 0.0f;  // max|x| below 2^-121: every element is divided
         scale = finite ? __uint_as_float(most) / 127.0f : __uint_as_float(0x7FC00000u);
     }
 };

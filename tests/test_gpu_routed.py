@@ -271,6 +271,34 @@ def test_combine_with_infinities_and_nans():
     assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_calls_with_no_rows_or_no_tokens(dtype):
+    """No row here: sums and gradients of zeros. No token: nothing is written."""
+    none, x = torch.empty((0, 40), dtype=dtype, device="cuda"), torch.ones((5, 40), dtype=dtype, device="cuda")
+    row_of, weights = ints(np.full((5, 3), -1)), torch.ones((5, 3), device="cuda")
+    for call in (lambda o: epi.moe_dispatch_bwd(none, row_of, o),
+                 lambda o: epi.moe_combine_weighted_fwd(none, row_of, weights, o)):
+        out = sentinel((5, 40), dtype)
+        call(out)
+        assert bool((out == 0).all())
+    grad_weights = sentinel((5, 3), torch.float32)
+    epi.moe_combine_weighted_bwd(x, none, row_of, weights, none, grad_weights)
+    assert bool((grad_weights == 0).all())
+    epi.moe_dispatch_fwd(x, ints([]), 3, none)
+    out = sentinel((4, 40), dtype)
+    epi.moe_dispatch_fwd(none, ints([0, 1, -1, 5]), 3, out)
+    assert bool((out == 0).all())
+    q, scale = epi.quantize_rows_int8(none)
+    assert q.shape == (0, 40) and scale.shape == (0,)
+    no_slots = torch.empty((0, 3), dtype=torch.int32, device="cuda")
+    epi.moe_dispatch_bwd(x, no_slots, none)
+    epi.moe_combine_weighted_fwd(x, no_slots, weights[:0], none)
+    xg, wg = x.clone().requires_grad_(), weights.clone().requires_grad_()
+    rows = epi.MoeDispatch.apply(xg, row_of, ints([]))
+    epi.MoeCombineWeighted.apply(rows, row_of, wg).sum().backward()
+    assert bool((xg.grad == 0).all()) and bool((wg.grad == 0).all())
+
+
 # ---- 8-bit rows ---------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", DTYPES)

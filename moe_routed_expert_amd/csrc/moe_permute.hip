@@ -269,10 +269,12 @@ constexpr int kGradRows = 2;  // rows whose loads are in flight together
 
 // L lanes per token: its gradient is read once for up to kSlotChunk slots,
 // each of their rows is read and its gradient written in the same pass, and
-// the products' partial sums stay in one register per slot. Rows of up to 256
-// vectors take a wavefront, wider ones four. 65536 tokens of 7168 bf16, about
-// one row each: 432 us, 5.8 TB/s (one vector at a time 450; 2 vectors a lane
-// 445; 448 lanes of 2, an exact fit, 483; default-policy stores 448).
+// the products' partial sums stay in one register per slot. Lanes by the row's
+// vectors, four each, up to 256 lanes. 65536 tokens of 7168 bf16, about one row
+// each: 432 us, 5.8 TB/s (128 lanes 456, 64 476; one vector at a time 450; 2
+// vectors a lane 445; 448 lanes of 2, an exact fit, 483; default-policy stores
+// 448; 4 instead of 5 blocks per CU 459, registers for 6 wavefronts a SIMD 470);
+// of 4096: 262 us (256 lanes 281, 64 271).
 template <int TG, int TE, int N, int L, bool kDot, bool kAligned>
 __global__ __launch_bounds__(L) void moe_combine_grad_kernel(
     const char* __restrict__ grad, const char* __restrict__ in, const int32_t* __restrict__ row_of,
@@ -371,6 +373,178 @@ __global__ __launch_bounds__(L) void moe_combine_grad_kernel(
     }
 }
 
+// ---- narrow rows --------------------------------------------------------------------------
+//
+// A row of up to 32 vectors leaves most lanes of a wavefront idle, and the
+// kernels above are then bound by the wavefronts they start. Here 2^gs lanes
+// (8, 16 or 32) take a row or token, so that a wavefront takes 8, 4 or 2. The
+// slots' indices differ between the lanes' groups and are read by the lanes.
+// bf16 rows of 64 / 128 / 256, us with these and with the kernels above:
+// dispatch of 262144 rows 10.6 / 20.3 / 39.3 against 57 / 58 / 58; sums of 4
+// rows for 131072 tokens 16.6 / 30.5 / 56 against 92 / 93 / 94; their gradients
+// 31 / 60 / 116 against 177 / 184 / 201.
+
+constexpr int kNarrowLanes = 256;
+constexpr int64_t kNarrowVecs = 32;
+constexpr int kNarrowRows = 4;  // rows whose loads are in flight together
+
+inline int group_shift(int64_t nvec) { return nvec > 16 ? 5 : (nvec > 8 ? 4 : 3); }
+
+template <int kAlign>
+__global__ __launch_bounds__(kNarrowLanes) void moe_dispatch_narrow_kernel(const char* __restrict__ x,
+                                                                           const int32_t* __restrict__ slot_of,
+                                                                           char* __restrict__ out, int64_t rows,
+                                                                           int64_t slots, uint32_t top_k,
+                                                                           int row_bytes, int gs) {
+    typedef typename Word<16, kAlign>::type Piece;
+    const int group = static_cast<int>(threadIdx.x) >> gs, lane = static_cast<int>(threadIdx.x) & ((1 << gs) - 1);
+    const int64_t per = kNarrowLanes >> gs;
+    const int pieces = row_bytes / 16, done = pieces * 16, left = (row_bytes - done) / 2;
+    for (int64_t b = blockIdx.x; b * per * kNarrowRows < rows; b += gridDim.x) {
+        int32_t slot[kNarrowRows];
+        u32x4 v[kNarrowRows];
+        uint16_t v1[kNarrowRows];
+#pragma unroll
+        for (int k = 0; k < kNarrowRows; ++k) {
+            const int64_t r = (b * kNarrowRows + k) * per + group;
+            slot[k] = r < rows ? slot_of[r] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kNarrowRows; ++k) {
+            v[k] = u32x4{0u, 0u, 0u, 0u};
+            v1[k] = 0;
+            if (slot[k] < 0 || slot[k] >= slots) continue;
+            const char* src = x + static_cast<int64_t>(static_cast<uint32_t>(slot[k]) / top_k) * row_bytes;
+            if (lane < pieces) v[k] = *reinterpret_cast<const Piece*>(src + lane * 16);
+            if (kAlign < 16 && lane < left) v1[k] = *reinterpret_cast<const uint16_t*>(src + done + 2 * lane);
+        }
+#pragma unroll
+        for (int k = 0; k < kNarrowRows; ++k) {
+            const int64_t r = (b * kNarrowRows + k) * per + group;
+            if (r >= rows) continue;
+            char* dst = out + r * row_bytes;
+            if (lane < pieces) store_word<16, kAlign>(dst + lane * 16, v[k]);
+            if (kAlign < 16 && lane < left) *reinterpret_cast<uint16_t*>(dst + done + 2 * lane) = v1[k];
+        }
+    }
+}
+
+template <int TI, int TO, int N, bool kWeighted, bool kAligned>
+__global__ __launch_bounds__(kNarrowLanes) void moe_row_sum_narrow_kernel(
+    const char* __restrict__ in, const int32_t* __restrict__ row_of, const float* __restrict__ weights,
+    char* __restrict__ out, int64_t rows, int64_t tokens, int64_t top_k, int hidden, int gs) {
+    typedef Vec<TI, N, kAligned> In;
+    typedef Vec<TO, N, kAligned> Out;
+    const int group = static_cast<int>(threadIdx.x) >> gs, lane = static_cast<int>(threadIdx.x) & ((1 << gs) - 1);
+    const int64_t per = kNarrowLanes >> gs;
+    const int nvec = hidden / N, done = nvec * N;
+    const bool full = lane < nvec, tail = !kAligned && lane < hidden - done;
+    for (int64_t t0 = blockIdx.x * per; t0 < tokens; t0 += gridDim.x * per) {
+        const int64_t t = t0 + group;
+        if (t >= tokens) continue;
+        float acc[N] = {};
+        float acc1 = 0.0f;
+        for (int64_t j0 = 0; j0 < top_k; j0 += kNarrowRows) {
+            int32_t r[kNarrowRows];
+            float w[kNarrowRows], v1[kNarrowRows];
+            typename In::Raw v[kNarrowRows];
+#pragma unroll
+            for (int q = 0; q < kNarrowRows; ++q) {
+                r[q] = j0 + q < top_k ? row_of[t * top_k + j0 + q] : -1;
+                w[q] = kWeighted && j0 + q < top_k ? weights[t * top_k + j0 + q] : 1.0f;
+            }
+#pragma unroll
+            for (int q = 0; q < kNarrowRows; ++q) {
+                v[q] = typename In::Raw{};
+                v1[q] = 0.0f;
+                if (r[q] < 0 || r[q] >= rows) continue;
+                const char* row = in + static_cast<int64_t>(r[q]) * hidden * kBytesOf<TI>;
+                if (full) v[q] = In::load(row, lane * N);
+                if (tail) v1[q] = Elem<TI>::load1(row, done + lane);
+            }
+#pragma unroll
+            for (int q = 0; q < kNarrowRows; ++q) {
+                if (r[q] < 0 || r[q] >= rows) continue;
+                float f[N];
+                In::widen(v[q], f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc[i] = kWeighted ? __fmaf_rn(w[q], f[i], acc[i]) : acc[i] + f[i];
+                acc1 = kWeighted ? __fmaf_rn(w[q], v1[q], acc1) : acc1 + v1[q];
+            }
+        }
+        char* orow = out + t * hidden * kBytesOf<TO>;
+        if (full) Out::store(orow, lane * N, acc);
+        if (tail) Elem<TO>::store1(orow, done + lane, acc1);
+    }
+}
+
+template <int TG, int TE, int N, bool kDot, bool kAligned>
+__global__ __launch_bounds__(kNarrowLanes) void moe_combine_grad_narrow_kernel(
+    const char* __restrict__ grad, const char* __restrict__ in, const int32_t* __restrict__ row_of,
+    const float* __restrict__ weights, char* __restrict__ grad_in, float* __restrict__ grad_w, int64_t rows,
+    int64_t tokens, int64_t top_k, int hidden, int gs) {
+    typedef Vec<TG, N, kAligned> G;
+    typedef Vec<TE, N, kAligned> E;
+    const int group = static_cast<int>(threadIdx.x) >> gs, lane = static_cast<int>(threadIdx.x) & ((1 << gs) - 1);
+    const int64_t per = kNarrowLanes >> gs;
+    const int nvec = hidden / N, done = nvec * N;
+    const bool full = lane < nvec, tail = !kAligned && lane < hidden - done;
+    for (int64_t t0 = blockIdx.x * per; t0 < tokens; t0 += gridDim.x * per) {
+        const int64_t t = t0 + group;
+        if (t >= tokens) continue;
+        const char* grow = grad + t * hidden * kBytesOf<TG>;
+        float g[N], g1 = 0.0f;
+        typename G::Raw raw{};
+        if (full) raw = G::load(grow, lane * N);
+        if (tail) g1 = Elem<TG>::load1(grow, done + lane);
+        G::widen(raw, g);
+        for (int64_t j0 = 0; j0 < top_k; j0 += kNarrowRows) {
+            int32_t r[kNarrowRows];
+            float w[kNarrowRows], v1[kNarrowRows];
+            typename E::Raw v[kNarrowRows];
+#pragma unroll
+            for (int q = 0; q < kNarrowRows; ++q) {
+                r[q] = j0 + q < top_k ? row_of[t * top_k + j0 + q] : -1;
+                w[q] = j0 + q < top_k ? weights[t * top_k + j0 + q] : 0.0f;
+            }
+#pragma unroll
+            for (int q = 0; q < kNarrowRows; ++q) {
+                v[q] = typename E::Raw{};
+                v1[q] = 0.0f;
+                if (!kDot || r[q] < 0 || r[q] >= rows) continue;
+                const char* row = in + static_cast<int64_t>(r[q]) * hidden * kBytesOf<TE>;
+                if (full) v[q] = E::load(row, lane * N);
+                if (tail) v1[q] = Elem<TE>::load1(row, done + lane);
+            }
+#pragma unroll
+            for (int q = 0; q < kNarrowRows; ++q) {
+                const bool has = r[q] >= 0 && r[q] < rows;
+                if (has) {
+                    char* row = grad_in + static_cast<int64_t>(r[q]) * hidden * kBytesOf<TE>;
+                    float o[N];
+#pragma unroll
+                    for (int i = 0; i < N; ++i) o[i] = w[q] * g[i];
+                    if (full) E::store(row, lane * N, o);
+                    if (tail) Elem<TE>::store1(row, done + lane, w[q] * g1);
+                }
+                if constexpr (kDot) {
+                    if (j0 + q >= top_k) continue;
+                    float dot = 0.0f;
+                    if (has) {
+                        float f[N];
+                        E::widen(v[q], f);
+                        dot = g1 * v1[q];
+#pragma unroll
+                        for (int i = 0; i < N; ++i) dot = __fmaf_rn(g[i], f[i], dot);
+                    }
+                    for (int off = (1 << gs) / 2; off > 0; off >>= 1) dot += __shfl_xor(dot, off, 64);
+                    if (lane == 0) grad_w[t * top_k + j0 + q] = has ? dot : 0.0f;
+                }
+            }
+        }
+    }
+}
+
 // ---- launches ------------------------------------------------------------------------
 
 template <int TI, int TO, bool kWeighted>
@@ -384,7 +558,15 @@ int launch_sum(const void* in, const int32_t* row_of, const float* weights, void
     const char* i = static_cast<const char*>(in);
     char* o = static_cast<char*>(out);
     (void)hipGetLastError();
-    if (fit)
+    if (nvec <= kNarrowVecs) {
+        const int gs = group_shift(nvec);
+        auto go = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3(grid_for_rows(tokens, kNarrowLanes >> gs)), dim3(kNarrowLanes), 0, st, i,
+                               row_of, weights, o, rows, tokens, top_k, static_cast<int>(hidden), gs);
+        };
+        fit ? go(moe_row_sum_narrow_kernel<TI, TO, N, kWeighted, true>)
+            : go(moe_row_sum_narrow_kernel<TI, TO, N, kWeighted, false>);
+    } else if (fit)
         hipLaunchKernelGGL((moe_row_sum_kernel<TI, TO, N, kWeighted, true>), grid, block, 0, st, i, row_of, weights, o,
                            rows, tokens, top_k, hidden, static_cast<uint32_t>(nseg));
     else
@@ -399,7 +581,6 @@ int launch_grad(const void* grad, const void* in, const int32_t* row_of, const f
     constexpr int N = TG == MOE_EPI_F32 || TE == MOE_EPI_F32 ? 4 : 8;
     const bool fit = hidden % N == 0 && aligned(grad, N * kBytesOf<TG>) && aligned(in, N * kBytesOf<TE>) &&
                      aligned(grad_in, N * kBytesOf<TE>);
-    const bool wide = hidden / N > 64 * kGradVecs;
     const dim3 grid(grid_for_rows(tokens, 1));
     auto go = [&](int lanes, auto kernel) {
         hipLaunchKernelGGL(kernel, grid, dim3(lanes), 0, st, static_cast<const char*>(grad),
@@ -418,10 +599,26 @@ int launch_grad(const void* grad, const void* in, const int32_t* row_of, const f
             go(L, moe_combine_grad_kernel<TG, TE, N, L, false, false>);
     };
     (void)hipGetLastError();
-    if (wide)
-        pick(std::integral_constant<int, 256>());
-    else
+    const int64_t nvec = hidden / N;
+    if (nvec <= kNarrowVecs) {
+        const int gs = group_shift(nvec);
+        auto narrow = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3(grid_for_rows(tokens, kNarrowLanes >> gs)), dim3(kNarrowLanes), 0, st,
+                               static_cast<const char*>(grad), static_cast<const char*>(in), row_of, weights,
+                               static_cast<char*>(grad_in), grad_w, rows, tokens, top_k, static_cast<int>(hidden), gs);
+        };
+        if (grad_w)
+            fit ? narrow(moe_combine_grad_narrow_kernel<TG, TE, N, true, true>)
+                : narrow(moe_combine_grad_narrow_kernel<TG, TE, N, true, false>);
+        else
+            fit ? narrow(moe_combine_grad_narrow_kernel<TG, TE, N, false, true>)
+                : narrow(moe_combine_grad_narrow_kernel<TG, TE, N, false, false>);
+    } else if (nvec <= 64 * kGradVecs)
         pick(std::integral_constant<int, 64>());
+    else if (nvec <= 128 * kGradVecs)
+        pick(std::integral_constant<int, 128>());
+    else
+        pick(std::integral_constant<int, 256>());
     return launch_status();
 }
 
@@ -462,10 +659,23 @@ extern "C" int moe_dispatch_fwd(const void* x, int dtype, const int32_t* slot_of
                            static_cast<char*>(out), rows, tokens * top_k, static_cast<uint32_t>(top_k), bytes,
                            static_cast<uint32_t>(nseg));
     };
+    auto narrow = [&](auto kernel) {
+        const int gs = group_shift(bytes / 16);
+        hipLaunchKernelGGL(kernel, dim3(grid_for_rows(rows, (kNarrowLanes >> gs) * kNarrowRows)), dim3(kNarrowLanes), 0,
+                           as_stream(stream), static_cast<const char*>(x), slot_of, static_cast<char*>(out), rows,
+                           tokens * top_k, static_cast<uint32_t>(top_k), static_cast<int>(bytes), gs);
+    };
+    const bool sixteen = bytes % 16 == 0 && aligned(x, 16) && aligned(out, 16),
+               four = bytes % 4 == 0 && aligned(x, 4) && aligned(out, 4);
     (void)hipGetLastError();
-    if (bytes % 16 == 0 && aligned(x, 16) && aligned(out, 16))
+    if (bytes / 16 <= kNarrowVecs) {
+        if (sixteen)
+            narrow(moe_dispatch_narrow_kernel<16>);
+        else
+            four ? narrow(moe_dispatch_narrow_kernel<4>) : narrow(moe_dispatch_narrow_kernel<2>);
+    } else if (sixteen)
         again ? go(moe_dispatch_kernel<16, 2>) : go(moe_dispatch_kernel<16, 1>);
-    else if (bytes % 4 == 0 && aligned(x, 4) && aligned(out, 4))
+    else if (four)
         again ? go(moe_dispatch_kernel<4, 2>) : go(moe_dispatch_kernel<4, 1>);
     else
         again ? go(moe_dispatch_kernel<2, 2>) : go(moe_dispatch_kernel<2, 1>);

@@ -16,9 +16,13 @@
 // reciprocal instead, and takes the remainder: where it shows that the nearest
 // integer is within 0.4999, that is what the rounded quotient gives too;
 // vectors with an element nearer to a tie are divided. The bits are the same
-// and the times 109 us (6.4 TB/s) and 63 us (6.3 TB/s). With 64, 128 or 512
-// lanes a row of 7168 takes 120, 109 or 139 us; a row of 2048 64 with 64
-// lanes, 66 with 128.
+// and the times 109 us (6.4 TB/s) and 63 us (6.3 TB/s).
+//
+// A row takes the fewest lanes that hold it, four vectors each: 65536 rows of
+// 256 13 us with 16 lanes, 19 with 32, 30 with 64; of 512 20, 25, 35; of 1024
+// 35 with 32, 45 with 64; 32768 of 7168 109 with 256 lanes, 139 with 512.
+#include <type_traits>
+
 #include "epi_common.h"
 #include "moe_routed.h"
 
@@ -108,7 +112,7 @@ __device__ __forceinline__ u32x2 quantize8(const RowScale& s, const float (&x)[8
 template <int L>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part) {
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
+    for (int off = (L < 64 ? L : 64) / 2; off > 0; off >>= 1) {
         const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), off, 64));
         v = o > v ? o : v;
     }
@@ -123,7 +127,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part) {
     return v;
 }
 
-// L lanes per row (64: a wavefront; 256: the block).
+// L lanes per row: part of a wavefront, a wavefront, half of the block or the block.
 template <int T, int L, bool kAligned>
 __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(const char* __restrict__ x, int8_t* __restrict__ q,
                                                                float* __restrict__ scale, int64_t rows,
@@ -188,16 +192,26 @@ __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(const char* __res
 template <int T>
 void launch_quantize(const void* x, int8_t* q, float* scale, int64_t rows, int64_t cols, hipStream_t st) {
     const bool fit = cols % 8 == 0 && aligned(x, 16) && aligned(q, 8);
-    // a wavefront holds 2048 elements; wider rows take the block
-    const bool wave = cols <= 64 * 8 * kVecs;
-    const dim3 block(kBlock), grid(grid_for_rows(rows, wave ? kBlock / 64 : 1));
-    auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, block, 0, st, static_cast<const char*>(x), q, scale, rows, cols);
+    // the fewest lanes that hold a row, from 16 (512 elements) to the block (8192; wider rows are read again)
+    auto go = [&](auto lanes) {
+        constexpr int L = decltype(lanes)::value;
+        const dim3 block(kBlock), grid(grid_for_rows(rows, kBlock / L));
+        auto launch = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, grid, block, 0, st, static_cast<const char*>(x), q, scale, rows, cols);
+        };
+        fit ? launch(quantize_rows_kernel<T, L, true>) : launch(quantize_rows_kernel<T, L, false>);
     };
-    if (wave)
-        fit ? go(quantize_rows_kernel<T, 64, true>) : go(quantize_rows_kernel<T, 64, false>);
+    const int64_t lanes = (cols + 8 * kVecs - 1) / (8 * kVecs);
+    if (lanes <= 16)
+        go(std::integral_constant<int, 16>());
+    else if (lanes <= 32)
+        go(std::integral_constant<int, 32>());
+    else if (lanes <= 64)
+        go(std::integral_constant<int, 64>());
+    else if (lanes <= 128)
+        go(std::integral_constant<int, 128>());
     else
-        fit ? go(quantize_rows_kernel<T, kBlock, true>) : go(quantize_rows_kernel<T, kBlock, false>);
+        go(std::integral_constant<int, kBlock>());
 }
 
 }  // namespace

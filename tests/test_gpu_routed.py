@@ -302,7 +302,8 @@ def test_calls_with_no_rows_or_no_tokens(dtype):
 # ---- 8-bit rows ---------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("cols", [1, 7, 8, 16, 520, 1001, 2048, 2049, 2056, 7168, 8192, 8200, 20001])
+@pytest.mark.parametrize("cols", [1, 7, 8, 16, 500, 512, 513, 520, 1001, 1024, 1032, 2048, 2049, 2056, 4096, 4099, 4104, 7168,
+                                  8192, 8200, 20001])
 def test_quantize_rows(dtype, cols):
     rng = np.random.default_rng(cols)
     rows = 23

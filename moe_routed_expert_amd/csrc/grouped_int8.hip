@@ -19,9 +19,12 @@
 //               along K: a row of a tile is then 128 bytes, eight 16-byte
 //               chunks, XOR-swizzled so that a fragment read (one chunk of each
 //               of 16 rows) takes 16 different bank groups. Memory goes
-//               straight to LDS in two stages; the next stage's loads are in
-//               flight while this one's products run. 64 x 64 and 128 x 64
-//               tiles share a CU and fill each other's waits;
+//               straight to LDS in two or three stages; the next stages' loads
+//               are in flight while this one's products run. Blocks of 64 x 64
+//               and 128 x 64 tiles fill each other's waits where a CU has
+//               several; where it has about one, the third stage does (gate_up
+//               as below, 48 rows an expert 58.9 -> 44.2 us, 64 rows 62.5 ->
+//               47.1), which with several would keep some of them out;
 //   large tiles 256 x 128 x 2, eight wavefronts of 64 x 64 x 2, 128
 //               accumulators a lane, one block per CU, with the loop written
 //               out so that fragment reads and loads go between the matrix
@@ -42,7 +45,14 @@
 //               against four: gate_up 1609 / 1641, down 947 / 940; row tiles
 //               per group: gate_up 1: 1691, 2: 1641, 4: 1648, 8: 1689; down 8:
 //               977, 16: 972, 32: 983, 128: 1002; steps of 64 with two blocks
-//               per CU (128 x 128 x 2 or 256 x 64 x 2): gate_up 1935, down 1099.
+//               per CU (128 x 128 x 2 or 256 x 64 x 2): gate_up 1935, down 1099;
+//               blocks that stay for several tiles and load the next one's first
+//               step under the stores: gate_up 1570 against 1591, down 989
+//               against 932 (registers spill, and the loads wait for the stores);
+//               output stored from registers, without LDS: 1580 against 1591,
+//               957 against 932.
+#include <type_traits>
+
 #include "epi_common.h"
 #include "grouped_map.h"
 #include "moe_routed.h"
@@ -75,11 +85,11 @@ struct Rows {
 enum class Out { kSwiglu, kBf16, kF32 };
 
 // BM rows and BN columns of each weight by WM x WN wavefronts; GM row tiles to
-// a group of the tile order; kLoadWaves wavefronts load; kRoll: the main loop
-// that keeps one block per CU busy (below), otherwise the plain one.
-template <int BM_, int BN_, int WM_, int WN_, int GM_, int LW_, bool kRoll_>
+// a group of the tile order; kLoadWaves wavefronts load; S stages of LDS; kRoll:
+// the main loop that keeps one block per CU busy (below), otherwise the plain one.
+template <int BM_, int BN_, int WM_, int WN_, int GM_, int LW_, int S_, bool kRoll_>
 struct Tile {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, GM = GM_, kLoadWaves = LW_;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, GM = GM_, kLoadWaves = LW_, S = S_;
     static constexpr bool kRoll = kRoll_;
     static constexpr int kThreads = 64 * WM * WN;
     static constexpr int MI = BM / (16 * WM), NI = BN / (16 * WN);
@@ -89,8 +99,9 @@ struct Tile {
     static constexpr int kLoads = kALoads + 2 * kWLoads;  // of a step, per loading wavefront
     static constexpr int kMfmas = 2 * MI * NI;            // of a sub-step of 64
     static constexpr int kEvery = kMfmas / kLoads;        // matrix instructions per load
-    static constexpr int kLds = 2 * kStage;
+    static constexpr int kLds = S * kStage;
     static_assert(BM * BN * 4 <= kLds, "a staged output tile fits: both halves in bf16, one in float32");
+    static_assert(S == 2 || (!kRoll && S == 3 && kLoadWaves == WM * WN), "stages of the two loops");
     static_assert(BM + 2 * BN <= kThreads, "a thread per row and per column of the scales");
     static_assert(kALoads >= 1 && kWLoads >= 1 && BM * kChunks % kLoadThreads == 0 && BN * kChunks % kLoadThreads == 0,
                   "whole chunks per lane");
@@ -108,9 +119,11 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// This wavefront's loads and LDS accesses are done, then the block meets.
+// This wavefront's loads but the last kLeft and its LDS accesses are done, then the block meets.
+template <int kLeft>
 __device__ __forceinline__ void stage_barrier() {
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    static_assert(kLeft < 64, "vmcnt has six bits");
+    __builtin_amdgcn_s_waitcnt((kLeft & 0xF) | 0x0070 | (kLeft >> 4) << 14);  // vmcnt(kLeft) lgkmcnt(0)
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -252,7 +265,7 @@ __device__ __forceinline__ void grouped_int8_tile(
     const int nk = (k_dim + kStep - 1) / kStep;
     const int last = k_dim % kStep ? nk - 1 : -1;  // the step that crosses, if one does
     auto issue_one = [&](int kt, int i) {
-        uint8_t* st = lds + (kt & 1) * C::kStage;
+        uint8_t* st = lds + static_cast<unsigned>(kt) % C::S * C::kStage;
         int k = kt * kStep, more = 0;
         if (kt == last) {
             more = k + kq < k_dim ? k : -kq;
@@ -283,17 +296,18 @@ __device__ __forceinline__ void grouped_int8_tile(
 #pragma unroll
             for (int i = 0; i < C::kLoads; ++i) issue_one(kt, i);
     };
-    // Step kt has landed and nobody reads the other stage any more. In the step
-    // that crosses the end of K the rows' chunks past it are cleared, so that
-    // whatever the weights hold there counts 0.
-    auto meet = [&](int kt) {
-        stage_barrier();
+    // Step kt has landed (`left` later loads may be on their way) and nobody reads
+    // the stage of the step before any more. In the step that crosses the end of K
+    // the rows' chunks past it are cleared, so that whatever the weights hold there
+    // counts 0.
+    auto meet = [&](int kt, auto left) {
+        stage_barrier<decltype(left)::value>();
         if (kt == last) {
+            uint8_t* const st = lds + static_cast<unsigned>(kt) % C::S * C::kStage;
             if (loads && kt * kStep + kq >= k_dim)
 #pragma unroll
                 for (int i = 0; i < C::kALoads; ++i)
-                    *reinterpret_cast<i32x4*>(lds + (kt & 1) * C::kStage + (i * C::kLoadThreads + tid) * 16) =
-                        i32x4{0, 0, 0, 0};
+                    *reinterpret_cast<i32x4*>(st + (i * C::kLoadThreads + tid) * 16) = i32x4{0, 0, 0, 0};
             lds_barrier();
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -343,6 +357,7 @@ __device__ __forceinline__ void grouped_int8_tile(
         }
     };
 
+    const std::integral_constant<int, 0> none;
     if constexpr (C::kRoll) {
         // From the middle of one step to the middle of the next: after the barrier the
         // next step is complete and this one's stage is free, so the step after next
@@ -350,18 +365,14 @@ __device__ __forceinline__ void grouped_int8_tile(
         issue(0);
         if (nk > 1) {
             issue(1);
-            __builtin_amdgcn_s_waitcnt((C::kLoads & 0xF) | 0x0070 | (C::kLoads >> 4) << 14);  // step 0 has landed
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_sched_barrier(0);
+            stage_barrier<C::kLoads>();  // not the step that crosses the end of K
         } else {
-            meet(0);
+            meet(0, none);
         }
 #pragma unroll
         for (int i = 0; i < C::kMfmas; ++i) reads_after(i, lds, 0);
         substep(lds, 1);
-        meet(1);
+        meet(1, none);
         for (int kt = 0; kt + 1 < nk; ++kt) {
             const uint8_t* next = lds + ((kt + 1) & 1) * C::kStage;
 #pragma unroll
@@ -373,20 +384,26 @@ __device__ __forceinline__ void grouped_int8_tile(
                 __builtin_amdgcn_sched_barrier(0);
             }
             substep(next, 1);
-            meet(kt + 2);
+            meet(kt + 2, none);
         }
 #pragma unroll
         for (int i = 0; i < C::kMfmas; ++i) mfma(i);
         __builtin_amdgcn_sched_barrier(0);
     } else {
-        // Several blocks share a CU and fill each other's waits.
-        issue(0);
+        // S - 1 steps are on their way; few rows give too few blocks to fill each
+        // other's waits.
+#pragma unroll
+        for (int i = 0; i < C::S - 1; ++i)
+            if (i < nk) issue(i);
         for (int kt = 0; kt < nk; ++kt) {
-            meet(kt);
-            if (kt + 1 < nk) issue(kt + 1);
+            if (C::S > 2 && kt + 1 < nk)
+                meet(kt, std::integral_constant<int, (C::S - 2) * C::kLoads>());
+            else
+                meet(kt, none);
+            if (kt + C::S - 1 < nk) issue(kt + C::S - 1);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-                const uint8_t* st = lds + (kt & 1) * C::kStage;
+                const uint8_t* const st = lds + static_cast<unsigned>(kt) % C::S * C::kStage;
 #pragma unroll
                 for (int mi = 0; mi < MI; ++mi) read_a(st, kk, mi);
 #pragma unroll
@@ -702,16 +719,15 @@ int launch_few(const int8_t* a, const Rows& rows_of, const int8_t* w1, const flo
 // ---- launches ------------------------------------------------------------------------
 
 // Three tile sizes. The large one has the fewest bytes per product and takes a
-// CU by itself; the smaller ones give few rows more blocks, several to a CU.
+// CU by itself; the smaller ones give few rows more blocks. The middle one has
+// two stages where several blocks share a CU, and three where there is about
+// one block per CU, so that more of the weights are on their way.
 template <Out kOut> struct Tiles {
-    typedef Tile<256, 128, 4, 2, 16, 4, true> Large;
-    typedef Tile<128, 64, 2, 2, 16, 4, false> Middle;
-    typedef Tile<64, 64, 2, 2, 16, 4, false> Small;
-};
-template <> struct Tiles<Out::kSwiglu> {
-    typedef Tile<256, 128, 4, 2, 2, 8, true> Large;
-    typedef Tile<128, 64, 2, 2, 2, 4, false> Middle;
-    typedef Tile<64, 64, 2, 2, 2, 4, false> Small;
+    static constexpr int kGroup = kOut == Out::kSwiglu ? 2 : 16;  // row tiles per group of the tile order
+    typedef Tile<256, 128, 4, 2, kGroup, kOut == Out::kSwiglu ? 8 : 4, 2, true> Large;
+    typedef Tile<128, 64, 2, 2, kGroup, 4, 2, false> Middle;
+    typedef Tile<128, 64, 2, 2, kGroup, 4, 3, false> MiddleDeep;
+    typedef Tile<64, 64, 2, 2, kGroup, 4, 3, false> Small;
 };
 
 template <class C, Out kOut>
@@ -750,27 +766,34 @@ int launch_int8(const int8_t* a, const Rows& rows_of, int64_t tokens, const int8
     // tile reads the weights fewer times, a smaller one wastes fewer rows of a
     // partial tile; and a tile size is taken only where it gives half of the CUs
     // a block. Measured (us, 8 experts, gate_up 7168 -> 2 x 2048 / down 2048 ->
-    // 7168, few rows by 16 / by 32, small, middle, large tiles):
-    //   8 rows an expert   39.2/19.8  41.1/20.9  64.3/25.5  68.5/26.8  96.0/36.6
-    //   24                 71.6/32.4  49.8/25.5  64.7/29.7  68.6/28.9  95.5/36.8
-    //   48                            96.4/47.5  60.3/32.7  64.1/29.5  96.0/37.6
-    //   96                             169/77.5  71.6/49.6  65.5/33.5  96.1/64.4
-    //   192                            291/140    121/76.4  81.2/51.1   101/42.3
-    //   256                            378/185    125/89.0   126/73.7   108/72.7
+    // 7168; few rows by 16 and by 32, small, middle, middle with three stages,
+    // large):
+    //   rows an expert  16          32          small       middle      deep        large
+    //     8             39.2/19.8   41.1/20.9   43/24       63/26       46/30       96/34
+    //    16             56.5/26.4   42.7/23.0   43.0/24.3   63.2/26.6   45.6/30.4   94.9/34.3
+    //    24             71.6/32.4   49.1/25.6   43.5/24.1   64.8/27.3   46.3/31.0   95.1/34.4
+    //    48                         96.9/47.7   44.2/25.9   62.1/27.4   47.1/40.9   94.1/34.8
+    //    64                          112/59.5   65.2/41.1   62.5/27.1   47.1/31.1   93.9/35.6
+    //    96                          168/77.1   69.7/40.0   63.9/29.4   49.4/31.8   95.3/57.8
+    //   128                          211/99.4   85.0/55.9   76.5/49.9   83.0/56.8   94.6/39.1
+    //   192                          291/142     101/67.3   78.2/53.2   85.8/57.5   99.3/38.1
+    //   256                          378/185     124/84.5    126/74.5    119/84.8    106/66.5
     // and where the grid is small (4 experts, 1024 -> 2 x 512):
-    //   100                6.6        6.7         9.8        10.1       19.7
-    //   400                15.6       15.4       10.2        12.1       20.9
-    //   1500               43.1       37.5       15.9        15.1       21.5
-    auto fills = [&](int bm, int cols) { return (rows / bm + experts / 2) * ((n_dim + cols - 1) / cols) >= 128; };
+    //   100              6.6         6.7         8.2        10.3        10.3        18.9
+    //   400             15.6        15.1         8.6        11.4        11.1        19.7
+    //  1500             43.1        37.3        17.0        14.0        20.4        20.3
+    auto grid_of = [&](int bm, int cols) { return (rows / bm + experts / 2) * ((n_dim + cols - 1) / cols); };
     constexpr int kCols = kOut == Out::kSwiglu ? 1 : 2;  // column ranges of a tile
     typedef typename Tiles<kOut>::Large Large;
     typedef typename Tiles<kOut>::Middle Middle;
     typedef typename Tiles<kOut>::Small Small;
+    const int64_t middle = grid_of(Middle::BM, kCols * Middle::BN);
     if (rows <= 10 * experts) return few(launch_few<1, kOut>);
-    if (rows <= 24 * experts || !fills(Small::BM, kCols * Small::BN)) return few(launch_few<2, kOut>);
-    if (rows <= 56 * experts || !fills(Middle::BM, kCols * Middle::BN)) return tiles(launch_tiles<Small, kOut>);
-    if (rows <= (kCols == 1 ? 192 : 112) * experts || !fills(Large::BM, kCols * Large::BN))
-        return tiles(launch_tiles<Middle, kOut>);
+    if (rows <= 18 * experts || grid_of(Small::BM, kCols * Small::BN) < 128) return few(launch_few<2, kOut>);
+    if (rows <= 56 * experts || middle < 128) return tiles(launch_tiles<Small, kOut>);
+    if (rows <= (kCols == 1 ? 192 : 112) * experts || grid_of(Large::BM, kCols * Large::BN) < 128)
+        return middle <= 320 ? tiles(launch_tiles<typename Tiles<kOut>::MiddleDeep, kOut>)
+                             : tiles(launch_tiles<Middle, kOut>);
     return tiles(launch_tiles<Large, kOut>);
 }
 
@@ -812,8 +835,8 @@ extern "C" int grouped_gate_up_swiglu_int8_fwd(const int8_t* a, const float* a_s
                            range_of(w_up_scale, sb), range_of(offs, ob), range_of(probs, probs ? rb : 0)})
         if (overlaps(ry, r)) return MOE_EPI_ERR_ALIAS;
     const Rows rows_of{a_scale, slot_of, static_cast<uint32_t>(top_k), tokens * top_k};
-    return launch_int8<Out::kSwiglu>(a, rows_of, tokens, w_gate, w_gate_scale, w_up, w_up_scale, offs, probs, y,
-                                                 rows, hidden, inter, experts, limit, as_stream(stream));
+    return launch_int8<Out::kSwiglu>(a, rows_of, tokens, w_gate, w_gate_scale, w_up, w_up_scale, offs, probs, y, rows,
+                                     hidden, inter, experts, limit, as_stream(stream));
 }
 
 extern "C" int grouped_down_router_int8_fwd(const int8_t* h, const float* h_scale, const int8_t* w_down,
@@ -839,8 +862,8 @@ extern "C" int grouped_down_router_int8_fwd(const int8_t* h, const float* h_scal
     const Rows rows_of{h_scale, nullptr, 1u, rows};
     const hipStream_t st = as_stream(stream);
     if (out_dtype == MOE_EPI_F32)
-        return launch_int8<Out::kF32>(h, rows_of, rows, w_down, w_down_scale, w_down, w_down_scale, offs, probs,
-                                                out, rows, inter, hidden, experts, 1.0f, st);
-    return launch_int8<Out::kBf16>(h, rows_of, rows, w_down, w_down_scale, w_down, w_down_scale, offs, probs, out,
-                                             rows, inter, hidden, experts, 1.0f, st);
+        return launch_int8<Out::kF32>(h, rows_of, rows, w_down, w_down_scale, w_down, w_down_scale, offs, probs, out,
+                                      rows, inter, hidden, experts, 1.0f, st);
+    return launch_int8<Out::kBf16>(h, rows_of, rows, w_down, w_down_scale, w_down, w_down_scale, offs, probs, out, rows,
+                                   inter, hidden, experts, 1.0f, st);
 }

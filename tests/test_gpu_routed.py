@@ -302,8 +302,8 @@ def test_calls_with_no_rows_or_no_tokens(dtype):
 # ---- 8-bit rows ---------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("cols", [1, 7, 8, 16, 500, 512, 513, 520, 1001, 1024, 1032, 2048, 2049, 2056, 4096, 4099, 4104, 7168,
-                                  8192, 8200, 20001])
+@pytest.mark.parametrize("cols", [1, 7, 8, 16, 500, 512, 513, 520, 1001, 1024, 1032, 2048, 2049, 2056, 4096, 4099, 4104,
+                                  7168, 8192, 8200, 20001])
 def test_quantize_rows(dtype, cols):
     rng = np.random.default_rng(cols)
     rows = 23
@@ -364,6 +364,7 @@ PRODUCTS = [([1], 16, 8), ([1], 128, 128), ([1, 0, 3], 48, 24), ([0, 16, 17, 0],
 # at and past one step and with odd numbers of steps
 PRODUCTS += [(counts * 7, k, n) for counts, n in (([30, 0, 25, 31, 64, 17], 520), ([100, 128, 1, 0, 140, 129], 520),
                                                   ([300, 256, 257, 1, 512, 0], 776)) for k in (16, 112, 128, 272, 384)]
+PRODUCTS += [([100, 128, 1, 0, 140, 129] * 7, k, n) for n in (264, 1032) for k in (16, 256, 272, 640)]
 
 
 @pytest.mark.parametrize("counts,k,n", PRODUCTS)

@@ -46,6 +46,9 @@
 //               per group: gate_up 1: 1691, 2: 1641, 4: 1648, 8: 1689; down 8:
 //               977, 16: 972, 32: 983, 128: 1002; steps of 64 with two blocks
 //               per CU (128 x 128 x 2 or 256 x 64 x 2): gate_up 1935, down 1099;
+//               128 x 128 x 2 in steps of 128 with three stages 1933 / 1141 (and
+//               at 128 rows an expert, gate_up 69 against 76 for the tiles above,
+//               down 46 against 35);
 //               blocks that stay for several tiles and load the next one's first
 //               step under the stores: gate_up 1570 against 1591, down 989
 //               against 932 (registers spill, and the loads wait for the stores);

@@ -27,7 +27,7 @@ namespace moe_epi {
 namespace {
 
 constexpr int64_t kMaxTopK = 1024;
-constexpr int kSlotChunk = 8;  // slots taken together: their indices are read at once
+constexpr int kSlotChunk = 8;  // slots taken together: their indices are read at once, a lane each
 
 // ---- N elements of storage type T at element `e` of a row --------------------------
 
@@ -51,7 +51,7 @@ MOE_WORD(8, u32x2, 2)
 
 // Aligned words are streamed (nontemporal); words at the element's alignment
 // share cache lines with their neighbours, whose loads should find them: a
-// weighted sum of 30021 rows of 1001 float16 22.2 -> 19.8 us.
+// weighted sum of 30021 rows of 1001 float16 22.2 -> 19.8 us (18.1 now).
 template <int kBytes, int kAlign>
 __device__ __forceinline__ typename Word<kBytes, kAlign>::plain load_word(const void* p) {
     const typename Word<kBytes, kAlign>::type* w = static_cast<const typename Word<kBytes, kAlign>::type*>(p);
@@ -162,21 +162,29 @@ __global__ __launch_bounds__(kCopyLanes) void moe_dispatch_kernel(const char* __
 // ---- sums over a token's rows ------------------------------------------------------
 
 constexpr int kSumLanes = 64;
-constexpr int kSumVecs = 2;  // vectors per lane of a segment
-constexpr int kSumRows = 4;  // rows whose loads are in flight together
 
-// One wavefront per (token, segment). Measured (us): 8 rows a token, 32768
-// tokens of 2048 bf16 206, 5.9 TB/s (128 lanes 214; one vector a lane with 8
-// rows in flight 203); about one row a token, 131072 of 7168 bf16 610, 6.2
-// TB/s (637; 964); float32 rows, 65536 of 7168, 600 (606; 953). The slots' rows and weights are the same
-// for the whole block (scalar loads); those with a row are kept as a bit mask
-// and taken in ascending order, kSumRows at a time.
-template <int TI, int TO, int N, bool kWeighted, bool kAligned>
+// One wavefront per (token, segment of kSumLanes * kVecs vectors), with 8 / kVecs
+// rows' loads in flight together. Its slots' rows and weights are read by a lane
+// each, so that a call of few tokens waits once for them and not once a slot
+// (sums of 8 rows for 32 tokens of 7168 bf16 4.9 -> 4.1 us on the GPU), those
+// with a row are kept as a bit mask and taken in ascending order.
+//
+// Two vectors a lane and four rows stream best. Measured (us): 8 rows a token,
+// 32768 tokens of 2048 bf16 204, 5.9 TB/s (128 lanes 214; one vector and 8 rows
+// 203); about one row a token, 131072 of 7168 bf16 602, 6.2 TB/s (637; 964);
+// float32 rows, 65536 of 7168, 600 (606; 953). Where tokens have several rows
+// and the call has fewer wavefronts than the chip holds at once, the waits set
+// the time, and one vector a lane with eight rows in flight is faster: 1, 32,
+// 64 and 128 tokens of 7168 2.9, 3.5, 3.9, 4.8 us against 3.3, 4.1, 4.5, 5.6;
+// 256 tokens 7.2 against 7.0; 512 of 2048 5.1 against 5.9, 1024 8.0 against 7.6;
+// with about one row a token 128 of 7168 3.6 against 3.2.
+template <int TI, int TO, int N, int kVecs, bool kWeighted, bool kAligned>
 __global__ __launch_bounds__(kSumLanes) void moe_row_sum_kernel(const char* __restrict__ in,
                                                                 const int32_t* __restrict__ row_of,
                                                                 const float* __restrict__ weights,
                                                                 char* __restrict__ out, int64_t rows, int64_t tokens,
                                                                 int64_t top_k, int64_t hidden, uint32_t nseg) {
+    constexpr int kRows = 8 / kVecs;
     typedef Vec<TI, N, kAligned> In;
     typedef Vec<TO, N, kAligned> Out;
     const uint32_t nvec = static_cast<uint32_t>(hidden / N), done = nvec * N;
@@ -185,63 +193,52 @@ __global__ __launch_bounds__(kSumLanes) void moe_row_sum_kernel(const char* __re
     for (int64_t b = blockIdx.x; b < pairs; b += gridDim.x) {
         const int64_t t = b / nseg;
         const uint32_t seg = static_cast<uint32_t>(b - t * nseg);
-        const uint32_t c0 = seg * (kSumLanes * kSumVecs) + threadIdx.x;
+        const uint32_t c0 = seg * (kSumLanes * kVecs) + threadIdx.x;
         const bool tail = !kAligned && seg + 1 == nseg && threadIdx.x < left;
-        float acc[kSumVecs][N] = {};
+        float acc[kVecs][N] = {};
         float acc1 = 0.0f;
         for (int64_t j0 = 0; j0 < top_k; j0 += kSlotChunk) {
-            int32_t r[kSlotChunk];
-            float w[kSlotChunk];
-            uint32_t mask = 0;
-#pragma unroll
-            for (int j = 0; j < kSlotChunk; ++j) {
-                r[j] = -1;
-                w[j] = 1.0f;
-                if (j0 + j < top_k) {
-                    r[j] = __builtin_amdgcn_readfirstlane(row_of[t * top_k + j0 + j]);
-                    if constexpr (kWeighted) w[j] = weights[t * top_k + j0 + j];
-                    if (r[j] >= 0 && r[j] < rows) mask |= 1u << j;
-                }
-            }
+            // a lane per slot: their indices and weights are one read each
+            const int64_t j = j0 + threadIdx.x % kSlotChunk;
+            const int32_t slot_row = j < top_k ? row_of[t * top_k + j] : -1;
+            const float slot_weight = kWeighted && j < top_k ? weights[t * top_k + j] : 1.0f;
+            uint32_t mask =
+                static_cast<uint32_t>(__ballot(slot_row >= 0 && slot_row < rows)) & ((1u << kSlotChunk) - 1u);
             while (mask) {
-                int64_t at[kSumRows];
-                float ww[kSumRows];
+                int64_t at[kRows];
+                float ww[kRows];
                 int n = 0;
 #pragma unroll
-                for (int q = 0; q < kSumRows; ++q) {
+                for (int q = 0; q < kRows; ++q) {
                     at[q] = 0;
                     ww[q] = 0.0f;
-                    if (mask) {  // the lowest flagged slot, picked by compile-time indices only
-                        const int j = __builtin_ctz(mask);
+                    if (mask) {  // the lowest flagged slot
+                        const int slot = __builtin_ctz(mask);
                         mask &= mask - 1;
-#pragma unroll
-                        for (int jj = 0; jj < kSlotChunk; ++jj)
-                            if (j == jj) {
-                                at[q] = r[jj];
-                                ww[q] = w[jj];
-                            }
+                        at[q] = __builtin_amdgcn_readlane(slot_row, slot);
+                        ww[q] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(slot_weight), slot));
                         n = q + 1;
                     }
                 }
-                typename In::Raw v[kSumRows][kSumVecs];
-                float v1[kSumRows];
+                typename In::Raw v[kRows][kVecs];
+                float v1[kRows];
 #pragma unroll
-                for (int q = 0; q < kSumRows; ++q) {
+                for (int q = 0; q < kRows; ++q) {
                     v1[q] = 0.0f;
                     if (q >= n) continue;
                     const void* row = in + at[q] * hidden * kBytesOf<TI>;
 #pragma unroll
-                    for (int k = 0; k < kSumVecs; ++k) {
+                    for (int k = 0; k < kVecs; ++k) {
                         const uint32_t c = c0 + k * kSumLanes;
                         v[q][k] = c < nvec ? In::load(row, c * N) : typename In::Raw{};
                     }
                     if (tail) v1[q] = Elem<TI>::load1(row, done + threadIdx.x);
                 }
 #pragma unroll
-                for (int q = 0; q < kSumRows; ++q) {
+                for (int q = 0; q < kRows; ++q) {
                     if (q >= n) continue;
 #pragma unroll
-                    for (int k = 0; k < kSumVecs; ++k) {
+                    for (int k = 0; k < kVecs; ++k) {
                         float f[N];
                         In::widen(v[q][k], f);
 #pragma unroll
@@ -254,7 +251,7 @@ __global__ __launch_bounds__(kSumLanes) void moe_row_sum_kernel(const char* __re
         }
         char* orow = out + t * hidden * kBytesOf<TO>;
 #pragma unroll
-        for (int k = 0; k < kSumVecs; ++k) {
+        for (int k = 0; k < kVecs; ++k) {
             const uint32_t c = c0 + k * kSumLanes;
             if (c < nvec) Out::store(orow, c * N, acc[k]);
         }
@@ -291,17 +288,17 @@ __global__ __launch_bounds__(L) void moe_combine_grad_kernel(
         for (int64_t j0 = 0; j0 < top_k; j0 += kSlotChunk) {
             int64_t at[kSlotChunk];
             float w[kSlotChunk], dot[kSlotChunk];
-            uint32_t mask = 0;
+            // a lane per slot: their indices and weights are one read each
+            const int64_t mine = j0 + threadIdx.x % kSlotChunk;
+            const int32_t slot_row = mine < top_k ? row_of[t * top_k + mine] : -1;
+            const float slot_weight = mine < top_k ? weights[t * top_k + mine] : 0.0f;
+            const uint32_t mask =
+                static_cast<uint32_t>(__ballot(slot_row >= 0 && slot_row < rows)) & ((1u << kSlotChunk) - 1u);
 #pragma unroll
             for (int j = 0; j < kSlotChunk; ++j) {
-                at[j] = 0;
-                w[j] = dot[j] = 0.0f;
-                if (j0 + j < top_k) {
-                    const int32_t r = __builtin_amdgcn_readfirstlane(row_of[t * top_k + j0 + j]);
-                    w[j] = weights[t * top_k + j0 + j];
-                    if (r >= 0 && r < rows) mask |= 1u << j;
-                    at[j] = static_cast<int64_t>(r) * hidden * kBytesOf<TE>;
-                }
+                dot[j] = 0.0f;
+                w[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(slot_weight), j));
+                at[j] = static_cast<int64_t>(__builtin_amdgcn_readlane(slot_row, j)) * hidden * kBytesOf<TE>;
             }
             if (mask) {
                 for (uint32_t c0 = threadIdx.x; c0 < nvec; c0 += L * kGradVecs) {
@@ -552,7 +549,10 @@ int launch_sum(const void* in, const int32_t* row_of, const float* weights, void
                int64_t top_k, int64_t hidden, hipStream_t st) {
     constexpr int N = TI == MOE_EPI_F32 || TO == MOE_EPI_F32 ? 4 : 8;
     const bool fit = hidden % N == 0 && aligned(in, N * kBytesOf<TI>) && aligned(out, N * kBytesOf<TO>);
-    const int64_t nvec = hidden / N, per = kSumLanes * kSumVecs;
+    const int64_t nvec = hidden / N;
+    // few wavefronts, tokens with several rows (at the kernel)
+    const bool few = rows > 2 * tokens && tokens * ((nvec + 2 * kSumLanes - 1) / (2 * kSumLanes)) <= 1024;
+    const int64_t per = kSumLanes * (few ? 1 : 2);
     const int64_t nseg = nvec <= per ? 1 : (nvec + per - 1) / per;
     const dim3 grid(grid_for_rows(tokens * nseg, 1)), block(kSumLanes);
     const char* i = static_cast<const char*>(in);
@@ -566,12 +566,18 @@ int launch_sum(const void* in, const int32_t* row_of, const float* weights, void
         };
         fit ? go(moe_row_sum_narrow_kernel<TI, TO, N, kWeighted, true>)
             : go(moe_row_sum_narrow_kernel<TI, TO, N, kWeighted, false>);
-    } else if (fit)
-        hipLaunchKernelGGL((moe_row_sum_kernel<TI, TO, N, kWeighted, true>), grid, block, 0, st, i, row_of, weights, o,
-                           rows, tokens, top_k, hidden, static_cast<uint32_t>(nseg));
-    else
-        hipLaunchKernelGGL((moe_row_sum_kernel<TI, TO, N, kWeighted, false>), grid, block, 0, st, i, row_of, weights,
-                           o, rows, tokens, top_k, hidden, static_cast<uint32_t>(nseg));
+    } else {
+        auto go = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, grid, block, 0, st, i, row_of, weights, o, rows, tokens, top_k, hidden,
+                               static_cast<uint32_t>(nseg));
+        };
+        if (few)
+            fit ? go(moe_row_sum_kernel<TI, TO, N, 1, kWeighted, true>)
+                : go(moe_row_sum_kernel<TI, TO, N, 1, kWeighted, false>);
+        else
+            fit ? go(moe_row_sum_kernel<TI, TO, N, 2, kWeighted, true>)
+                : go(moe_row_sum_kernel<TI, TO, N, 2, kWeighted, false>);
+    }
     return launch_status();
 }
 

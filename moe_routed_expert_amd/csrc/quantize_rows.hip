@@ -85,7 +85,6 @@ struct RowScale {
 constexpr float kMagic = 12582912.0f;
 
 // rint(x * mul / den) of eight elements, as bytes. |x * mul / den| <= 127 (1 + 2^-23).
-
 __device__ __forceinline__ u32x2 quantize8(const RowScale& s, const float (&x)[8]) {
     float t[8], far = 0.0f;
 #pragma unroll

@@ -218,6 +218,25 @@ def test_combine_and_its_gradients(dtype, out_dtype, hidden):
         assert torch.equal(bits(gr2), bits(gr))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hidden,top_k", [(264, 3), (1001, 9), (2048, 17)])
+def test_a_tokens_sum_is_the_same_in_calls_of_all_sizes(dtype, hidden, top_k):
+    rng = np.random.default_rng(hidden + top_k)
+    tokens = 1200
+    _, offs, row_of, _ = route(rng, tokens, top_k, 20, 18)
+    x = normal(rng, (int(offs[-1]), hidden), dtype)
+    w = torch.from_numpy(rng.standard_normal((tokens, top_k)).astype(np.float32)).cuda()
+    rows = ints(row_of)
+    whole, gx = sentinel((tokens, hidden), dtype), sentinel((tokens, hidden), dtype)
+    epi.moe_combine_weighted_fwd(x, rows, w, whole)
+    epi.moe_dispatch_bwd(x, rows, gx)
+    for t0, n in ((0, 1), (tokens - 5, 5), (7, 300)):
+        part, gpart = sentinel((n, hidden), dtype), sentinel((n, hidden), dtype)
+        epi.moe_combine_weighted_fwd(x, rows[t0:t0 + n], w[t0:t0 + n], part)
+        epi.moe_dispatch_bwd(x, rows[t0:t0 + n], gpart)
+        assert torch.equal(bits(part), bits(whole[t0:t0 + n])) and torch.equal(bits(gpart), bits(gx[t0:t0 + n]))
+
+
 def test_combine_gradients_against_differences():
     """The combine is linear in the rows and in the weights: a central difference of any step is the
     derivative, up to the rounding of the two sums, 2 k eps of their size."""

@@ -272,26 +272,37 @@ constexpr int kGradRows = 2;  // rows whose loads are in flight together
 // vectors a lane 445; 448 lanes of 2, an exact fit, 483; default-policy stores
 // 448; 4 instead of 5 blocks per CU 459, registers for 6 wavefronts a SIMD 470);
 // of 4096: 262 us (256 lanes 281, 64 271).
+//
+// Few tokens leave most CUs without a block, each going through its token's
+// slots: then a token's slots are spread over `parts` blocks, `span` each, and
+// its gradient is read once more by each of them (from L2). 8 rows a token, us
+// with spans of 1, 2, 4 and with all slots in one block: 32 tokens of 7168 5.9,
+// 6.2, 7.7, 11.0, 128 12.2, 9.0, 10.0, 14.3, 256 20.5, 15.5, 15.3, 16.9, 512
+// 35.3, 29.4, 26.8, 26.7; of 2048, 128 tokens 6.1, 6.2, 7.1, 10.4, 512 12.7,
+// 11.0, 10.9, 13.7, 2048 38.9, 33.6, 30.7, 30.3. About one row a token: 32
+// tokens of 7168 3.8, 4.3, 4.7, 5.7, 128 5.9, 5.8, 6.1, 7.1.
 template <int TG, int TE, int N, int L, bool kDot, bool kAligned>
 __global__ __launch_bounds__(L) void moe_combine_grad_kernel(
     const char* __restrict__ grad, const char* __restrict__ in, const int32_t* __restrict__ row_of,
     const float* __restrict__ weights, char* __restrict__ grad_in, float* __restrict__ grad_w, int64_t rows,
-    int64_t tokens, int64_t top_k, int64_t hidden) {
+    int64_t tokens, int64_t top_k, int64_t hidden, uint32_t parts, uint32_t span) {
     typedef Vec<TG, N, kAligned> G;
     typedef Vec<TE, N, kAligned> E;
     constexpr int kWaves = L / 64;
     __shared__ float part[kWaves][kSlotChunk];
     const uint32_t nvec = static_cast<uint32_t>(hidden / N), done = nvec * N;
     const uint32_t left = static_cast<uint32_t>(hidden) - done;
-    for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
+    for (int64_t b = blockIdx.x; b < tokens * parts; b += gridDim.x) {
+        const int64_t t = parts == 1 ? b : static_cast<uint32_t>(b) / parts;
+        const int64_t first = (b - t * parts) * span, end = first + span < top_k ? first + span : top_k;
         const char* grow = grad + t * hidden * kBytesOf<TG>;
-        for (int64_t j0 = 0; j0 < top_k; j0 += kSlotChunk) {
+        for (int64_t j0 = first; j0 < end; j0 += kSlotChunk) {
             int64_t at[kSlotChunk];
             float w[kSlotChunk], dot[kSlotChunk];
             // a lane per slot: their indices and weights are one read each
             const int64_t mine = j0 + threadIdx.x % kSlotChunk;
-            const int32_t slot_row = mine < top_k ? row_of[t * top_k + mine] : -1;
-            const float slot_weight = mine < top_k ? weights[t * top_k + mine] : 0.0f;
+            const int32_t slot_row = mine < end ? row_of[t * top_k + mine] : -1;
+            const float slot_weight = mine < end ? weights[t * top_k + mine] : 0.0f;
             const uint32_t mask =
                 static_cast<uint32_t>(__ballot(slot_row >= 0 && slot_row < rows)) & ((1u << kSlotChunk) - 1u);
 #pragma unroll
@@ -358,7 +369,7 @@ __global__ __launch_bounds__(L) void moe_combine_grad_kernel(
                     if (lane == 0) part[wave][j] = s;
                 }
                 __syncthreads();
-                if (threadIdx.x < kSlotChunk && j0 + threadIdx.x < top_k) {
+                if (threadIdx.x < kSlotChunk && j0 + threadIdx.x < end) {
                     float s = 0.0f;
 #pragma unroll
                     for (int v = 0; v < kWaves; ++v) s += part[v][threadIdx.x];
@@ -587,11 +598,14 @@ int launch_grad(const void* grad, const void* in, const int32_t* row_of, const f
     constexpr int N = TG == MOE_EPI_F32 || TE == MOE_EPI_F32 ? 4 : 8;
     const bool fit = hidden % N == 0 && aligned(grad, N * kBytesOf<TG>) && aligned(in, N * kBytesOf<TE>) &&
                      aligned(grad_in, N * kBytesOf<TE>);
-    const dim3 grid(grid_for_rows(tokens, 1));
     auto go = [&](int lanes, auto kernel) {
+        const int64_t waves = tokens * top_k * (lanes / 64);  // with a block for every slot
+        const int64_t span = waves <= 1024 ? 1 : (waves <= 4096 ? 2 : (waves <= 8192 ? 4 : top_k));
+        const int64_t parts = (top_k + span - 1) / span;
+        const dim3 grid(grid_for_rows(tokens * parts, 1));
         hipLaunchKernelGGL(kernel, grid, dim3(lanes), 0, st, static_cast<const char*>(grad),
                            static_cast<const char*>(in), row_of, weights, static_cast<char*>(grad_in), grad_w, rows,
-                           tokens, top_k, hidden);
+                           tokens, top_k, hidden, static_cast<uint32_t>(parts), static_cast<uint32_t>(span));
     };
     auto pick = [&](auto lanes) {
         constexpr int L = decltype(lanes)::value;

@@ -235,6 +235,15 @@ def test_a_tokens_sum_is_the_same_in_calls_of_all_sizes(dtype, hidden, top_k):
         epi.moe_combine_weighted_fwd(x, rows[t0:t0 + n], w[t0:t0 + n], part)
         epi.moe_dispatch_bwd(x, rows[t0:t0 + n], gpart)
         assert torch.equal(bits(part), bits(whole[t0:t0 + n])) and torch.equal(bits(gpart), bits(gx[t0:t0 + n]))
+    # and its gradients: the slots of few tokens are spread over several blocks
+    g, gr, gw = normal(rng, (tokens, hidden), dtype), sentinel(x.shape, dtype), sentinel(w.shape, torch.float32)
+    epi.moe_combine_weighted_bwd(g, x, rows, w, gr, gw)
+    for t0, n in ((0, 1), (3, 33), (tokens - 5, 5), (7, 300)):
+        gr2, gw2 = gr.clone(), sentinel((n, top_k), torch.float32)
+        mine = torch.from_numpy(row_of[t0:t0 + n][row_of[t0:t0 + n] >= 0].astype(np.int64)).cuda()
+        gr2[mine] = 7.0
+        epi.moe_combine_weighted_bwd(g[t0:t0 + n], x, rows[t0:t0 + n], w[t0:t0 + n], gr2, gw2)
+        assert torch.equal(bits(gr2), bits(gr)) and torch.equal(bits(gw2), bits(gw[t0:t0 + n]))
 
 
 def test_combine_gradients_against_differences():

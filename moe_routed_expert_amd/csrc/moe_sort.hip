@@ -15,8 +15,9 @@
 // wavefront, so no atomic operation is needed.
 //
 // Short calls are bound by their chain of reads, counts and writes, and a call
-// of up to 1024 slots is one block (32 x 8 slots over 64 experts 2.9 us, 1 x 8
-// over 256 experts 3.8). Longer ones count tiles of slots first: two launches,
+// of up to 2048 slots is one block (32 x 8 slots over 64 experts 2.9 us, 1 x 8
+// over 256 experts 3.8; 256 x 8 over 64 4.5, against 6.0 by two launches, but
+// 512 x 8 over 256 8.1 against 7.5). Longer ones count tiles of slots first: two launches,
 // 131072 x 8 slots over 8 local experts 10.0 us, of which the 12 MB that are
 // read and written need 2; with more than 8192 counts a third launch sums them,
 // since every block would read them all (131072 x 8 over 256 experts 20.3 us
@@ -34,6 +35,7 @@ constexpr int64_t kMaxSlotsPerToken = 1024;
 constexpr int kTileThreads = 1024;
 constexpr int kTileWaves = kTileThreads / 64;
 constexpr int kMostGroups = 4;                   // groups of 64 slots per wavefront of a tile, at most
+constexpr int kOneGroups = 2;                    // and of a call's only tile
 constexpr int64_t kTiles = 256;                  // tiles that a call aims at: one per CU
 constexpr int kDirect = 8;                       // counts per thread that a block reads of all tiles
 
@@ -257,6 +259,7 @@ int64_t tiles_of(int64_t slots, int groups) {
 bool scans(int64_t tiles, int64_t experts) { return tiles * experts > kDirect * kTileThreads; }
 
 int groups_of(int64_t slots, int64_t experts) {
+    if (slots <= kTileThreads * kOneGroups) return slots <= kTileThreads ? 1 : kOneGroups;
     int g = 1;
     while (g < kMostGroups && tiles_of(slots, g) > kTiles) g *= 2;
     if (g == 2 && scans(tiles_of(slots, 2), experts) && !scans(tiles_of(slots, 4), experts)) g = 4;
@@ -275,7 +278,9 @@ void launch_sort(const void* ids, int64_t first, int* offs, int* row_of, int* sl
                            slots, first, experts, bits_for(experts), tiles);
     };
     if (slots <= 256) return place(256, moe_sort_place<Id, 256, 1, false>);
-    if (tiles == 1) return place(kTileThreads, moe_sort_place<Id, kTileThreads, 1, false>);
+    if (tiles == 1)
+        return groups == 1 ? place(kTileThreads, moe_sort_place<Id, kTileThreads, 1, false>)
+                           : place(kTileThreads, moe_sort_place<Id, kTileThreads, kOneGroups, false>);
     auto many = [&](auto groups) {
         constexpr int G = decltype(groups)::value;
         hipLaunchKernelGGL((moe_sort_count<Id, G>), dim3(tiles), dim3(kTileThreads), 0, st, p, hist, slots, first,

@@ -92,7 +92,8 @@ def check(got, want, slack, dtype, what):
     (1, 1, 1, 0, 1), (1, 8, 64, 0, 64), (3, 2, 5, 3, 2), (32, 8, 64, 0, 64), (63, 1, 7, 2, 3), (257, 3, 12, 0, 12),
     (512, 8, 64, 24, 8), (513, 8, 64, 24, 8), (1365, 3, 1024, 0, 1024), (4096, 1, 2, 0, 1), (4097, 1, 2, 1, 1),
     (5000, 7, 128, 32, 32), (20011, 8, 64, 0, 64), (3001, 8, 1024, 0, 1024), (8200, 8, 1024, 7, 1000),
-    (60000, 7, 128, 0, 128), (50021, 7, 64, 0, 16), (40000, 8, 64, 0, 64), (70001, 8, 64, 3, 8)])
+    (60000, 7, 128, 0, 128), (128, 8, 64, 0, 64), (129, 8, 64, 8, 40), (293, 7, 1024, 0, 1024), (256, 8, 16, 0, 16),
+    (2049, 1, 3, 1, 2), (50021, 7, 64, 0, 16), (40000, 8, 64, 0, 64), (70001, 8, 64, 3, 8)])
 def test_sort(dtype, tokens, top_k, experts, first, local):
     rng = np.random.default_rng(tokens + local)
     ids, offs_w, row_w, slot_w = route(rng, tokens, top_k, experts, local, first)

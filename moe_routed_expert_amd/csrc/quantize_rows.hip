@@ -20,7 +20,11 @@
 //
 // A row takes the fewest lanes that hold it, four vectors each: 65536 rows of
 // 256 13 us with 16 lanes, 19 with 32, 30 with 64; of 512 20, 25, 35; of 1024
-// 35 with 32, 45 with 64; 32768 of 7168 109 with 256 lanes, 139 with 512.
+// 35 with 32, 45 with 64; 32768 of 7168 109 with 256 lanes, 139 with 512. Up to
+// 512 rows, two per CU, do not fill the chip, and a row is done sooner by more
+// lanes with one or two vectors each: 32 rows of 2048 3.4 -> 2.6 us, of 4096 3.6
+// -> 2.9, of 7168 3.6 -> 3.4, of 16384 6.0 -> 4.5; 512 rows 3.9 -> 3.3, 4.4 -> 3.9,
+// 5.3 -> 5.1, 11.2 -> 8.0; but 1024 rows of 640 3.56 and 3.58, of 7168 6.5 and 6.7.
 #include <type_traits>
 
 #include "epi_common.h"
@@ -29,8 +33,8 @@
 namespace moe_epi {
 namespace {
 
-constexpr int kBlock = 256;
-constexpr int kVecs = 4;  // vectors of 8 elements that a lane keeps
+constexpr int kBlock = 256;         // threads, or the lanes of a row if they are more
+constexpr int64_t kFewRows = 512;
 
 // Eight elements at element e of a row, as stored. kAligned: 16-byte aligned
 // rows, read once; others share cache lines between lanes and rows, so they
@@ -115,7 +119,12 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part) {
         const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), off, 64));
         v = o > v ? o : v;
     }
-    if constexpr (L > 64) {
+    if constexpr (L > kBlock) {
+        if ((threadIdx.x & 63) == 0) atomicMax(part, v);  // any order, one maximum; cleared before the row's loads
+        __syncthreads();
+        v = *part;
+        __syncthreads();
+    } else if constexpr (L > 64) {
         if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
         __syncthreads();
         const int first = threadIdx.x / L * (L / 64);
@@ -126,14 +135,14 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part) {
     return v;
 }
 
-// L lanes per row: part of a wavefront, a wavefront, half of the block or the block.
-template <int T, int L, bool kAligned>
-__global__ __launch_bounds__(kBlock) void quantize_rows_kernel(const char* __restrict__ x, int8_t* __restrict__ q,
-                                                               float* __restrict__ scale, int64_t rows,
-                                                               int64_t cols) {
+// L lanes per row, from part of a wavefront to the block; kVecs vectors of 8
+// elements that a lane keeps.
+template <int T, int L, int kVecs, bool kAligned>
+__global__ __launch_bounds__(L > kBlock ? L : kBlock) void quantize_rows_kernel(
+    const char* __restrict__ x, int8_t* __restrict__ q, float* __restrict__ scale, int64_t rows, int64_t cols) {
     typedef Eight<T, kAligned> X;
-    constexpr int kRowsPerBlock = kBlock / L;
-    __shared__ uint32_t part[kBlock / 64];
+    constexpr int kThreads = L > kBlock ? L : kBlock, kRowsPerBlock = kThreads / L;
+    __shared__ uint32_t part[kBlock / 64];  // a word per wavefront, or one for a row of more
     const uint32_t lane = threadIdx.x % L;
     const uint32_t nvec = static_cast<uint32_t>(cols / 8), left = static_cast<uint32_t>(cols) - nvec * 8;
     const int64_t groups = (rows + kRowsPerBlock - 1) / kRowsPerBlock;
@@ -145,6 +154,10 @@ __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(const char* __res
         int8_t* qrow = q + r * cols;
         typename X::Raw raw[kVecs];
         uint32_t most = 0;
+        if constexpr (L > kBlock) {
+            if (threadIdx.x == 0) *part = 0;
+            __syncthreads();
+        }
         auto grow = [&](const typename X::Raw& v) {
             float f[8];
             X::widen(v, f);
@@ -191,26 +204,34 @@ __global__ __launch_bounds__(kBlock) void quantize_rows_kernel(const char* __res
 template <int T>
 void launch_quantize(const void* x, int8_t* q, float* scale, int64_t rows, int64_t cols, hipStream_t st) {
     const bool fit = cols % 8 == 0 && aligned(x, 16) && aligned(q, 8);
-    // the fewest lanes that hold a row, from 16 (512 elements) to the block (8192; wider rows are read again)
-    auto go = [&](auto lanes) {
-        constexpr int L = decltype(lanes)::value;
-        const dim3 block(kBlock), grid(grid_for_rows(rows, kBlock / L));
+    auto go = [&](auto lanes, auto vecs) {
+        constexpr int L = decltype(lanes)::value, V = decltype(vecs)::value, kThreads = L > kBlock ? L : kBlock;
+        const dim3 block(kThreads), grid(grid_for_rows(rows, kThreads / L));
         auto launch = [&](auto kernel) {
             hipLaunchKernelGGL(kernel, grid, block, 0, st, static_cast<const char*>(x), q, scale, rows, cols);
         };
-        fit ? launch(quantize_rows_kernel<T, L, true>) : launch(quantize_rows_kernel<T, L, false>);
+        fit ? launch(quantize_rows_kernel<T, L, V, true>) : launch(quantize_rows_kernel<T, L, V, false>);
     };
-    const int64_t lanes = (cols + 8 * kVecs - 1) / (8 * kVecs);
-    if (lanes <= 16)
-        go(std::integral_constant<int, 16>());
-    else if (lanes <= 32)
-        go(std::integral_constant<int, 32>());
-    else if (lanes <= 64)
-        go(std::integral_constant<int, 64>());
-    else if (lanes <= 128)
-        go(std::integral_constant<int, 128>());
-    else
-        go(std::integral_constant<int, kBlock>());
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    const std::integral_constant<int, 4> four;
+    const std::integral_constant<int, 128> l128;
+    const std::integral_constant<int, 256> l256;
+    const std::integral_constant<int, 512> l512;
+    // the fewest lanes that hold a row; of the widest rows what they do not hold is read again
+    const int64_t vecs = (cols + 7) / 8;
+    if (vecs <= 16 * 4) return go(std::integral_constant<int, 16>(), four);
+    if (rows <= kFewRows) {
+        if (vecs <= 128) return go(l128, one);
+        if (vecs <= 256) return go(l256, one);
+        if (vecs <= 512) return go(l512, one);
+        if (vecs <= 512 * 2) return go(l512, two);
+        return go(std::integral_constant<int, 1024>(), two);
+    }
+    if (vecs <= 32 * 4) return go(std::integral_constant<int, 32>(), four);
+    if (vecs <= 64 * 4) return go(std::integral_constant<int, 64>(), four);
+    if (vecs <= 128 * 4) return go(l128, four);
+    return go(l256, four);
 }
 
 }  // namespace

@@ -363,6 +363,22 @@ def test_quantize_rows(dtype, cols):
         assert np.abs(got).max() <= 127
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", [100, 520, 1001, 1032, 2056, 4099, 8192, 9001])
+def test_quantize_gives_a_row_the_same_in_calls_of_all_sizes(dtype, cols):
+    rng = np.random.default_rng(cols + 7)
+    x = rng.standard_normal((700, cols)) * 10.0 ** rng.integers(-4, 4, (700, 1))
+    t = torch.from_numpy(x.astype(np.float32)).to(dtype).cuda()
+    q, scale = epi.quantize_rows_int8(t)
+    v = ref.f64(t)
+    amax = np.abs(v).max(1)
+    assert np.abs(q.cpu().numpy() - 127.0 * v / amax[:, None]).max() <= 0.5 + 127 * 2.0 ** -23
+    assert torch.equal(bits(scale), bits(torch.from_numpy(amax.astype(np.float32) / np.float32(127))))
+    for r0, n in ((0, 1), (3, 512), (187, 513), (693, 7)):
+        part = epi.quantize_rows_int8(t[r0:r0 + n].clone())
+        assert torch.equal(part[0], q[r0:r0 + n]) and torch.equal(bits(part[1]), bits(scale[r0:r0 + n]))
+
+
 def test_quantize_ties_to_even_and_rows_that_are_not_finite():
     # 127 * 0.5 / 1 = 63.5 and its like: the integer is the even neighbour
     x = torch.tensor([[1.0, 0.5, -0.5, 0.25], [2.0, 1.0, -1.0, 0.0], [float("inf"), 1, 2, 3],

@@ -139,8 +139,8 @@ int quantize_rows_int8_fwd(const void *x, int dtype, int8_t *q, float *scale, in
  * rest is float32, rounded once. slot_of == NULL: u = r, tokens == rows, top_k == 1.
  * A row whose slot is outside [0, tokens * top_k) gives y = 0 * probs[r]. Rows
  * at or past the last end are not written.
- *   a            [tokens, hidden] int8             in
- *   a_scale      [tokens] float32                  in
+ *   a            [tokens, hidden] int8             in (may be NULL if tokens == 0)
+ *   a_scale      [tokens] float32                  in (may be NULL if tokens == 0)
  *   slot_of      [rows] int32 or NULL              in
  *   w_gate, w_up [experts, inter, hidden] int8     in
  *   w_*_scale    [experts, inter] float32          in

@@ -825,8 +825,8 @@ extern "C" int grouped_gate_up_swiglu_int8_fwd(const int8_t* a, const float* a_s
         !bytes_ok(experts, inter, 4, &sb) || !bytes_ok(experts, 1, 4, &ob))
         return MOE_EPI_ERR_BAD_SHAPE;
     if (!(limit > 0.0f) || !isfinite(limit)) return MOE_EPI_ERR_BAD_LIMIT;
-    if (rows == 0 || tokens == 0) return MOE_EPI_SUCCESS;
-    if (!a || !a_scale || !w_gate || !w_gate_scale || !w_up || !w_up_scale || !offs || !y)
+    if (rows == 0) return MOE_EPI_SUCCESS;
+    if ((tokens > 0 && (!a || !a_scale)) || !w_gate || !w_gate_scale || !w_up || !w_up_scale || !offs || !y)
         return MOE_EPI_ERR_NULL_POINTER;
     if (!aligned(a, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16) || !aligned(y, 16) || !aligned(a_scale, 4) ||
         !aligned(slot_of, 4) || !aligned(w_gate_scale, 4) || !aligned(w_up_scale, 4) || !aligned(offs, 4) ||
@@ -837,6 +837,9 @@ extern "C" int grouped_gate_up_swiglu_int8_fwd(const int8_t* a, const float* a_s
                            range_of(w_gate, wb), range_of(w_up, wb), range_of(w_gate_scale, sb),
                            range_of(w_up_scale, sb), range_of(offs, ob), range_of(probs, probs ? rb : 0)})
         if (overlaps(ry, r)) return MOE_EPI_ERR_ALIAS;
+    // Without tokens no slot is in range. The kernels read row 0 of a for such a slot, times a scale of 0, and
+    // any `hidden` bytes will do for it: a row of the weights.
+    if (tokens == 0) a = w_gate;
     const Rows rows_of{a_scale, slot_of, static_cast<uint32_t>(top_k), tokens * top_k};
     return launch_int8<Out::kSwiglu>(a, rows_of, tokens, w_gate, w_gate_scale, w_up, w_up_scale, offs, probs, y, rows,
                                      hidden, inter, experts, limit, as_stream(stream));

@@ -601,6 +601,30 @@ def test_chain_replayed_from_a_graph_equals_eager():
     assert same(c.outs, want)                     # the same on another stream
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
+@pytest.mark.parametrize("counts,n", [([7], 16), ([40, 0, 35], 16), ([30, 0, 25, 31, 64, 17] * 7, 520),
+                                      ([100, 128, 1, 0, 140, 129] * 7, 520), ([300, 256, 257, 1, 512, 0] * 7, 776)])
+def test_gate_up_of_no_tokens_gives_rows_of_zeros(counts, n):
+    """Without tokens every slot is out of range: y = 0 * probs below the last expert's end, by every kernel."""
+    rng = np.random.default_rng(n)
+    offs, k, top_k = np.cumsum(counts).astype(np.int32), 144, 2
+    rows, extra = int(offs[-1]), 2
+    w, s = int8_of(rng, (len(counts), n, k)), scales(rng, (len(counts), n), 1.0)
+    p = torch.from_numpy(rng.random(rows + extra).astype(np.float32)).cuda()
+    p[3] = float("inf")
+    none, no_scale = torch.empty((0, k), dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda")
+    for probs in (None, p):
+        y = sentinel((rows + extra, n), torch.bfloat16)
+        kept = bits(y[rows:].clone())
+        epi.grouped_gate_up_swiglu_int8_fwd(none, no_scale, ints(rng.integers(-2, 50, rows + extra)), top_k, w, s, w, s,
+                                            ints(offs), probs, y, 7.0)
+        zeros = y[:rows].float()
+        if probs is not None:
+            assert bool(torch.isnan(zeros[3]).all())
+            zeros[3] = 0.0
+        assert bool((zeros == 0).all())
+        assert torch.equal(bits(y[rows:]), kept)
+
+
         c.step()
     noise = torch.randn(256, 256, device="cuda")
     for _ in range(3):

@@ -147,6 +147,15 @@ def test_products(L):
     expect(d, OK, {"rows": 0})
 
 
+def test_gate_up_without_tokens_still_has_rows_to_write(L):
+    """A call of no tokens writes rows of zeros: it needs its other tensors and takes no shortcut around their checks."""
+    f = calls(L)["gate_up"]
+    expect(f, NULLP, *({"tokens": 0, "a": None, "sa": None, k: None} for k in ("wg", "sg", "wu", "su", "offs", "y")))
+    expect(f, MISAL, {"tokens": 0, "y": P[9] + 2})
+    expect(f, ALIAS, {"tokens": 0, "y": P[3]})
+    expect(f, OK, {"tokens": 0, "rows": 0})
+
+
 def test_binding_refuses_tensors_the_calls_cannot_take():
     x = torch.zeros(4, 32, dtype=torch.bfloat16)
     i = torch.zeros(8, dtype=torch.int32)

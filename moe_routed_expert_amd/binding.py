@@ -280,6 +280,16 @@ def moe_combine_fwd(expert_out, row_of, out, stream=None) -> None:
 
 # ---- allocating helpers and autograd wrappers ------------------------------
 
+def _first_derivative_only(name: str, again: bool) -> None:
+    """Refuse a backward pass under create_graph=True whose gradients depend (`again`) on tensors that need
+    gradients themselves: the kernels' results carry no graph, and a second derivative would lose those terms
+    without an error. (A once_differentiable mark is not enough: its error stands on no path to the inputs, so
+    torch.autograd.grad passes it by, and it does not look at what the forward pass kept.)"""
+    if again and torch.is_grad_enabled():
+        raise RuntimeError(f"{name} has first derivatives only: its backward pass cannot be differentiated again "
+                           "(create_graph=True)")
+
+
 def swiglu_clamped(x, probs, limit: float):
     y = torch.empty((x.shape[0], x.shape[1] // 2), dtype=x.dtype, device=x.device)
     swiglu_clamped_fwd(x, probs, y, limit)

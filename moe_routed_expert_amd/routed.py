@@ -11,9 +11,10 @@ Names follow the C ABI (include/moe_routed.h):
                                   y, limit)
   grouped_down_router_int8_fwd(h, h_scale, w_down, w_down_scale, offs, probs, out)
 plus allocating helpers (moe_sort, quantize_rows_int8) and torch.autograd.Function wrappers
-(MoeDispatch, MoeCombineWeighted). Every call writes into tensors of the caller, on the current
-stream of their device, and raises TypeError / ValueError for tensors the C ABI cannot take and
-MoeEpiError for a status other than success. There is no fallback.
+(MoeDispatch, MoeCombineWeighted), which have first derivatives and refuse a second. Every call
+writes into tensors of the caller, on the current stream of their device, and raises TypeError /
+ValueError for tensors the C ABI cannot take and MoeEpiError for a status other than success. There
+is no fallback.
 
 These calls are also made for single tokens, where a kernel runs for a few microseconds, so each
 call tests all its tensors in one expression, and looks for the one to name only when that fails.
@@ -267,6 +268,7 @@ class MoeDispatch(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_out):
+        binding._first_derivative_only("MoeDispatch", grad_out.requires_grad)
         row_of, = ctx.saved_tensors
         grad_x = torch.empty((ctx.tokens, grad_out.shape[1]), dtype=grad_out.dtype, device=grad_out.device)
         moe_dispatch_bwd(grad_out.contiguous(), row_of, grad_x)
@@ -289,6 +291,9 @@ class MoeCombineWeighted(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_out):
+        # each gradient is linear in grad_out and in the other input
+        again = grad_out.requires_grad or (ctx.needs_input_grad[0] and ctx.needs_input_grad[2])
+        binding._first_derivative_only("MoeCombineWeighted", again)
         expert_out, row_of, weights = ctx.saved_tensors
         # rows that belong to no slot have gradient 0
         grad_rows = torch.zeros((ctx.rows, grad_out.shape[1]), dtype=ctx.dtype, device=grad_out.device)

@@ -304,7 +304,7 @@ def router_weight_mul(x, probs, out_dtype=None):
 
 class SwigluClamped(torch.autograd.Function):
     """silu(clamp(gate, max=L)) * clamp(up, -L, L) * probs with the HIP forward and
-    single-pass backward; saves only x and probs."""
+    single-pass backward; saves only x and probs. First derivatives only."""
 
     @staticmethod
     def forward(ctx, x, probs, limit: float):
@@ -316,6 +316,8 @@ class SwigluClamped(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_y):
+        # the gradients are linear in grad_y, and not linear in x
+        _first_derivative_only("SwigluClamped", grad_y.requires_grad or ctx.needs_input_grad[0])
         x, probs = ctx.saved_tensors
         grad_x = torch.empty_like(x)
         grad_probs = torch.empty_like(probs) if ctx.needs_input_grad[1] else None
@@ -326,7 +328,8 @@ class SwigluClamped(torch.autograd.Function):
 class RouterWeightMul(torch.autograd.Function):
     """fp32(x) * probs rounded to out_dtype (default: x's dtype; float32 for a
     scatter-add combine) with the HIP forward and a one-pass backward. x is
-    saved only when probs needs a gradient (it is read only for that gradient)."""
+    saved only when probs needs a gradient (it is read only for that gradient).
+    First derivatives only."""
 
     @staticmethod
     def forward(ctx, x, probs, out_dtype=None):
@@ -340,6 +343,9 @@ class RouterWeightMul(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_out):
+        # each gradient is linear in grad_out and in the other input
+        again = grad_out.requires_grad or (ctx.needs_input_grad[0] and ctx.needs_input_grad[1])
+        _first_derivative_only("RouterWeightMul", again)
         x, probs = ctx.saved_tensors
         grad_out = grad_out.contiguous()
         grad_x = torch.empty(grad_out.shape, dtype=ctx.x_dtype, device=grad_out.device)

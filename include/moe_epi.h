@@ -16,6 +16,9 @@
  *             memset or synchronisation inside, a call can be captured into a
  *             HIP graph on `stream` and replayed; the graph then reads and
  *             writes the buffers passed at capture.
+ *   Device    The kernel is launched on the GPU of `stream`, and for NULL on
+ *             the calling thread's current GPU. The caller sees to it that
+ *             this is the GPU of the tensors (hipSetDevice); it is not checked.
  *   Dtypes    x, y, gradients of x/y: bfloat16. probs, grad_probs: float32.
  *             All arithmetic is float32; each bfloat16 result is rounded once,
  *             to nearest with ties to even.

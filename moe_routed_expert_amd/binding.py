@@ -43,6 +43,7 @@ STATUS = {
 DTYPE_CODE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 _lib = None
+_several_gpus = False              # whether this process sees more than one GPU; set with _lib
 
 
 class MoeEpiError(RuntimeError):
@@ -53,7 +54,7 @@ class MoeEpiError(RuntimeError):
 
 def lib() -> ctypes.CDLL:
     """The loaded C-ABI library. Raises if it has not been built."""
-    global _lib
+    global _lib, _several_gpus
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -80,6 +81,7 @@ def lib() -> ctypes.CDLL:
         getattr(L, name).restype = ctypes.c_int
     L.moe_epi_status_string.argtypes = [ctypes.c_int]
     L.moe_epi_status_string.restype = ctypes.c_char_p
+    _several_gpus = torch.cuda.device_count() > 1
     _lib = L
     return L
 
@@ -93,10 +95,28 @@ def _check(status: int, where: str) -> None:
         raise MoeEpiError(status, where)
 
 
-def _stream_handle(t: torch.Tensor, stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream(t.device)
-    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+def _handle(stream, device: int) -> int:
+    """The hipStream_t of a stream given by the caller: a torch stream of this GPU, or the handle itself."""
+    if not hasattr(stream, "cuda_stream"):
+        return int(stream)
+    if getattr(stream, "device_index", device) != device:
+        raise ValueError(f"the stream is on GPU {stream.device_index}, the tensors are on GPU {device}")
+    return int(stream.cuda_stream)
+
+
+def _on(device: int, call, *args) -> int:
+    """call(*args) with this GPU as the current one. The handle of a default stream is 0 on every GPU, and a launch
+    on it goes to the current GPU, whichever one the tensors are on."""
+    if not _several_gpus or torch.cuda.current_device() == device:
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
+
+
+def _queue(call, device: int, stream, *args) -> int:
+    """The status of call(*args, stream), by default on the current stream of the tensors' GPU."""
+    handle = _handle(torch.cuda.current_stream(device) if stream is None else stream, device)
+    return _on(device, call, *args, handle)
 
 
 def _need(t: torch.Tensor | None, name: str, dtype, shape, device) -> None:
@@ -141,11 +161,12 @@ def swiglu_clamped_fwd(x, probs, y, limit: float, stream=None) -> None:
     _need(x, "x", x.dtype, [(rows, two_i)], dev)
     _need(probs, "probs", torch.float32, [(rows,), (rows, 1)], dev)
     _need(y, "y", x.dtype, [(rows, inter)], dev)
-    st = _stream_handle(x, stream)
     if code == 0:
-        status = lib().swiglu_clamped_fwd(_ptr(x), _ptr(probs), _ptr(y), rows, inter, float(limit), st)
+        status = _queue(lib().swiglu_clamped_fwd, dev.index, stream, _ptr(x), _ptr(probs), _ptr(y), rows, inter,
+                        float(limit))
     else:
-        status = lib().swiglu_clamped_fwd_typed(_ptr(x), _ptr(probs), _ptr(y), rows, inter, float(limit), code, st)
+        status = _queue(lib().swiglu_clamped_fwd_typed, dev.index, stream, _ptr(x), _ptr(probs), _ptr(y), rows, inter,
+                        float(limit), code)
     _check(status, "swiglu_clamped_fwd")
 
 
@@ -162,13 +183,12 @@ def swiglu_clamped_bwd(x, probs, grad_y, grad_x, grad_probs, limit: float, strea
     _need(grad_x, "grad_x", x.dtype, [(rows, two_i)], dev)
     if grad_probs is not None:
         _need(grad_probs, "grad_probs", torch.float32, [(rows,), (rows, 1)], dev)
-    st = _stream_handle(x, stream)
     if code == 0:
-        status = lib().swiglu_clamped_bwd(_ptr(x), _ptr(probs), _ptr(grad_y), _ptr(grad_x), _ptr(grad_probs), rows,
-                                          inter, float(limit), st)
+        status = _queue(lib().swiglu_clamped_bwd, dev.index, stream, _ptr(x), _ptr(probs), _ptr(grad_y), _ptr(grad_x),
+                        _ptr(grad_probs), rows, inter, float(limit))
     else:
-        status = lib().swiglu_clamped_bwd_typed(_ptr(x), _ptr(probs), _ptr(grad_y), _ptr(grad_x), _ptr(grad_probs),
-                                                rows, inter, float(limit), code, st)
+        status = _queue(lib().swiglu_clamped_bwd_typed, dev.index, stream, _ptr(x), _ptr(probs), _ptr(grad_y),
+                        _ptr(grad_x), _ptr(grad_probs), rows, inter, float(limit), code)
     _check(status, "swiglu_clamped_bwd")
 
 
@@ -181,11 +201,11 @@ def router_weight_mul_fwd(x, probs, out, stream=None) -> None:
     _need(probs, "probs", torch.float32, [(rows,), (rows, 1)], dev)
     _need(out, "out", out.dtype, [(rows, hidden)], dev)
     oc = _code(out, "out")
-    st = _stream_handle(x, stream)
     if xc == 0 and oc == 0:
-        status = lib().router_weight_mul_fwd(_ptr(x), _ptr(probs), _ptr(out), rows, hidden, st)
+        status = _queue(lib().router_weight_mul_fwd, dev.index, stream, _ptr(x), _ptr(probs), _ptr(out), rows, hidden)
     else:
-        status = lib().router_weight_mul_fwd_typed(_ptr(x), xc, _ptr(probs), _ptr(out), oc, rows, hidden, st)
+        status = _queue(lib().router_weight_mul_fwd_typed, dev.index, stream, _ptr(x), xc, _ptr(probs), _ptr(out), oc,
+                        rows, hidden)
     _check(status, "router_weight_mul_fwd")
 
 
@@ -203,13 +223,12 @@ def router_weight_mul_bwd(grad_out, x, probs, grad_x, grad_probs, stream=None) -
         _need(grad_probs, "grad_probs", torch.float32, [(rows,), (rows, 1)], dev)
     _need(probs, "probs", torch.float32, [(rows,), (rows, 1)], dev)
     xp = _ptr(x) if grad_probs is not None else None
-    st = _stream_handle(grad_out, stream)
     if xc == 0 and oc == 0:
-        status = lib().router_weight_mul_bwd(_ptr(grad_out), xp, _ptr(probs), _ptr(grad_x), _ptr(grad_probs), rows,
-                                             hidden, st)
+        status = _queue(lib().router_weight_mul_bwd, dev.index, stream, _ptr(grad_out), xp, _ptr(probs), _ptr(grad_x),
+                        _ptr(grad_probs), rows, hidden)
     else:
-        status = lib().router_weight_mul_bwd_typed(_ptr(grad_out), oc, xp, xc, _ptr(probs), _ptr(grad_x),
-                                                   _ptr(grad_probs), rows, hidden, st)
+        status = _queue(lib().router_weight_mul_bwd_typed, dev.index, stream, _ptr(grad_out), oc, xp, xc, _ptr(probs),
+                        _ptr(grad_x), _ptr(grad_probs), rows, hidden)
     _check(status, "router_weight_mul_bwd")
 
 
@@ -231,10 +250,9 @@ def grouped_gate_up_swiglu_fwd(a, w_gate, w_up, offs, probs, y, x_out, limit: fl
     _need(y, "y", torch.bfloat16, [(tokens, inter)], dev)
     if x_out is not None:
         _need(x_out, "x_out", torch.bfloat16, [(tokens, 2 * inter)], dev)
-    st = _stream_handle(a, stream)
-    status = lib().grouped_gate_up_swiglu_fwd(a.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), offs.data_ptr(),
-                                              probs.data_ptr(), y.data_ptr(), _ptr(x_out), tokens, hidden, inter,
-                                              experts, float(limit), st)
+    status = _queue(lib().grouped_gate_up_swiglu_fwd, dev.index, stream, a.data_ptr(), w_gate.data_ptr(),
+                    w_up.data_ptr(), offs.data_ptr(), probs.data_ptr(), y.data_ptr(), _ptr(x_out), tokens, hidden,
+                    inter, experts, float(limit))
     _check(status, "grouped_gate_up_swiglu_fwd")
 
 
@@ -255,10 +273,8 @@ def grouped_down_router_fwd(h, w_down, offs, probs, out, stream=None) -> None:
     if out.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"out: expected bfloat16 or float32, got {out.dtype}")
     _need(out, "out", out.dtype, [(tokens, hidden)], dev)
-    st = _stream_handle(h, stream)
-    status = lib().grouped_down_router_fwd(h.data_ptr(), w_down.data_ptr(), offs.data_ptr(), probs.data_ptr(),
-                                           out.data_ptr(), DTYPE_CODE[out.dtype], tokens, inter, hidden, experts,
-                                           st)
+    status = _queue(lib().grouped_down_router_fwd, dev.index, stream, h.data_ptr(), w_down.data_ptr(), offs.data_ptr(),
+                    probs.data_ptr(), out.data_ptr(), DTYPE_CODE[out.dtype], tokens, inter, hidden, experts)
     _check(status, "grouped_down_router_fwd")
 
 
@@ -272,9 +288,8 @@ def moe_combine_fwd(expert_out, row_of, out, stream=None) -> None:
     _need(expert_out, "expert_out", expert_out.dtype, [(rows, hidden)], dev)
     _need(row_of, "row_of", torch.int32, [(tokens, top_k)], dev)
     _need(out, "out", torch.float32, [(tokens, hidden)], dev)
-    st = _stream_handle(out, stream)
-    status = lib().moe_combine_fwd(_ptr(expert_out) if rows else None, _code(expert_out, "expert_out"),
-                                   row_of.data_ptr(), out.data_ptr(), rows, tokens, top_k, hidden, st)
+    status = _queue(lib().moe_combine_fwd, dev.index, stream, _ptr(expert_out) if rows else None,
+                    _code(expert_out, "expert_out"), row_of.data_ptr(), out.data_ptr(), rows, tokens, top_k, hidden)
     _check(status, "moe_combine_fwd")
 
 

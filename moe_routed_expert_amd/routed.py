@@ -26,7 +26,7 @@ import ctypes
 import torch
 
 from . import binding
-from .binding import DTYPE_CODE, MoeEpiError
+from .binding import DTYPE_CODE, MoeEpiError, _handle, _on
 
 _BF16, _F32, _I32, _I64, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.int8
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -104,12 +104,6 @@ def _optional(t, name: str, dtype, rows: int, device: int):
     return t.data_ptr()
 
 
-def _stream(device: int, stream) -> int:
-    if stream is None:
-        return _raw_stream(device)
-    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-
-
 def _fail(status: int, where: str) -> None:
     raise MoeEpiError(status, where)
 
@@ -145,9 +139,9 @@ def moe_sort_fwd(expert_of, first_expert: int, offs, row_of, slot_of, workspace=
         if not (workspace.dtype is torch.uint8 and workspace.get_device() == dev and workspace.is_contiguous()):
             _refuse(dev, (workspace, "workspace", torch.uint8, None))
         ws = workspace.data_ptr()
-    status = (_fns or _lib()).moe_sort_fwd(
-        expert_of.data_ptr(), 8 if dt is _I64 else 4, first_expert, offs.data_ptr(), row_of.data_ptr(),
-        slot_of.data_ptr(), ws, nbytes, tokens, top_k, experts, _stream(dev, stream))
+    handle = _raw_stream(dev) if stream is None else _handle(stream, dev)
+    status = _on(dev, (_fns or _lib()).moe_sort_fwd, expert_of.data_ptr(), 8 if dt is _I64 else 4, first_expert,
+                 offs.data_ptr(), row_of.data_ptr(), slot_of.data_ptr(), ws, nbytes, tokens, top_k, experts, handle)
     if status:
         _fail(status, "moe_sort_fwd")
 
@@ -176,8 +170,9 @@ def moe_dispatch_fwd(x, slot_of, top_k: int, out, stream=None) -> None:
             and out is not None and out.dtype is dt and out.get_device() == dev and out.shape == (rows, hidden)
             and out.is_contiguous()):
         _refuse(dev, (x, "x", dt, None), (slot_of, "slot_of", _I32, None), (out, "out", dt, (rows, hidden)))
-    status = (_fns or _lib()).moe_dispatch_fwd(x.data_ptr(), code, slot_of.data_ptr(), out.data_ptr(), rows, tokens,
-                                               top_k, hidden, _stream(dev, stream))
+    handle = _raw_stream(dev) if stream is None else _handle(stream, dev)
+    status = _on(dev, (_fns or _lib()).moe_dispatch_fwd, x.data_ptr(), code, slot_of.data_ptr(), out.data_ptr(), rows,
+                 tokens, top_k, hidden, handle)
     if status:
         _fail(status, "moe_dispatch_fwd")
 
@@ -194,8 +189,9 @@ def moe_dispatch_bwd(grad_out, row_of, grad_x, stream=None) -> None:
             and grad_x.shape == (tokens, hidden) and grad_x.is_contiguous()):
         _refuse(dev, (grad_out, "grad_out", dt, None), (row_of, "row_of", _I32, None),
                 (grad_x, "grad_x", dt, (tokens, hidden)))
-    status = (_fns or _lib()).moe_dispatch_bwd(grad_out.data_ptr(), code, row_of.data_ptr(), grad_x.data_ptr(), rows,
-                                               tokens, top_k, hidden, _stream(dev, stream))
+    handle = _raw_stream(dev) if stream is None else _handle(stream, dev)
+    status = _on(dev, (_fns or _lib()).moe_dispatch_bwd, grad_out.data_ptr(), code, row_of.data_ptr(),
+                 grad_x.data_ptr(), rows, tokens, top_k, hidden, handle)
     if status:
         _fail(status, "moe_dispatch_bwd")
 
@@ -214,9 +210,9 @@ def moe_combine_weighted_fwd(expert_out, row_of, weights, out, stream=None) -> N
             and out.get_device() == dev and out.shape == (tokens, hidden) and out.is_contiguous()):
         _refuse(dev, (expert_out, "expert_out", expert_out.dtype, None), (row_of, "row_of", _I32, None),
                 (weights, "weights", _F32, (tokens, top_k)), (out, "out", out.dtype, (tokens, hidden)))
-    status = (_fns or _lib()).moe_combine_weighted_fwd(
-        expert_out.data_ptr(), code, row_of.data_ptr(), weights.data_ptr(), out.data_ptr(), out_code, rows, tokens,
-        top_k, hidden, _stream(dev, stream))
+    handle = _raw_stream(dev) if stream is None else _handle(stream, dev)
+    status = _on(dev, (_fns or _lib()).moe_combine_weighted_fwd, expert_out.data_ptr(), code, row_of.data_ptr(),
+                 weights.data_ptr(), out.data_ptr(), out_code, rows, tokens, top_k, hidden, handle)
     if status:
         _fail(status, "moe_combine_weighted_fwd")
 
@@ -247,9 +243,10 @@ def moe_combine_weighted_bwd(grad_out, expert_out, row_of, weights, grad_expert_
                 and grad_weights.shape == slots and grad_weights.is_contiguous()):
             _refuse(dev, (expert_out, "expert_out", dt, (rows, hidden)), (grad_weights, "grad_weights", _F32, slots))
         eo, gw = expert_out.data_ptr(), grad_weights.data_ptr()
-    status = (_fns or _lib()).moe_combine_weighted_bwd(
-        grad_out.data_ptr(), grad_code, eo, code, row_of.data_ptr(), weights.data_ptr(), grad_expert_out.data_ptr(),
-        gw, rows, tokens, top_k, hidden, _stream(dev, stream))
+    handle = _raw_stream(dev) if stream is None else _handle(stream, dev)
+    status = _on(dev, (_fns or _lib()).moe_combine_weighted_bwd, grad_out.data_ptr(), grad_code, eo, code,
+                 row_of.data_ptr(), weights.data_ptr(), grad_expert_out.data_ptr(), gw, rows, tokens, top_k, hidden,
+                 handle)
     if status:
         _fail(status, "moe_combine_weighted_bwd")
 
@@ -315,8 +312,9 @@ def quantize_rows_int8_fwd(x, q, scale, stream=None) -> None:
             and scale is not None and scale.dtype is _F32 and scale.get_device() == dev and scale.shape == (rows,)
             and scale.is_contiguous()):
         _refuse(dev, (x, "x", x.dtype, None), (q, "q", _I8, (rows, cols)), (scale, "scale", _F32, (rows,)))
-    status = (_fns or _lib()).quantize_rows_int8_fwd(x.data_ptr(), code, q.data_ptr(), scale.data_ptr(), rows, cols,
-                                                     _stream(dev, stream))
+    handle = _raw_stream(dev) if stream is None else _handle(stream, dev)
+    status = _on(dev, (_fns or _lib()).quantize_rows_int8_fwd, x.data_ptr(), code, q.data_ptr(), scale.data_ptr(), rows,
+                 cols, handle)
     if status:
         _fail(status, "quantize_rows_int8_fwd")
 
@@ -358,11 +356,11 @@ def grouped_gate_up_swiglu_int8_fwd(a, a_scale, slot_of, top_k: int, w_gate, w_g
                 (w_gate_scale, "w_gate_scale", _F32, channels), (w_up, "w_up", _I8, weight),
                 (w_up_scale, "w_up_scale", _F32, channels), (offs, "offs", _I32, (experts,)),
                 (y, "y", _BF16, (rows, inter)))
-    status = (_fns or _lib()).grouped_gate_up_swiglu_int8_fwd(
-        a.data_ptr(), a_scale.data_ptr(), _optional(slot_of, "slot_of", _I32, rows, dev), w_gate.data_ptr(),
-        w_gate_scale.data_ptr(), w_up.data_ptr(), w_up_scale.data_ptr(), offs.data_ptr(),
-        _optional(probs, "probs", _F32, rows, dev), y.data_ptr(), rows, tokens, top_k, hidden, inter, experts, limit,
-        _stream(dev, stream))
+    handle = _raw_stream(dev) if stream is None else _handle(stream, dev)
+    status = _on(dev, (_fns or _lib()).grouped_gate_up_swiglu_int8_fwd, a.data_ptr(), a_scale.data_ptr(),
+                 _optional(slot_of, "slot_of", _I32, rows, dev), w_gate.data_ptr(), w_gate_scale.data_ptr(),
+                 w_up.data_ptr(), w_up_scale.data_ptr(), offs.data_ptr(), _optional(probs, "probs", _F32, rows, dev),
+                 y.data_ptr(), rows, tokens, top_k, hidden, inter, experts, limit, handle)
     if status:
         _fail(status, "grouped_gate_up_swiglu_int8_fwd")
 
@@ -390,9 +388,10 @@ def grouped_down_router_int8_fwd(h, h_scale, w_down, w_down_scale, offs, probs, 
                 (w_down, "w_down", _I8, (experts, hidden, inter)),
                 (w_down_scale, "w_down_scale", _F32, (experts, hidden)), (offs, "offs", _I32, (experts,)),
                 (out, "out", out.dtype, (rows, hidden)))
-    status = (_fns or _lib()).grouped_down_router_int8_fwd(
-        h.data_ptr(), h_scale.data_ptr(), w_down.data_ptr(), w_down_scale.data_ptr(), offs.data_ptr(),
-        _optional(probs, "probs", _F32, rows, dev), out.data_ptr(), DTYPE_CODE[out.dtype], rows, inter, hidden,
-        experts, _stream(dev, stream))
+    handle = _raw_stream(dev) if stream is None else _handle(stream, dev)
+    status = _on(dev, (_fns or _lib()).grouped_down_router_int8_fwd, h.data_ptr(), h_scale.data_ptr(),
+                 w_down.data_ptr(), w_down_scale.data_ptr(), offs.data_ptr(),
+                 _optional(probs, "probs", _F32, rows, dev), out.data_ptr(), DTYPE_CODE[out.dtype], rows, inter, hidden,
+                 experts, handle)
     if status:
         _fail(status, "grouped_down_router_int8_fwd")

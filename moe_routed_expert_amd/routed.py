@@ -67,7 +67,13 @@ def _refuse(device: int, *tensors) -> None:
     raise ValueError(f"expected tensors on {where}")
 
 
+def _missing(name: str) -> None:
+    raise ValueError(f"{name} is required")
+
+
 def _code(t: torch.Tensor, name: str) -> int:
+    if t is None:
+        _missing(name)
     code = DTYPE_CODE.get(t.dtype)
     if code is None:
         raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
@@ -75,6 +81,8 @@ def _code(t: torch.Tensor, name: str) -> int:
 
 
 def _matrix(t: torch.Tensor, name: str):
+    if t is None:
+        _missing(name)
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D, got {tuple(shape)}")
@@ -82,6 +90,8 @@ def _matrix(t: torch.Tensor, name: str):
 
 
 def _vector(t: torch.Tensor, name: str) -> int:
+    if t is None:
+        _missing(name)
     shape = t.shape
     if len(shape) != 1:
         raise ValueError(f"{name} must be 1-D, got {tuple(shape)}")
@@ -89,6 +99,8 @@ def _vector(t: torch.Tensor, name: str) -> int:
 
 
 def _experts(w: torch.Tensor, name: str):
+    if w is None:
+        _missing(name)
     shape = w.shape
     if len(shape) != 3:
         raise ValueError(f"{name} must be 3-D [experts, out, in], got {tuple(shape)}")
@@ -373,6 +385,8 @@ def grouped_down_router_int8_fwd(h, h_scale, w_down, w_down_scale, offs, probs, 
     rows, inter = _matrix(h, "h")
     weight = experts, hidden, _ = _experts(w_down, "w_down")
     dev = h.get_device()
+    if out is None:
+        _missing("out")
     if out.dtype is not _BF16 and out.dtype is not _F32:
         raise TypeError(f"out: expected bfloat16 or float32, got {out.dtype}")
     if not (dev >= 0 and h.dtype is _I8 and h.is_contiguous()

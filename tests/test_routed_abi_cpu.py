@@ -285,3 +285,29 @@ def test_binding_passes_only_tensors_that_fit(name, monkeypatch):
     with pytest.raises((TypeError, ValueError)):
         call(tensors)
     assert len(reached) == 1                       # the library was never reached again
+
+
+OPTIONAL = {("moe_sort_fwd", 4), ("moe_combine_weighted_bwd", 5), ("grouped_gate_up_swiglu_int8_fwd", 2),
+            ("grouped_gate_up_swiglu_int8_fwd", 8), ("grouped_down_router_int8_fwd", 5)}
+
+
+@pytest.mark.parametrize("name", sorted(TENSORS))
+def test_binding_names_a_tensor_that_is_missing(name, monkeypatch):
+    """None in the place of a tensor that a call cannot do without is a ValueError, whichever one it is."""
+    class Library:
+        def __getattr__(self, call):
+            return lambda *args: 0
+
+    monkeypatch.setattr(routed, "_fns", Library())
+    monkeypatch.setattr(routed, "_raw_stream", lambda device: 0)
+    specs, others = TENSORS[name]
+    for i in range(len(specs)):
+        args = [Tensor(*s) for s in specs]
+        args[i] = None
+        for at in sorted(others):
+            args.insert(at, others[at])
+        if (name, i) in OPTIONAL:
+            getattr(routed, name)(*args)
+        else:
+            with pytest.raises(ValueError, match="is required"):
+                getattr(routed, name)(*args)

@@ -61,6 +61,25 @@ def combine_grads(grad, rows, row_of, weights):
     return grad_rows, grad_weights, scale
 
 
+def quantize(x):
+    """scale and q of rows of storage values, in float32: each row brought to a maximum near 1 by a power of two
+    (exact), then one rounding of 127 x, one of the quotient, and one to an integer, ties to even."""
+    amax = np.abs(x).max(1, keepdims=True)
+    live = amax > 0
+    e = np.frexp(np.where(live, amax, 1.0))[1]
+    unit, most = np.ldexp(x, -e).astype(np.float32), np.ldexp(np.where(live, amax, 1.0), -e).astype(np.float32)
+    q = np.rint(np.float32(127) * unit / most).astype(np.int8)
+    return q, (amax[:, 0].astype(np.float32) / np.float32(127)).astype(np.float32)
+
+
+def tie_rows(dtype):
+    """Rows whose elements lie exactly between two integers: odd multiples of max / 254, where the reciprocal of the
+    maximum is exact (254) and where it is not (254 * 3, 5 and 7, which bfloat16 does not hold)."""
+    odd = 2 * np.arange(-127, 127) + 1
+    return [np.concatenate([[254.0 * m], odd * m, [-254.0 * m]])
+            for m in ((1,) if dtype == torch.bfloat16 else (1, 3, 5, 7))]
+
+
 def bounds(offs, rows):
     """[start, end) of each expert's rows."""
     start = 0

@@ -437,6 +437,42 @@ def test_down_product(counts, k, n, extra):
 @pytest.mark.parametrize("gathered", [False, True])
 def test_gate_up_product(counts, k, n, gathered):
     rng = np.random.default_rng(k + 2 * n)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", [256, 264, 271, 520, 1032, 2056, 4104, 9001, 16392])
+def test_quantize_rounds_as_the_division_does(dtype, cols):
+    """Every integer is that of the division in float32, ties to even among them, in vectors and in a row's last
+    elements, aligned or not, with the lanes of few rows and of many."""
+    rng = np.random.default_rng(cols + 13)
+    rows = 600
+    x = rng.standard_normal((rows, cols)) * 10.0 ** rng.integers(-3, 3, (rows, 1))
+    t = torch.from_numpy(x.astype(np.float32)).to(dtype)
+    for i, tie in enumerate(ref.tie_rows(dtype)):
+        tie = torch.from_numpy(tie).to(dtype)
+        t[i, :256] = tie
+        t[i, 256:] = tie.repeat(cols // 256 + 1)[:cols][256:]
+        t[8 + i] = t[i].roll(cols - 256)          # the ties at the end of the row
+    want_q, want_scale = ref.quantize(ref.f64(t))
+    t = t.cuda()
+    for offset in (0, 1):
+        for n in (23, rows):                      # up to 512 rows take more lanes each
+            q, scale = sentinel((n, cols), torch.int8, offset), sentinel((n,), torch.float32)
+            epi.quantize_rows_int8_fwd(placed(t[:n], offset), q, scale)
+            assert np.array_equal(q.cpu().numpy(), want_q[:n])
+            assert np.array_equal(scale.cpu().numpy().view(np.uint32), want_scale[:n].view(np.uint32))
+
+
+@pytest.mark.parametrize("cols,rows", [(8, 16_800_003), (4104, 1_050_007)])
+def test_quantize_more_rows_than_a_grid_has_blocks(cols, rows):
+    """2^20 blocks at most: each goes on to further rows, within a wavefront and with a block for a row."""
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda").normal_()
+    q, scale = epi.quantize_rows_int8(x)
+    for r0 in range(0, rows, 1 << 16):
+        v = x[r0:r0 + (1 << 16)].float()
+        most = v.abs().amax(1)
+        assert torch.equal(bits(scale[r0:r0 + (1 << 16)]), bits(most / torch.full_like(most, 127)))
+        assert torch.equal(q[r0:r0 + (1 << 16)], torch.round(127 * v / most[:, None]).to(torch.int8))
+
+
     offs = np.cumsum(counts).astype(np.int32)
     rows, extra = int(offs[-1]), 2
     top_k = 3 if gathered else 1

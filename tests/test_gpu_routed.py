@@ -389,6 +389,30 @@ def test_quantize_ties_to_even_and_rows_that_are_not_finite():
     assert q[2:].abs().max() == 0 and bool(torch.isnan(scale[2:]).all()) and bool(torch.isfinite(scale[:2]).all())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", [256, 264, 271, 520, 1032, 2056, 4104, 9001, 16392])
+def test_quantize_rounds_as_the_division_does(dtype, cols):
+    """Every integer is that of the division in float32, ties to even among them, in vectors and in a row's last
+    elements, aligned or not, with the lanes of few rows and of many."""
+    rng = np.random.default_rng(cols + 13)
+    rows = 600
+    x = rng.standard_normal((rows, cols)) * 10.0 ** rng.integers(-3, 3, (rows, 1))
+    t = torch.from_numpy(x.astype(np.float32)).to(dtype)
+    for i, tie in enumerate(ref.tie_rows(dtype)):
+        tie = torch.from_numpy(tie).to(dtype)
+        t[i, :256] = tie
+        t[i, 256:] = tie.repeat(cols // 256 + 1)[:cols][256:]
+        t[8 + i] = t[i].roll(cols - 256)          # the ties at the end of the row
+    want_q, want_scale = ref.quantize(ref.f64(t))
+    t = t.cuda()
+    for offset in (0, 1):
+        for n in (23, rows):                      # up to 512 rows take more lanes each
+            q, scale = sentinel((n, cols), torch.int8, offset), sentinel((n,), torch.float32)
+            epi.quantize_rows_int8_fwd(placed(t[:n], offset), q, scale)
+            assert np.array_equal(q.cpu().numpy(), want_q[:n])
+            assert np.array_equal(scale.cpu().numpy().view(np.uint32), want_scale[:n].view(np.uint32))
+
+
 # ---- products in 8-bit integers -----------------------------------------------------------------
 
 def int8_of(rng, shape):
@@ -437,42 +461,6 @@ def test_down_product(counts, k, n, extra):
 @pytest.mark.parametrize("gathered", [False, True])
 def test_gate_up_product(counts, k, n, gathered):
     rng = np.random.default_rng(k + 2 * n)
-@pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("cols", [256, 264, 271, 520, 1032, 2056, 4104, 9001, 16392])
-def test_quantize_rounds_as_the_division_does(dtype, cols):
-    """Every integer is that of the division in float32, ties to even among them, in vectors and in a row's last
-    elements, aligned or not, with the lanes of few rows and of many."""
-    rng = np.random.default_rng(cols + 13)
-    rows = 600
-    x = rng.standard_normal((rows, cols)) * 10.0 ** rng.integers(-3, 3, (rows, 1))
-    t = torch.from_numpy(x.astype(np.float32)).to(dtype)
-    for i, tie in enumerate(ref.tie_rows(dtype)):
-        tie = torch.from_numpy(tie).to(dtype)
-        t[i, :256] = tie
-        t[i, 256:] = tie.repeat(cols // 256 + 1)[:cols][256:]
-        t[8 + i] = t[i].roll(cols - 256)          # the ties at the end of the row
-    want_q, want_scale = ref.quantize(ref.f64(t))
-    t = t.cuda()
-    for offset in (0, 1):
-        for n in (23, rows):                      # up to 512 rows take more lanes each
-            q, scale = sentinel((n, cols), torch.int8, offset), sentinel((n,), torch.float32)
-            epi.quantize_rows_int8_fwd(placed(t[:n], offset), q, scale)
-            assert np.array_equal(q.cpu().numpy(), want_q[:n])
-            assert np.array_equal(scale.cpu().numpy().view(np.uint32), want_scale[:n].view(np.uint32))
-
-
-@pytest.mark.parametrize("cols,rows", [(8, 16_800_003), (4104, 1_050_007)])
-def test_quantize_more_rows_than_a_grid_has_blocks(cols, rows):
-    """2^20 blocks at most: each goes on to further rows, within a wavefront and with a block for a row."""
-    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda").normal_()
-    q, scale = epi.quantize_rows_int8(x)
-    for r0 in range(0, rows, 1 << 16):
-        v = x[r0:r0 + (1 << 16)].float()
-        most = v.abs().amax(1)
-        assert torch.equal(bits(scale[r0:r0 + (1 << 16)]), bits(most / torch.full_like(most, 127)))
-        assert torch.equal(q[r0:r0 + (1 << 16)], torch.round(127 * v / most[:, None]).to(torch.int8))
-
-
     offs = np.cumsum(counts).astype(np.int32)
     rows, extra = int(offs[-1]), 2
     top_k = 3 if gathered else 1
@@ -543,6 +531,30 @@ def test_offs_out_of_order_or_past_the_rows_are_clamped():
         want, slack = ref.down(h.cpu().numpy(), sh.cpu().numpy(), w.cpu().numpy(), sw.cpu().numpy(), offs,
                                np.ones(50, np.float32))
         check(out, want, slack, torch.float32, "down")
+
+
+@pytest.mark.parametrize("counts,n", [([7], 16), ([40, 0, 35], 16), ([30, 0, 25, 31, 64, 17] * 7, 520),
+                                      ([100, 128, 1, 0, 140, 129] * 7, 520), ([300, 256, 257, 1, 512, 0] * 7, 776)])
+def test_gate_up_of_no_tokens_gives_rows_of_zeros(counts, n):
+    """Without tokens every slot is out of range: y = 0 * probs below the last expert's end, by every kernel."""
+    rng = np.random.default_rng(n)
+    offs, k, top_k = np.cumsum(counts).astype(np.int32), 144, 2
+    rows, extra = int(offs[-1]), 2
+    w, s = int8_of(rng, (len(counts), n, k)), scales(rng, (len(counts), n), 1.0)
+    p = torch.from_numpy(rng.random(rows + extra).astype(np.float32)).cuda()
+    p[3] = float("inf")
+    none, no_scale = torch.empty((0, k), dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda")
+    for probs in (None, p):
+        y = sentinel((rows + extra, n), torch.bfloat16)
+        kept = bits(y[rows:].clone())
+        epi.grouped_gate_up_swiglu_int8_fwd(none, no_scale, ints(rng.integers(-2, 50, rows + extra)), top_k, w, s, w, s,
+                                            ints(offs), probs, y, 7.0)
+        zeros = y[:rows].float()
+        if probs is not None:
+            assert bool(torch.isnan(zeros[3]).all())
+            zeros[3] = 0.0
+        assert bool((zeros == 0).all())
+        assert torch.equal(bits(y[rows:]), kept)
 
 
 def test_tokens_past_two_and_four_gigabytes():
@@ -637,30 +649,6 @@ def test_chain_replayed_from_a_graph_equals_eager():
     assert same(c.outs, want)                     # the same on another stream
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-@pytest.mark.parametrize("counts,n", [([7], 16), ([40, 0, 35], 16), ([30, 0, 25, 31, 64, 17] * 7, 520),
-                                      ([100, 128, 1, 0, 140, 129] * 7, 520), ([300, 256, 257, 1, 512, 0] * 7, 776)])
-def test_gate_up_of_no_tokens_gives_rows_of_zeros(counts, n):
-    """Without tokens every slot is out of range: y = 0 * probs below the last expert's end, by every kernel."""
-    rng = np.random.default_rng(n)
-    offs, k, top_k = np.cumsum(counts).astype(np.int32), 144, 2
-    rows, extra = int(offs[-1]), 2
-    w, s = int8_of(rng, (len(counts), n, k)), scales(rng, (len(counts), n), 1.0)
-    p = torch.from_numpy(rng.random(rows + extra).astype(np.float32)).cuda()
-    p[3] = float("inf")
-    none, no_scale = torch.empty((0, k), dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda")
-    for probs in (None, p):
-        y = sentinel((rows + extra, n), torch.bfloat16)
-        kept = bits(y[rows:].clone())
-        epi.grouped_gate_up_swiglu_int8_fwd(none, no_scale, ints(rng.integers(-2, 50, rows + extra)), top_k, w, s, w, s,
-                                            ints(offs), probs, y, 7.0)
-        zeros = y[:rows].float()
-        if probs is not None:
-            assert bool(torch.isnan(zeros[3]).all())
-            zeros[3] = 0.0
-        assert bool((zeros == 0).all())
-        assert torch.equal(bits(y[rows:]), kept)
-
-
         c.step()
     noise = torch.randn(256, 256, device="cuda")
     for _ in range(3):

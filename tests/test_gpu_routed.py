@@ -103,6 +103,18 @@ def test_sort(dtype, tokens, top_k, experts, first, local):
     assert np.array_equal(slot_of.cpu(), slot_w)
 
 
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("tokens,top_k,experts,first,local", [(131072, 8, 256, 0, 256), (75001, 8, 1024, 20, 1000),
+                                                              (90007, 7, 300, 11, 60)])
+def test_sort_of_long_calls_with_many_experts(dtype, tokens, top_k, experts, first, local):
+    """Four groups a wavefront, and more counts than each block reads for itself: a launch of its own sums them."""
+    rng = np.random.default_rng(tokens)
+    ids = rng.integers(0, experts, (tokens, top_k)).astype(np.int32)
+    want = ref.sort(ids, first, local)
+    for got, w in zip(epi.moe_sort(torch.from_numpy(ids).to(dtype).cuda(), local, first), want):
+        assert np.array_equal(got.cpu(), w)
+
+
 @pytest.mark.parametrize("tokens", [40, 3000])
 def test_sort_of_uneven_and_foreign_experts(tokens):
     """One expert for all; repeats within a token; ids that are negative, past the last or far out."""
@@ -328,6 +340,42 @@ def test_calls_with_no_rows_or_no_tokens(dtype):
     assert bool((xg.grad == 0).all()) and bool((wg.grad == 0).all())
 
 
+def shuffled(n):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n)
+    return torch.randperm(n, generator=g, device="cuda").to(torch.int32)
+
+
+@pytest.mark.parametrize("hidden,tokens", [(264, 1_100_003), (1, 33_600_001), (8, 33_600_001)])
+def test_moves_of_more_rows_than_a_grid_has_blocks(hidden, tokens):
+    """2^20 blocks at most: each of them goes on to further rows or tokens, whole rows and narrow ones."""
+    x = torch.empty((tokens, hidden), dtype=torch.bfloat16, device="cuda").normal_()
+    row_of = shuffled(tokens).view(tokens, 1)
+    weights = torch.rand((tokens, 1), device="cuda") + 0.5
+    at = row_of[:, 0].long()
+    out = sentinel((tokens, hidden), torch.bfloat16)
+    epi.moe_dispatch_bwd(x, row_of, out)
+    assert torch.equal(out, x[at])
+    epi.moe_combine_weighted_fwd(x, row_of, weights, out)
+    assert torch.equal(out, (x[at].float() * weights).bfloat16())
+    rows, grad_w = sentinel((tokens, hidden), torch.bfloat16), sentinel((tokens, 1), torch.float32)
+    epi.moe_combine_weighted_bwd(out, x, row_of, weights, rows, grad_w)
+    assert torch.equal(rows[at], (out.float() * weights).bfloat16())
+    for t0 in range(0, tokens, 1 << 22):
+        here = slice(t0, t0 + (1 << 22))
+        terms = out[here].double() * x[at[here]].double()
+        assert bool(((grad_w[here, 0] - terms.sum(1)).abs() <= (hidden + 8) * ref.EPS * terms.abs().sum(1)).all())
+
+
+@pytest.mark.parametrize("hidden,rows", [(264, 1_100_003), (1, 134_300_001)])
+def test_dispatch_of_more_rows_than_a_grid_has_blocks(hidden, rows):
+    x = torch.empty((1001, hidden), dtype=torch.bfloat16, device="cuda").normal_()
+    slot_of = torch.randint(0, 1001, (rows,), dtype=torch.int32, device="cuda")
+    out = sentinel((rows, hidden), torch.bfloat16)
+    epi.moe_dispatch_fwd(x, slot_of, 1, out)
+    assert torch.equal(out, x[slot_of])
+
+
 # ---- 8-bit rows ---------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -411,6 +459,18 @@ def test_quantize_rounds_as_the_division_does(dtype, cols):
             epi.quantize_rows_int8_fwd(placed(t[:n], offset), q, scale)
             assert np.array_equal(q.cpu().numpy(), want_q[:n])
             assert np.array_equal(scale.cpu().numpy().view(np.uint32), want_scale[:n].view(np.uint32))
+
+
+@pytest.mark.parametrize("cols,rows", [(8, 16_800_003), (4104, 1_050_007)])
+def test_quantize_more_rows_than_a_grid_has_blocks(cols, rows):
+    """2^20 blocks at most: each goes on to further rows, within a wavefront and with a block for a row."""
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda").normal_()
+    q, scale = epi.quantize_rows_int8(x)
+    for r0 in range(0, rows, 1 << 16):
+        v = x[r0:r0 + (1 << 16)].float()
+        most = v.abs().amax(1)
+        assert torch.equal(bits(scale[r0:r0 + (1 << 16)]), bits(most / torch.full_like(most, 127)))
+        assert torch.equal(q[r0:r0 + (1 << 16)], torch.round(127 * v / most[:, None]).to(torch.int8))
 
 
 # ---- products in 8-bit integers -----------------------------------------------------------------

@@ -138,7 +138,11 @@ int quantize_rows_int8_fwd(const void *x, int dtype, int8_t *q, float *scale, in
  * The sums are exact 32-bit integers (a hidden below 131072 keeps them so), the
  * rest is float32, rounded once. slot_of == NULL: u = r, tokens == rows, top_k == 1.
  * A row whose slot is outside [0, tokens * top_k) gives y = 0 * probs[r]. Rows
- * at or past the last end are not written.
+ * at or past the last end are not written. `rows` is what the tensors hold; how
+ * many of them there are stands in offs, on the device, which the host does not
+ * read. The results do not depend on rows beyond that, the time may: the kernel
+ * is chosen by rows / experts, so tensors several times larger than the rows
+ * they have get one made for more rows.
  *   a            [tokens, hidden] int8             in (may be NULL if tokens == 0)
  *   a_scale      [tokens] float32                  in (may be NULL if tokens == 0)
  *   slot_of      [rows] int32 or NULL              in

@@ -286,7 +286,9 @@ class MoeDispatch(torch.autograd.Function):
 
 class MoeCombineWeighted(torch.autograd.Function):
     """The weighted sum of each token's rows: MoeCombineWeighted.apply(expert_out, row_of, weights,
-    out_dtype=None). expert_out is kept for the backward pass only when weights need a gradient."""
+    out_dtype=None). expert_out is kept for the backward pass only when weights need a gradient. The
+    backward pass fills the rows' gradient with zeros before the kernel writes the rows that have a slot
+    (65536 rows of 7168 bf16: 138 us beside 444)."""
 
     @staticmethod
     def forward(ctx, expert_out, row_of, weights, out_dtype=None):

@@ -338,7 +338,7 @@ def quantize_rows_int8(x):
     [experts, out, in] get a scale for each output channel."""
     q = torch.empty(x.shape, dtype=_I8, device=x.device)
     scale = torch.empty(x.shape[:-1], dtype=_F32, device=x.device)
-    quantize_rows_int8_fwd(x.reshape(-1, x.shape[-1]), q.view(-1, x.shape[-1]), scale.view(-1))
+    quantize_rows_int8_fwd(x.reshape(-1, x.shape[-1]).contiguous(), q.view(-1, x.shape[-1]), scale.view(-1))
     return q, scale
 
 

@@ -311,3 +311,18 @@ def test_binding_names_a_tensor_that_is_missing(name, monkeypatch):
         else:
             with pytest.raises(ValueError, match="is required"):
                 getattr(routed, name)(*args)
+
+
+@pytest.mark.parametrize("strided", [lambda t: t.t(), lambda t: t[:, 1:5], lambda t: t.view(2, 4, 8).transpose(1, 2),
+                                     lambda t: t.view(2, 4, 8)[:, :, ::2], lambda t: t[3]])
+def test_quantize_helper_takes_any_strides(strided, monkeypatch):
+    """The call gets contiguous rows with the same values, however the leading dimensions and the columns lie."""
+    got = []
+    monkeypatch.setattr(routed, "quantize_rows_int8_fwd", lambda x, q, scale: got.append((x, q, scale)))
+    t = strided(torch.arange(64.0).view(8, 8))
+    q, scale = routed.quantize_rows_int8(t)
+    (x, q2, scale2), = got
+    assert x.is_contiguous() and q2.is_contiguous() and torch.equal(x.view(t.shape), t)
+    assert x.shape == q2.shape and scale2.shape == x.shape[:1]
+    assert q.shape == t.shape and scale.shape == t.shape[:-1]
+    assert q.data_ptr() == q2.data_ptr() and scale.data_ptr() == scale2.data_ptr()

@@ -269,6 +269,8 @@ class MoeDispatch(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, row_of, slot_of):
+        if row_of.shape[0] != x.shape[0]:          # the order of other tokens
+            raise ValueError(f"row_of: expected {x.shape[0]} tokens as x has, got {row_of.shape[0]}")
         ctx.save_for_backward(row_of)
         ctx.tokens = x.shape[0]
         out = torch.empty((slot_of.shape[0], x.shape[1]), dtype=x.dtype, device=x.device)

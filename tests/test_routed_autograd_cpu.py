@@ -96,3 +96,13 @@ def test_gradients_that_depend_on_an_input_are_refused_and_others_are_right():
         assert torch.allclose(got, want, rtol=1e-5, atol=1e-6)
         got, want = (torch.autograd.grad(g.pow(2).sum(), used)[0] for g in (got, want))
         assert torch.allclose(got, want, rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("tokens", [3, 5])
+def test_a_dispatch_of_other_tokens_than_the_orders_is_refused(tokens):
+    """Its backward pass would be refused; the forward pass alone must not answer with other tokens' rows."""
+    x, = leaves((tokens, 5))
+    with pytest.raises(ValueError, match=f"row_of.*{tokens}"):
+        routed.MoeDispatch.apply(x, ROW_OF, SLOT_OF)
+    with pytest.raises(ValueError, match="row_of"):
+        routed.MoeDispatch.apply(x.detach(), ROW_OF, SLOT_OF)

@@ -7,6 +7,7 @@
 namespace moe_epi {
 namespace {
 
+constexpr int kBlock = 256;
 constexpr int kMostExperts = 1024, kMostGroups = 64, kMostChosen = 64;
 constexpr float kInf = __builtin_inff();
 
@@ -16,158 +17,534 @@ struct Choice {
     float scale;
 };
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
-    return v;
-}
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-    return v;
-}
-__device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-static_cast<double>(l))); }
+// ---- over the L lanes of a token -------------------------------------------------
 
-// One wavefront per token. An expert's place is the number of experts that come before it.
+// The lane's partner in step `kXor` (1, 2, 4, 8, 16, 32) of an exchange that
+// leaves every lane of an aligned group of 2 kXor with the group's result: the
+// steps up to 8 mirror quads, halves and rows of 16 lanes, without LDS.
+template <int kXor>
+__device__ __forceinline__ int partner(int v) {
+    if constexpr (kXor == 1)
+        return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, true);
+    else if constexpr (kXor == 2)
+        return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, true);
+    else if constexpr (kXor == 4)
+        return __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);
+    else if constexpr (kXor == 8)
+        return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);
+    else
+        return __shfl_xor(v, kXor, 64);
+}
+template <int kXor>
+__device__ __forceinline__ float partner(float v) {
+    return __int_as_float(partner<kXor>(__float_as_int(v)));
+}
+template <int kXor>
+__device__ __forceinline__ double partner(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = static_cast<uint32_t>(partner<kXor>(static_cast<int>(u)));
+    const uint32_t hi = static_cast<uint32_t>(partner<kXor>(static_cast<int>(u >> 32)));
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+template <int L, int kXor = 1, class V, class F>
+__device__ __forceinline__ V over_lanes(V v, F f) {
+    if constexpr (kXor < L)
+        return over_lanes<L, 2 * kXor>(f(v, partner<kXor>(v)), f);
+    else
+        return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+    return over_lanes<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int L, class V>
+__device__ __forceinline__ V lanes_sum(V v) {
+    return over_lanes<L>(v, [](V a, V b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ bool lanes_any(bool v) {
+    if constexpr (L == 64)
+        return __any(v);
+    else
+        return (__ballot(v) >> (threadIdx.x & 63 & ~(L - 1)) & ((1ull << L) - 1)) != 0;
+}
+
+// ---- keys ----------------------------------------------------------------------------
+//
+// A key is a float32 value as a float64, whose last 10 bits (of the 29 that the
+// value leaves free) are the expert's number, turned so that of equal values the
+// lowest expert has the largest key. -inf: not to be chosen.
+
+constexpr uint64_t kNumber = kMostExperts - 1;
+
+__device__ __forceinline__ double key_of(float value, int expert) {
+    if (!(value > -kInf)) return -kInf;  // NaN too
+    const double v = fmin(static_cast<double>(value) + 0.0, 0x1p1000);  // +0 for -0; a number for infinity
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, u | static_cast<uint64_t>(v >= 0 ? kNumber - expert : expert));
+}
+__device__ __forceinline__ int expert_of(double key) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, key);
+    const int n = static_cast<int>(u & kNumber);
+    return key == -kInf ? -1 : (u >> 63 ? n : static_cast<int>(kNumber) - n);
+}
+__device__ __forceinline__ double value_of(double key) {
+    return key == -kInf ? key : __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, key) & ~kNumber);
+}
+// One instruction each: keys are never NaN, so they need not be made quiet first.
+__device__ __forceinline__ double larger(double a, double b) {
+    double d;
+    asm("v_max_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+    return d;
+}
+__device__ __forceinline__ double smaller(double a, double b) {
+    double d;
+    asm("v_min_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+    return d;
+}
+// Descending, by Batcher's odd-even merge.
+template <int N>
+__device__ __forceinline__ void sort_keys(double (&key)[N]) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const double a = key[i + j], b = key[i + j + k];
+                        key[i + j] = larger(a, b);
+                        key[i + j + k] = smaller(a, b);
+                    }
+}
+
+// ---- scores ----------------------------------------------------------------------------
+
+__device__ __forceinline__ float sigmoid32(float l) {
+    const float e = expf(-fabsf(l));
+    return (l >= 0.0f ? 1.0f : e) / (1.0f + e);
+}
+// What a float32 score may be off. A sigmoid: four roundings of at most 1. A
+// softmax: 2^-24 of itself for |l - m| (m - l is at most log(experts) on average
+// over the scores, which the sum is off by, and at most 0.37 of the largest
+// score for the score itself) and for each of up to 22 additions, the quotient
+// and the exponentials: below 2^-18 of the largest score, 1 / sum.
+__device__ __forceinline__ double score_error(bool sigmoid, float sum) {
+    return sigmoid ? 0x1p-21 : 0x1p-18 / static_cast<double>(sum);
+}
+
 template <int T>
-__global__ __launch_bounds__(64) void route_kernel(const void* logits, const float* bias, int32_t* ids, float* weights,
-                                                   int64_t tokens, Choice p) {
-    __shared__ double c[kMostExperts], of_group[kMostGroups];
-    __shared__ int chosen[kMostChosen];
-    const int lane = threadIdx.x, size = p.experts / p.groups;
-    for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
-        auto logit = [&](int e) { return Elem<T>::load1(logits, t * p.experts + e); };
-        float m = -kInf;
-        bool bad = false;
-        for (int e = lane; e < p.experts; e += 64) {
-            const float l = logit(e);
-            bad |= l != l || (!p.sigmoid && l == kInf);
-            m = fmaxf(m, l);
-        }
-        m = wave_max(m);
-        bad = __any(bad);
-        double sum = 0.0;
-        if (!p.sigmoid) {
-            for (int e = lane; e < p.experts; e += 64) sum += exp(static_cast<double>(logit(e)) - m);
-            sum = wave_sum(sum);
-        }
-        auto score = [&](float l) {
-            return p.sigmoid ? sigmoid64(l) : exp(static_cast<double>(l) - m) / sum;
-        };
-        for (int e = lane; e < p.experts; e += 64) {
-            const float l = logit(e);
-            double v = bias ? score(l) + static_cast<double>(bias[e]) : static_cast<double>(l);
-            if (!(v > -kInf) || !(l > -kInf)) v = -kInf;  // NaN too
-            c[e] = v;
-        }
-        if (lane < kMostChosen) chosen[lane] = -1;
-        __syncthreads();
-        if (lane < p.groups) {
-            double a = -kInf, b = -kInf;
-            for (int i = 0; i < size; ++i) {
-                double v = c[lane * size + i];
-                if (p.top2 && !bias && v > -kInf) v = score(static_cast<float>(v));
-                if (v > a) {
-                    b = a;
-                    a = v;
-                } else if (v > b) {
-                    b = v;
-                }
+__device__ __forceinline__ float load_logit(const char* row, int e) {
+    return Elem<T>::load1(row, e);
+}
+// Experts e0 .. e0 + N - 1 of a row, -inf past the last.
+template <int T, int N>
+__device__ __forceinline__ void load_logits(const char* row, int e0, int experts, float (&l)[N]) {
+    constexpr int V = N < 4 ? N : 4;
+#pragma unroll
+    for (int i = 0; i < N; i += V) {
+        if (V == 4 && e0 + i + 4 <= experts) {
+            if constexpr (T == MOE_EPI_F32) {
+                typedef u32x4 loose __attribute__((aligned(4)));
+                const u32x4 w = *reinterpret_cast<const loose*>(row + 4 * (e0 + i));
+#pragma unroll
+                for (int j = 0; j < V; ++j) l[i + j] = __uint_as_float(w[j]);
+            } else {
+                typedef u32x2 loose __attribute__((aligned(2)));
+                const u32x2 w = *reinterpret_cast<const loose*>(row + 2 * (e0 + i));
+                float f[8];
+                Elem<T>::unpack(u32x4{w[0], w[1], 0, 0}, f);
+#pragma unroll
+                for (int j = 0; j < V; ++j) l[i + j] = f[j];
             }
-            of_group[lane] = p.top2 && p.groups > 1 ? a + b : a;
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) l[i + j] = e0 + i + j < experts ? load_logit<T>(row, e0 + i + j) : -kInf;
         }
-        __syncthreads();
-        bool keep = false;
-        if (lane < p.groups) {
-            int before = 0;
-            for (int g = 0; g < p.groups; ++g)
-                before += of_group[g] > of_group[lane] || (of_group[g] == of_group[lane] && g < lane);
-            keep = before < p.top_groups;
-        }
-        const uint64_t mask = __ballot(keep);
-        for (int e = lane; e < p.experts; e += 64) {
-            if (!(mask >> (e / size) & 1) || !(c[e] > -kInf)) continue;
-            int before = 0;
-            for (int i = 0; i < p.experts; ++i)
-                before += (mask >> (i / size) & 1) && (c[i] > c[e] || (c[i] == c[e] && i < e));
-            if (before < p.top_k) chosen[before] = e;
-        }
-        __syncthreads();
-        const int id = lane < p.top_k ? chosen[lane] : -1;
-        const float l = id >= 0 ? logit(id) : -kInf;
-        const float most = wave_max(l);
-        double w = 0.0;
-        if (id >= 0) {
-            if (!p.renormalise)
-                w = score(l);
-            else if (!p.sigmoid)
-                w = exp(static_cast<double>(l) - most);
-            else  // sigmoid(l) over e^min(most, 0), which does not underflow
-                w = exp(fmin(static_cast<double>(l), 0.0) - fmin(static_cast<double>(most), 0.0)) /
-                    (1.0 + exp(-fabs(static_cast<double>(l))));
-        }
-        if (p.renormalise) {
-            const double all = wave_sum(w);
-            w = id >= 0 ? w / all : 0.0;
-        }
-        if (lane < p.top_k) {
-            ids[t * p.top_k + lane] = id;
-            weights[t * p.top_k + lane] = bad ? __builtin_nanf("") : static_cast<float>(w * p.scale);
-        }
-        __syncthreads();
     }
 }
 
-template <int T>
-__global__ __launch_bounds__(64) void route_grad_kernel(const float* grad_weights, const void* logits,
-                                                        const int32_t* ids, void* grad_logits, int64_t tokens,
-                                                        Choice p) {
-    __shared__ double part[kMostChosen];
-    __shared__ int chosen[kMostChosen];
-    const int lane = threadIdx.x;
-    for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x) {
-        auto logit = [&](int64_t e) { return static_cast<double>(Elem<T>::load1(logits, t * p.experts + e)); };
-        int id = lane < p.top_k ? ids[t * p.top_k + lane] : -1;
-        if (id < 0 || id >= p.experts) id = -1;
-        const double u = id >= 0 ? static_cast<double>(grad_weights[t * p.top_k + lane]) * p.scale : 0.0;
-        const double l = id >= 0 ? logit(id) : -kInf;
-        double m = -kInf, sum = 0.0;
-        if (!p.sigmoid && !p.renormalise) {
-            for (int e = lane; e < p.experts; e += 64) m = fmax(m, logit(e));
-            m = static_cast<double>(wave_max(static_cast<float>(m)));
-            for (int e = lane; e < p.experts; e += 64) sum += m > -kInf ? exp(logit(e) - m) : 0.0;
-            sum = wave_sum(sum);
+// The groups (a bit each) that fewer than top_groups others come before. look(v, w): at each pair of their values.
+template <int L, class F>
+__device__ __forceinline__ uint64_t best_groups(const double* value, const Choice& p, int lane, F look) {
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+    uint64_t kept = 0;
+    for (int g = 0; g < p.groups; ++g) {
+        const double v = value[g];
+        int before = 0;
+        for (int o = lane; o < p.groups; o += L) {
+            const double w = value[o];
+            before += w > v || (w == v && o < g);
+            if (o != g) look(v, w);
         }
-        auto softmax = [&](double v) { return m > -kInf ? exp(v - m) / sum : 0.0; };
-        double d = 0.0, dot = 0.0;
-        if (p.renormalise) {
-            const double most = wave_max(static_cast<float>(l));
-            double v = 0.0;
-            if (id >= 0 && most > -kInf)
-                v = p.sigmoid ? exp(fmin(l, 0.0) - fmin(most, 0.0)) / (1.0 + exp(-fabs(l))) : exp(l - most);
-            const double all = wave_sum(v);
-            v = all > 0.0 || all != all ? v / all : 0.0;
-            dot = wave_sum(u * v);
-            d = id >= 0 ? v * (u - dot) : 0.0;
-            if (p.sigmoid && id >= 0) d *= 1.0 / (1.0 + exp(l));
-        } else if (p.sigmoid) {
-            const double s = 1.0 / (1.0 + exp(-l));
-            d = id >= 0 ? u * s / (1.0 + exp(l)) : 0.0;
-        } else {
-            dot = wave_sum(id >= 0 ? u * softmax(l) : 0.0);
-            d = u;
-        }
-        part[lane] = d;
-        chosen[lane] = id;
-        __syncthreads();
-        for (int e = lane; e < p.experts; e += 64) {
-            double g = 0.0;
-            for (int j = 0; j < p.top_k; ++j) g += chosen[j] == e ? part[j] : 0.0;
-            if (!p.sigmoid && !p.renormalise) g = softmax(logit(e)) * (g - dot);
-            Elem<T>::store1(grad_logits, t * p.experts + e, static_cast<float>(g));
-        }
-        __syncthreads();
+        before = lanes_sum<L>(before);
+        kept |= static_cast<uint64_t>(before < p.top_groups) << g;
     }
+    __builtin_amdgcn_wave_barrier();
+    return kept;
+}
+
+// L lanes per token, N experts in a lane, S chosen experts in a lane.
+template <int T, int L, int N, int S>
+__global__ __launch_bounds__(kBlock) void route_kernel(const char* __restrict__ logits, const float* __restrict__ bias,
+                                                       int32_t* __restrict__ ids, float* __restrict__ weights,
+                                                       int64_t tokens, Choice p) {
+    constexpr int kTokens = kBlock / L;
+    __shared__ double of_group[kTokens][kMostGroups];  // only of groups that do not lie in whole lanes
+    const int lane = threadIdx.x % L, e0 = lane * N, size = p.experts / p.groups;
+    const bool grouped = p.groups > 1, scored = bias || (grouped && p.top2);
+    // lanes of a group, where its experts are those of 2^n lanes
+    const int wide = size % N == 0 ? size / N : 0;
+    const bool whole = grouped && wide >= 1 && wide <= L && (wide & (wide - 1)) == 0;
+    float b[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) b[i] = bias && e0 + i < p.experts ? bias[e0 + i] : 0.0f;
+
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens; t0 < tokens; t0 += static_cast<int64_t>(gridDim.x) * kTokens) {
+        const int64_t mine = t0 + threadIdx.x / L, t = mine < tokens ? mine : tokens - 1;
+        const char* row = logits + t * p.experts * Elem<T>::kBytes;
+        float l[N], m = -kInf;
+        load_logits<T, N>(row, e0, p.experts, l);
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            bad |= l[i] != l[i] || (!p.sigmoid && l[i] == kInf);
+            m = fmaxf(m, l[i]);
+        }
+        bad = lanes_any<L>(bad);
+        float sum = 0.0f;
+        if (!p.sigmoid) {
+            m = lanes_max<L>(m);
+            if (scored || !p.renormalise) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) sum += expf(l[i] - m);
+                sum = lanes_sum<L>(sum);
+            }
+        }
+
+        int id[S];
+        // The choice by float32 values; returns whether some were too near to tell.
+        auto choose = [&]() {
+            auto score = [&](float v) { return p.sigmoid ? sigmoid32(v) : expf(v - m) / sum; };
+            const double off = scored ? 2.0 * score_error(p.sigmoid, sum) : 0.0;
+            bool near = false;
+            // a >= c; each of `times` scores off, and their sums with the bias rounded
+            auto tell = [&](double a, double c, double times) { near |= a - c <= times * off + fabs(a) * 0x1p-22; };
+            auto group_value = [&](double first, double second) -> double {
+                if (!p.top2 || second == -kInf) return p.top2 ? second : value_of(first);
+                if (bias) return value_of(first) + value_of(second);
+                return static_cast<double>(score(static_cast<float>(value_of(first)))) +
+                       score(static_cast<float>(value_of(second)));
+            };
+            double key[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                key[i] = key_of(bias && l[i] > -kInf ? score(l[i]) + b[i] : l[i], e0 + i);
+            if (grouped && !whole) {
+                double* value = of_group[threadIdx.x / L];
+                for (int g = 0; g < p.groups; ++g) {
+                    double first = -kInf, second = -kInf;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const double v = e0 + i >= g * size && e0 + i < (g + 1) * size ? key[i] : -kInf;
+                        second = larger(second, smaller(first, v));
+                        first = larger(first, v);
+                    }
+#pragma unroll
+                    for (int x = 1; x < L; x *= 2) {
+                        const double a = __shfl_xor(first, x, 64), c = __shfl_xor(second, x, 64);
+                        second = larger(smaller(first, a), larger(second, c));
+                        first = larger(first, a);
+                    }
+                    const double v = group_value(first, second);
+                    if (lane == 0) value[g] = v;
+                }
+                const uint64_t kept = best_groups<L>(value, p, lane, [&](double v, double w) {
+                    if (scored) tell(larger(v, w), smaller(v, w), 2.0);
+                });
+                near = lanes_any<L>(near);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (!(kept >> ((e0 + i) / size & 63) & 1)) key[i] = -kInf;
+            }
+            sort_keys<N>(key);
+            if (whole) {
+                double first = key[0], second = N > 1 ? key[N > 1 ? 1 : 0] : -kInf;
+                for (int x = 1; x < wide; x *= 2) {
+                    const double a = __shfl_xor(first, x, 64), c = __shfl_xor(second, x, 64);
+                    second = larger(smaller(first, a), larger(second, c));
+                    first = larger(first, a);
+                }
+                const double v = group_value(first, second);
+                const int group = lane / wide;
+                int before = 0;
+                for (int g = 0; g < p.groups; ++g) {
+                    const double w = __shfl(v, g * wide, L);
+                    before += w > v || (w == v && g < group);
+                    if (scored && g != group && group < p.groups) tell(larger(v, w), smaller(v, w), 2.0);
+                }
+                near = lanes_any<L>(near);
+                if (before >= p.top_groups || group >= p.groups)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) key[i] = -kInf;
+            }
+            double last = 0x1p1020;
+            const int rounds = p.top_k + (bias ? 1 : 0);  // with a bias also the best that is left
+            for (int r = 0; r < rounds; ++r) {
+                const double best = over_lanes<L>(key[0], [](double a, double c) { return larger(a, c); });
+                if (bias) tell(last, best, 1.0);
+                last = best;
+                const bool pop = key[0] == best;
+#pragma unroll
+                for (int i = 0; i + 1 < N; ++i) key[i] = pop ? key[i + 1] : key[i];
+                key[N - 1] = pop ? static_cast<double>(-kInf) : key[N - 1];
+                const int e = expert_of(best);
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    if (r < p.top_k && r == lane + s * L) id[s] = e;
+            }
+            return near;
+        };
+        // The choice by float64 values.
+        auto choose64 = [&]() {
+            double all = 0.0, v[N];
+            if (!p.sigmoid) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) all += exp(static_cast<double>(l[i]) - m);
+                all = lanes_sum<L>(all);
+            }
+            auto score = [&](double x) { return p.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / all; };
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const double c = bias ? score(l[i]) + static_cast<double>(b[i]) : l[i];
+                v[i] = l[i] > -kInf && c > -kInf ? c : -kInf;  // not where either is NaN
+            }
+            if (grouped) {
+                double* value = of_group[threadIdx.x / L];
+                for (int g = 0; g < p.groups; ++g) {
+                    double first = -kInf, second = -kInf;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const double x = e0 + i >= g * size && e0 + i < (g + 1) * size ? v[i] : -kInf;
+                        second = larger(second, smaller(first, x));
+                        first = larger(first, x);
+                    }
+#pragma unroll
+                    for (int x = 1; x < L; x *= 2) {
+                        const double a = __shfl_xor(first, x, 64), c = __shfl_xor(second, x, 64);
+                        second = larger(smaller(first, a), larger(second, c));
+                        first = larger(first, a);
+                    }
+                    double of = first;
+                    if (p.top2) of = second == -kInf ? second : (bias ? first + second : score(first) + score(second));
+                    if (lane == 0) value[g] = of;
+                }
+                const uint64_t kept = best_groups<L>(value, p, lane, [](double, double) {});
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (!(kept >> ((e0 + i) / size & 63) & 1)) v[i] = -kInf;
+            }
+            struct Best {
+                double value;
+                int expert;
+            };
+            for (int r = 0; r < p.top_k; ++r) {
+                Best best = {-kInf, kMostExperts};
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (v[i] > best.value) best = Best{v[i], e0 + i};
+#pragma unroll
+                for (int x = 1; x < L; x *= 2) {
+                    const Best o = {__shfl_xor(best.value, x, 64), __shfl_xor(best.expert, x, 64)};
+                    if (o.value > best.value || (o.value == best.value && o.expert < best.expert)) best = o;
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (best.expert == e0 + i) v[i] = -kInf;
+                const int e = best.value > -kInf ? best.expert : -1;
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    if (r == lane + s * L) id[s] = e;
+            }
+        };
+#pragma unroll
+        for (int s = 0; s < S; ++s) id[s] = -1;
+        // float32 values tell nearly all tokens; a wavefront with one that they cannot is done again
+        if (__any(choose())) choose64();
+
+        float w[S], lw[S], most = -kInf, all = 0.0f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            lw[s] = id[s] >= 0 ? load_logit<T>(row, id[s]) : -kInf;
+            most = fmaxf(most, lw[s]);
+        }
+        most = lanes_max<L>(most);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            if (!p.renormalise)
+                w[s] = p.sigmoid ? sigmoid32(lw[s]) : expf(lw[s] - m) / sum;
+            else if (!p.sigmoid)
+                w[s] = expf(lw[s] - most);
+            else  // sigmoid(l) over e^min(most, 0), which does not underflow
+                w[s] = expf(fminf(lw[s], 0.0f) - fminf(most, 0.0f)) / (1.0f + expf(-fabsf(lw[s])));
+            if (id[s] < 0) w[s] = 0.0f;
+            all += w[s];
+        }
+        if (p.renormalise) all = lanes_sum<L>(all);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int j = lane + s * L;
+            if (p.renormalise && id[s] >= 0) w[s] /= all;
+            if (j < p.top_k && mine < tokens) {
+                ids[t * p.top_k + j] = id[s];
+                weights[t * p.top_k + j] = bad ? __builtin_nanf("") : w[s] * p.scale;
+            }
+        }
+    }
+}
+
+// L lanes per token, N experts and S slots in a lane.
+template <int T, int L, int N, int S>
+__global__ __launch_bounds__(kBlock) void route_grad_kernel(const float* __restrict__ grad_weights,
+                                                            const char* __restrict__ logits,
+                                                            const int32_t* __restrict__ ids,
+                                                            char* __restrict__ grad_logits, int64_t tokens, Choice p) {
+    constexpr int kTokens = kBlock / L;
+    struct Slot {
+        int id;
+        float d;
+    };
+    __shared__ Slot slots[kTokens][S * L];
+    const int lane = threadIdx.x % L, e0 = lane * N;
+    Slot* mine_slots = slots[threadIdx.x / L];
+    const bool dense = !p.sigmoid && !p.renormalise;
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens; t0 < tokens; t0 += static_cast<int64_t>(gridDim.x) * kTokens) {
+        const int64_t mine = t0 + threadIdx.x / L, t = mine < tokens ? mine : tokens - 1;
+        const char* row = logits + t * p.experts * Elem<T>::kBytes;
+        float l[N], m = -kInf, sum = 0.0f;
+        if (dense) {
+            load_logits<T, N>(row, e0, p.experts, l);
+#pragma unroll
+            for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
+            m = lanes_max<L>(m);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                l[i] = m > -kInf ? expf(l[i] - m) : 0.0f;
+                sum += l[i];
+            }
+            sum = lanes_sum<L>(sum);
+#pragma unroll
+            for (int i = 0; i < N; ++i) l[i] = m > -kInf ? l[i] / sum : 0.0f;
+        }
+        int id[S];
+        float u[S], lw[S], v[S], most = -kInf;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int j = lane + s * L;
+            id[s] = j < p.top_k ? ids[t * p.top_k + j] : -1;
+            if (id[s] < 0 || id[s] >= p.experts) id[s] = -1;
+            u[s] = id[s] >= 0 ? grad_weights[t * p.top_k + j] * p.scale : 0.0f;
+            lw[s] = id[s] >= 0 ? load_logit<T>(row, id[s]) : -kInf;
+            most = fmaxf(most, lw[s]);
+        }
+        float dot = 0.0f, all = 0.0f;
+        if (p.renormalise) {
+            most = lanes_max<L>(most);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                v[s] = 0.0f;
+                if (id[s] >= 0 && !(most == -kInf))
+                    v[s] = p.sigmoid ? expf(fminf(lw[s], 0.0f) - fminf(most, 0.0f)) / (1.0f + expf(-fabsf(lw[s])))
+                                     : expf(lw[s] - most);
+                all += v[s];
+            }
+            all = lanes_sum<L>(all);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                v[s] = all == 0.0f ? 0.0f : v[s] / all;
+                dot += u[s] * v[s];
+            }
+            dot = lanes_sum<L>(dot);
+        } else if (!p.sigmoid) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) dot += id[s] >= 0 && m > -kInf ? u[s] * (expf(lw[s] - m) / sum) : 0.0f;
+            dot = lanes_sum<L>(dot);
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            float d = u[s];
+            if (p.renormalise) d = v[s] * (u[s] - dot);
+            if (p.sigmoid) d *= p.renormalise ? sigmoid32(-lw[s]) : sigmoid32(lw[s]) * sigmoid32(-lw[s]);
+            mine_slots[lane + s * L] = Slot{id[s], id[s] >= 0 ? d : 0.0f};
+        }
+        __threadfence_block();
+        __builtin_amdgcn_wave_barrier();
+        float g[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[i] = 0.0f;
+        for (int j = 0; j < p.top_k; ++j) {
+            const Slot s = mine_slots[j];
+#pragma unroll
+            for (int i = 0; i < N; ++i) g[i] += s.id == e0 + i ? s.d : 0.0f;
+        }
+        __builtin_amdgcn_wave_barrier();
+        if (dense)
+#pragma unroll
+            for (int i = 0; i < N; ++i) g[i] = l[i] * (g[i] - dot);
+        if (mine >= tokens) continue;
+        char* to = grad_logits + t * p.experts * Elem<T>::kBytes;
+        constexpr int V = N < 4 ? N : 4;
+#pragma unroll
+        for (int i = 0; i < N; i += V) {
+            if (V == 4 && e0 + i + 4 <= p.experts) {
+                if constexpr (T == MOE_EPI_F32) {
+                    typedef u32x4 loose __attribute__((aligned(4)));
+                    u32x4 w;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) w[j] = __float_as_uint(g[i + j]);
+                    *reinterpret_cast<loose*>(to + 4 * (e0 + i)) = w;
+                } else {
+                    typedef u32x2 loose __attribute__((aligned(2)));
+                    const float f[8] = {g[i], g[i + 1 < N ? i + 1 : i], g[i + 2 < N ? i + 2 : i],
+                                        g[i + 3 < N ? i + 3 : i], 0, 0, 0, 0};
+                    const u32x4 w = Elem<T>::pack(f);
+                    *reinterpret_cast<loose*>(to + 2 * (e0 + i)) = u32x2{w[0], w[1]};
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (e0 + i + j < p.experts) Elem<T>::store1(to, e0 + i + j, g[i + j]);
+            }
+        }
+    }
+}
+
+// f(lanes of a token, experts of a lane, chosen of a lane)
+template <class F>
+void by_size(int experts, int top_k, F f) {
+    auto go = [&](auto l, auto n) {
+        constexpr int L = decltype(l)::value;
+        if (top_k <= L) return f(l, n, std::integral_constant<int, 1>());
+        f(l, n, std::integral_constant<int, kMostChosen / L>());
+    };
+    const std::integral_constant<int, 16> l16, n16;
+    if (experts <= 16) return go(l16, std::integral_constant<int, 1>());
+    if (experts <= 32) return go(l16, std::integral_constant<int, 2>());
+    if (experts <= 64) return go(l16, std::integral_constant<int, 4>());
+    if (experts <= 128) return go(l16, std::integral_constant<int, 8>());
+    if (experts <= 256) return go(l16, n16);
+    if (experts <= 512) return go(std::integral_constant<int, 32>(), n16);
+    f(std::integral_constant<int, 64>(), n16, std::integral_constant<int, 1>());
+}
+
+template <class F>
+void by_type(int dtype, F f) {
+    if (dtype == MOE_EPI_BF16) return f(std::integral_constant<int, MOE_EPI_BF16>());
+    if (dtype == MOE_EPI_F16) return f(std::integral_constant<int, MOE_EPI_F16>());
+    f(std::integral_constant<int, MOE_EPI_F32>());
 }
 
 bool sizes_ok(int64_t tokens, int64_t experts, int64_t top_k) {
@@ -205,13 +582,14 @@ extern "C" int moe_route_fwd(const void* logits, int dtype, const float* bias, i
                       static_cast<int>(top_groups), score == MOE_EPI_SIGMOID, group_score == MOE_EPI_GROUP_TOP2,
                       renormalise != 0, scale};
     (void)hipGetLastError();
-    const dim3 grid(grid_for_rows(tokens, 1)), block(64);
-    const hipStream_t st = as_stream(stream);
-    switch (dtype) {
-        case MOE_EPI_BF16: hipLaunchKernelGGL((route_kernel<MOE_EPI_BF16>), grid, block, 0, st, logits, bias, ids, weights, tokens, p); break;
-        case MOE_EPI_F16: hipLaunchKernelGGL((route_kernel<MOE_EPI_F16>), grid, block, 0, st, logits, bias, ids, weights, tokens, p); break;
-        default: hipLaunchKernelGGL((route_kernel<MOE_EPI_F32>), grid, block, 0, st, logits, bias, ids, weights, tokens, p); break;
-    }
+    by_type(dtype, [&](auto t) {
+        by_size(p.experts, p.top_k, [&](auto l, auto n, auto k) {
+            constexpr int L = decltype(l)::value;
+            hipLaunchKernelGGL((route_kernel<decltype(t)::value, L, decltype(n)::value, decltype(k)::value>),
+                               dim3(grid_for_rows(tokens, kBlock / L)), dim3(kBlock), 0, as_stream(stream),
+                               static_cast<const char*>(logits), bias, ids, weights, tokens, p);
+        });
+    });
     return launch_status();
 }
 
@@ -233,12 +611,13 @@ extern "C" int moe_route_bwd(const float* grad_weights, const void* logits, int 
     const Choice p = {static_cast<int>(experts), static_cast<int>(top_k), 1, 1, score == MOE_EPI_SIGMOID, false,
                       renormalise != 0, scale};
     (void)hipGetLastError();
-    const dim3 grid(grid_for_rows(tokens, 1)), block(64);
-    const hipStream_t st = as_stream(stream);
-    switch (dtype) {
-        case MOE_EPI_BF16: hipLaunchKernelGGL((route_grad_kernel<MOE_EPI_BF16>), grid, block, 0, st, grad_weights, logits, ids, grad_logits, tokens, p); break;
-        case MOE_EPI_F16: hipLaunchKernelGGL((route_grad_kernel<MOE_EPI_F16>), grid, block, 0, st, grad_weights, logits, ids, grad_logits, tokens, p); break;
-        default: hipLaunchKernelGGL((route_grad_kernel<MOE_EPI_F32>), grid, block, 0, st, grad_weights, logits, ids, grad_logits, tokens, p); break;
-    }
+    by_type(dtype, [&](auto t) {
+        by_size(p.experts, p.top_k, [&](auto l, auto n, auto k) {
+            constexpr int L = decltype(l)::value;
+            hipLaunchKernelGGL((route_grad_kernel<decltype(t)::value, L, decltype(n)::value, decltype(k)::value>),
+                               dim3(grid_for_rows(tokens, kBlock / L)), dim3(kBlock), 0, as_stream(stream), grad_weights,
+                               static_cast<const char*>(logits), ids, static_cast<char*>(grad_logits), tokens, p);
+        });
+    });
     return launch_status();
 }

@@ -8,6 +8,7 @@ namespace moe_epi {
 namespace {
 
 constexpr int kBlock = 256;
+constexpr int64_t kMostTokens = 1 << 20;  // of a launch
 constexpr int kMostExperts = 1024, kMostGroups = 64, kMostChosen = 64;
 constexpr float kInf = __builtin_inff();
 
@@ -21,7 +22,8 @@ struct Choice {
 
 // The lane's partner in step `kXor` (1, 2, 4, 8, 16, 32) of an exchange that
 // leaves every lane of an aligned group of 2 kXor with the group's result: the
-// steps up to 8 mirror quads, halves and rows of 16 lanes, without LDS.
+// steps up to 8 mirror quads, halves and rows of 16 lanes, the others swap rows
+// and halves of the wavefront; none goes through LDS.
 template <int kXor>
 __device__ __forceinline__ int partner(int v) {
     if constexpr (kXor == 1)
@@ -32,8 +34,12 @@ __device__ __forceinline__ int partner(int v) {
         return __builtin_amdgcn_mov_dpp(v, 0x141, 0xF, 0xF, true);
     else if constexpr (kXor == 8)
         return __builtin_amdgcn_mov_dpp(v, 0x140, 0xF, 0xF, true);
-    else
-        return __shfl_xor(v, kXor, 64);
+    else {
+        // the rows (halves) of the pair: their own in one of the two, the partner's in the other
+        const auto r = kXor == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                                  : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return (threadIdx.x & kXor) != 0 ? r[0] : r[1];
+    }
 }
 template <int kXor>
 __device__ __forceinline__ float partner(float v) {
@@ -120,17 +126,71 @@ __device__ __forceinline__ void sort_keys(double (&key)[N]) {
                     }
 }
 
+// A sequence that rises and falls, descending.
+template <int N, int M>
+__device__ __forceinline__ void settle(double (&key)[M]) {
+#pragma unroll
+    for (int d = N / 2; d >= 1; d /= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (!(i & d)) {
+                const double a = key[i], b = key[i + d];
+                key[i] = larger(a, b);
+                key[i + d] = smaller(a, b);
+            }
+}
+// The K largest of two descending lists of K, in `a`; `left` grows to the largest that is left out.
+template <int K>
+__device__ __forceinline__ void join(double (&a)[K], const double (&b)[K], double& left) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        left = larger(left, smaller(a[i], b[K - 1 - i]));
+        a[i] = larger(a[i], b[K - 1 - i]);
+    }
+    settle<K>(a);
+}
+// The K largest keys of L lanes that have n each, descending, in every lane.
+template <int L, int K, int n, int kXor = 1>
+__device__ __forceinline__ void join_lanes(double (&key)[K], double& left) {
+    if constexpr (kXor < L) {
+        if constexpr (2 * n <= K) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) key[2 * n - 1 - i] = partner<kXor>(key[i]);
+            settle<2 * n>(key);
+            join_lanes<L, K, 2 * n, 2 * kXor>(key, left);
+        } else {
+            double other[K];
+#pragma unroll
+            for (int i = 0; i < K; ++i) other[i] = partner<kXor>(key[i]);
+            join<K>(key, other, left);
+            left = larger(left, partner<kXor>(left));
+            join_lanes<L, K, n, 2 * kXor>(key, left);
+        }
+    }
+}
+
 // ---- scores ----------------------------------------------------------------------------
 
 __device__ __forceinline__ float sigmoid32(float l) {
     const float e = expf(-fabsf(l));
     return (l >= 0.0f ? 1.0f : e) / (1.0f + e);
 }
-// What a float32 score may be off. A sigmoid: four roundings of at most 1. A
-// softmax: 2^-24 of itself for |l - m| (m - l is at most log(experts) on average
-// over the scores, which the sum is off by, and at most 0.37 of the largest
-// score for the score itself) and for each of up to 22 additions, the quotient
-// and the exponentials: below 2^-18 of the largest score, 1 / sum.
+// As sigmoid32 with the hardware's exponential and reciprocal, for the choice.
+__device__ __forceinline__ float rough_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+__device__ __forceinline__ float rough_sigmoid(float l) {
+    const float e = rough_exp(-fabsf(l));
+    return (l >= 0.0f ? 1.0f : e) * __builtin_amdgcn_rcpf(1.0f + e);
+}
+// sigmoid(l) over e^min(most, 0), which does not underflow for the largest of some logits.
+__device__ __forceinline__ float over_most(float l, float most) {
+    return expf(fminf(l, 0.0f) - fminf(most, 0.0f)) / (1.0f + expf(-fabsf(l)));
+}
+// What a float32 score may be off. Steps of 2^-24: a sigmoid
+// 0.4 for the exponential's argument (x e^-x), 2 each for the exponential and the
+// reciprocal, and 2 roundings, below 2^-21; a softmax |l - m| of itself (m - l is
+// at most log(experts) on average over the scores, which the sum is off by, and
+// at most 0.4 of the largest score for the score itself), up to 22 additions and
+// 8 for exponentials and quotient: below 2^-18 of the largest score, 1 / sum.
 __device__ __forceinline__ double score_error(bool sigmoid, float sum) {
     return sigmoid ? 0x1p-21 : 0x1p-18 / static_cast<double>(sum);
 }
@@ -166,136 +226,326 @@ __device__ __forceinline__ void load_logits(const char* row, int e0, int experts
     }
 }
 
-// The groups (a bit each) that fewer than top_groups others come before. look(v, w): at each pair of their values.
-template <int L, class F>
-__device__ __forceinline__ uint64_t best_groups(const double* value, const Choice& p, int lane, F look) {
+// The groups (a bit each) that fewer than top_groups others come before.
+template <int L>
+__device__ __forceinline__ uint64_t best_groups(const double* value, const Choice& p, int lane) {
     __threadfence_block();
     __builtin_amdgcn_wave_barrier();
     uint64_t kept = 0;
-    for (int g = 0; g < p.groups; ++g) {
-        const double v = value[g];
-        int before = 0;
-        for (int o = lane; o < p.groups; o += L) {
+#pragma unroll 1
+    for (int g0 = 0; g0 < p.groups; g0 += L) {
+        const int g = g0 + lane;
+        const double v = g < p.groups ? value[g] : -kInf;
+        int before = g < p.groups ? 0 : kMostGroups;
+
+#pragma unroll 1
+        for (int o = 0; o < p.groups; ++o) {
             const double w = value[o];
             before += w > v || (w == v && o < g);
-            if (o != g) look(v, w);
         }
-        before = lanes_sum<L>(before);
-        kept |= static_cast<uint64_t>(before < p.top_groups) << g;
+        const uint64_t best = __ballot(before < p.top_groups);
+        if constexpr (L == 64)
+            kept |= best;
+        else
+            kept |= (best >> (threadIdx.x & 63 & ~(L - 1)) & ((1ull << L) - 1)) << g0;
     }
     __builtin_amdgcn_wave_barrier();
     return kept;
 }
 
-// L lanes per token, N experts in a lane, S chosen experts in a lane.
-template <int T, int L, int N, int S>
+// e^x to an ulp or so: x = n ln 2 + r, the Taylor series to r^13 (|r| <= 0.35: what is left out is 2^-57), times
+// 2^n. The coefficients are read in a loop: as constants they would be kept in registers from every token.
+__device__ const double kOverFactorial[14] = {1.0 / 6227020800.0, 1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0,
+                                              1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0, 1.0 / 120.0,
+                                              1.0 / 24.0, 1.0 / 6.0, 0.5, 1.0, 1.0};
+__device__ __forceinline__ double exp64(double x) {
+    x = fmin(fmax(x, -800.0), 800.0);  // 0 and infinity from there on
+    const double n = rint(x * 0x1.71547652b82fep+0);
+    double r = fma(-n, 0x1.62e42fefa39efp-1, x);
+    r = fma(-n, 0x1.abc9e3b39803fp-56, r);
+    double sum = kOverFactorial[0];
+#pragma unroll 1
+    for (int i = 1; i < 14; ++i) sum = fma(sum, r, kOverFactorial[i]);
+    return ldexp(sum, static_cast<int>(n));
+}
+
+// Token t by float64 values, by the whole wavefront, an expert that is chosen in each lane. Few tokens come here, so
+// its code is kept short: what is not in the instruction cache takes longer to read than to run.
+template <int T>
+__device__ __forceinline__ void route64(const char* logits, const float* bias, int32_t* ids, float* weights, int64_t t,
+                                        const Choice& p, double* value, double* of_group) {
+    const int lane = threadIdx.x & 63, size = p.experts / p.groups;
+    const char* row = logits + t * p.experts * Elem<T>::kBytes;
+    float m = -kInf;
+    double all = 0.0;
+    bool bad = false;
+#pragma unroll 1
+    for (int e = lane; e < p.experts; e += 64) {
+        const float l = load_logit<T>(row, e);
+        bad |= l != l || (!p.sigmoid && l == kInf);
+        m = fmaxf(m, l);
+    }
+    bad = lanes_any<64>(bad);
+    if (!p.sigmoid) {
+        m = lanes_max<64>(m);
+#pragma unroll 1
+        for (int e = lane; e < p.experts; e += 64) all += exp64(static_cast<double>(load_logit<T>(row, e)) - m);
+        all = lanes_sum<64>(all);
+    }
+    // an expert's value, its score where groups count sums of those and there is no bias
+    const bool sums = p.top2 && p.groups > 1;
+    auto fill = [&](bool by_score) {
+#pragma unroll 1
+        for (int e = lane; e < p.experts; e += 64) {
+            const float l = load_logit<T>(row, e);
+            double v = l;
+            if (by_score) v = p.sigmoid ? 1.0 / (1.0 + exp64(-v)) : exp64(v - m) / all;
+            if (bias) v += static_cast<double>(bias[e]);
+            value[e] = l > -kInf && v > -kInf ? v : -kInf;  // not where either is NaN
+        }
+        __threadfence_block();
+        __builtin_amdgcn_wave_barrier();
+    };
+    fill(bias || sums);
+    uint64_t kept = ~0ull;
+    if (p.groups > 1) {
+        if (lane < p.groups) {
+            double first = -kInf, second = -kInf;
+
+#pragma unroll 1
+            for (int i = 0; i < size; ++i) {
+                const double v = value[lane * size + i];
+                second = larger(second, smaller(first, v));
+                first = larger(first, v);
+            }
+            of_group[lane] = sums ? first + second : first;
+        }
+        kept = best_groups<64>(of_group, p, lane);
+        if (sums && !bias) {
+#pragma unroll 1
+            for (int e = lane; e < p.experts; e += 64) value[e] = value[e] > -kInf ? load_logit<T>(row, e) : -kInf;
+            __threadfence_block();
+            __builtin_amdgcn_wave_barrier();
+        }
+    }
+    // a lane holds experts in a row, so that of equal ones the lowest lane has the lowest
+    const int n = (p.experts + 63) / 64;
+    int id = -1;
+#pragma unroll 1
+    for (int r = 0; r < p.top_k; ++r) {
+        double best = -kInf;
+        int expert = -1;
+
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            const int e = lane * n + i;
+            const double v = e < p.experts && (kept >> (e / size & 63) & 1) ? value[e] : -kInf;
+            if (v > best) {
+                best = v;
+                expert = e;
+            }
+        }
+        const double most = over_lanes<64>(best, [](double a, double c) { return larger(a, c); });
+        const int at = __builtin_ctzll(__ballot(best == most));  // -inf: the first lane, which has no expert then
+        const int e = __shfl(expert, at, 64);
+        if (lane == r) id = e;
+        if (lane == at && expert >= 0) value[expert] = -kInf;
+        __threadfence_block();
+        __builtin_amdgcn_wave_barrier();
+    }
+    const float l = id >= 0 ? load_logit<T>(row, id) : -kInf, most = lanes_max<64>(l);
+    float w;
+    if (!p.renormalise)
+        w = p.sigmoid ? sigmoid32(l) : expf(l - m) / static_cast<float>(all);
+    else if (!p.sigmoid)
+        w = expf(l - most);
+    else
+        w = over_most(l, most);
+    if (id < 0) w = 0.0f;
+    if (p.renormalise) {
+        const float sum = lanes_sum<64>(w);
+        if (id >= 0) w /= sum;
+    }
+    if (lane < p.top_k) {
+        ids[t * p.top_k + lane] = id;
+        weights[t * p.top_k + lane] = bad ? __builtin_nanf("") : w * p.scale;
+    }
+}
+
+// L lanes per token, N experts in a lane, S chosen experts in a lane. K: the
+// lanes' lists are joined, of which the K >= top_k largest are kept; 0: one
+// expert at a time. kScored: the order is that of scores, with a bias or as sums
+// of two for a group's value, and not that of the logits.
+template <int T, int L, int N, int S, int K, bool kScored>
 __global__ __launch_bounds__(kBlock) void route_kernel(const char* __restrict__ logits, const float* __restrict__ bias,
                                                        int32_t* __restrict__ ids, float* __restrict__ weights,
                                                        int64_t tokens, Choice p) {
     constexpr int kTokens = kBlock / L;
     __shared__ double of_group[kTokens][kMostGroups];  // only of groups that do not lie in whole lanes
+    __shared__ double value64[kScored ? kBlock / 64 : 1][kScored ? (L * N < 64 ? 64 : L * N) : 1];
+    __shared__ double group64[kScored ? kBlock / 64 : 1][kScored ? kMostGroups : 1];
     const int lane = threadIdx.x % L, e0 = lane * N, size = p.experts / p.groups;
-    const bool grouped = p.groups > 1, scored = bias || (grouped && p.top2);
+    const bool grouped = p.groups > 1, biased = kScored && bias;
     // lanes of a group, where its experts are those of 2^n lanes
     const int wide = size % N == 0 ? size / N : 0;
     const bool whole = grouped && wide >= 1 && wide <= L && (wide & (wide - 1)) == 0;
-    float b[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) b[i] = bias && e0 + i < p.experts ? bias[e0 + i] : 0.0f;
 
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens; t0 < tokens; t0 += static_cast<int64_t>(gridDim.x) * kTokens) {
-        const int64_t mine = t0 + threadIdx.x / L, t = mine < tokens ? mine : tokens - 1;
-        const char* row = logits + t * p.experts * Elem<T>::kBytes;
-        float l[N], m = -kInf;
-        load_logits<T, N>(row, e0, p.experts, l);
-        bool bad = false;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
+    const int64_t mine = t0 + threadIdx.x / L, t = mine < tokens ? mine : tokens - 1;
+    const char* row = logits + t * p.experts * Elem<T>::kBytes;
+    float l[N], b[N], m = -kInf;
+    load_logits<T, N>(row, e0, p.experts, l);
+    if (biased) load_logits<MOE_EPI_F32, N>(reinterpret_cast<const char*>(bias), e0, p.experts, b);
+    bool bad = false;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            bad |= l[i] != l[i] || (!p.sigmoid && l[i] == kInf);
-            m = fmaxf(m, l[i]);
+    for (int i = 0; i < N; ++i) {
+        bad |= l[i] != l[i] || (!p.sigmoid && l[i] == kInf);
+        m = fmaxf(m, l[i]);
+    }
+    bad = lanes_any<L>(bad);
+    float sum = 0.0f;
+    if (!p.sigmoid) {
+        m = lanes_max<L>(m);
+        if (kScored || !p.renormalise) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) sum += expf(l[i] - m);
+            sum = lanes_sum<L>(sum);
         }
-        bad = lanes_any<L>(bad);
-        float sum = 0.0f;
-        if (!p.sigmoid) {
-            m = lanes_max<L>(m);
-            if (scored || !p.renormalise) {
+    }
+
+    int id[S];
+    // The choice by float32 values; returns whether some were too near to tell.
+    auto choose = [&]() {
+        const float over = p.sigmoid ? 0.0f : 1.0f / sum;
+        auto score = [&](float v) { return p.sigmoid ? rough_sigmoid(v) : rough_exp(v - m) * over; };
+        const double off = kScored ? 2.0 * score_error(p.sigmoid, sum) : 0.0;
+        bool near = false;
+        // a >= c; each of `times` scores off, and their sums with the bias rounded
+        auto tell = [&](double a, double c, double times) { near |= a - c <= times * off + fabs(a) * 0x1p-22; };
+        auto group_value = [&](double first, double second) -> double {
+            if (!kScored || !p.top2 || second == -kInf) return kScored && p.top2 ? second : value_of(first);
+            if (biased) return value_of(first) + value_of(second);
+            return static_cast<double>(score(static_cast<float>(value_of(first)))) +
+                   score(static_cast<float>(value_of(second)));
+        };
+        float c[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) sum += expf(l[i] - m);
-                sum = lanes_sum<L>(sum);
+        for (int i = 0; i < N; ++i) c[i] = l[i];
+        if (biased) {
+            if (p.sigmoid) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) c[i] = l[i] > -kInf ? rough_sigmoid(l[i]) + b[i] : -kInf;
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) c[i] = l[i] > -kInf ? rough_exp(l[i] - m) * over + b[i] : -kInf;
             }
         }
-
-        int id[S];
-        // The choice by float32 values; returns whether some were too near to tell.
-        auto choose = [&]() {
-            auto score = [&](float v) { return p.sigmoid ? sigmoid32(v) : expf(v - m) / sum; };
-            const double off = scored ? 2.0 * score_error(p.sigmoid, sum) : 0.0;
-            bool near = false;
-            // a >= c; each of `times` scores off, and their sums with the bias rounded
-            auto tell = [&](double a, double c, double times) { near |= a - c <= times * off + fabs(a) * 0x1p-22; };
-            auto group_value = [&](double first, double second) -> double {
-                if (!p.top2 || second == -kInf) return p.top2 ? second : value_of(first);
-                if (bias) return value_of(first) + value_of(second);
-                return static_cast<double>(score(static_cast<float>(value_of(first)))) +
-                       score(static_cast<float>(value_of(second)));
-            };
-            double key[N];
+        double key[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                key[i] = key_of(bias && l[i] > -kInf ? score(l[i]) + b[i] : l[i], e0 + i);
-            if (grouped && !whole) {
-                double* value = of_group[threadIdx.x / L];
-                for (int g = 0; g < p.groups; ++g) {
-                    double first = -kInf, second = -kInf;
+        for (int i = 0; i < N; ++i) key[i] = key_of(c[i], e0 + i);
+        if (grouped && !whole) {
+            double* value = of_group[threadIdx.x / L];
+            for (int g = 0; g < p.groups; ++g) {
+                double first = -kInf, second = -kInf;
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const double v = e0 + i >= g * size && e0 + i < (g + 1) * size ? key[i] : -kInf;
-                        second = larger(second, smaller(first, v));
-                        first = larger(first, v);
-                    }
-#pragma unroll
-                    for (int x = 1; x < L; x *= 2) {
-                        const double a = __shfl_xor(first, x, 64), c = __shfl_xor(second, x, 64);
-                        second = larger(smaller(first, a), larger(second, c));
-                        first = larger(first, a);
-                    }
-                    const double v = group_value(first, second);
-                    if (lane == 0) value[g] = v;
+                for (int i = 0; i < N; ++i) {
+                    const double v = e0 + i >= g * size && e0 + i < (g + 1) * size ? key[i] : -kInf;
+                    second = larger(second, smaller(first, v));
+                    first = larger(first, v);
                 }
-                const uint64_t kept = best_groups<L>(value, p, lane, [&](double v, double w) {
-                    if (scored) tell(larger(v, w), smaller(v, w), 2.0);
-                });
-                near = lanes_any<L>(near);
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (!(kept >> ((e0 + i) / size & 63) & 1)) key[i] = -kInf;
-            }
-            sort_keys<N>(key);
-            if (whole) {
-                double first = key[0], second = N > 1 ? key[N > 1 ? 1 : 0] : -kInf;
-                for (int x = 1; x < wide; x *= 2) {
+                for (int x = 1; x < L; x *= 2) {
                     const double a = __shfl_xor(first, x, 64), c = __shfl_xor(second, x, 64);
                     second = larger(smaller(first, a), larger(second, c));
                     first = larger(first, a);
                 }
                 const double v = group_value(first, second);
-                const int group = lane / wide;
-                int before = 0;
-                for (int g = 0; g < p.groups; ++g) {
-                    const double w = __shfl(v, g * wide, L);
-                    before += w > v || (w == v && g < group);
-                    if (scored && g != group && group < p.groups) tell(larger(v, w), smaller(v, w), 2.0);
-                }
-                near = lanes_any<L>(near);
-                if (before >= p.top_groups || group >= p.groups)
-#pragma unroll
-                    for (int i = 0; i < N; ++i) key[i] = -kInf;
+                if (lane == 0) value[g] = v;
             }
+            const uint64_t kept = best_groups<L>(value, p, lane);
+            if (kScored) {
+                double in = kInf, out = -kInf;  // the least of the groups that stay, the largest of the others
+                for (int g = 0; g < p.groups; ++g) {
+                    const bool stays = kept >> g & 1;
+                    in = smaller(in, stays ? value[g] : static_cast<double>(kInf));
+                    out = larger(out, stays ? static_cast<double>(-kInf) : value[g]);
+                }
+                tell(in, out, 2.0);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (!(kept >> ((e0 + i) / size & 63) & 1)) key[i] = -kInf;
+        }
+        if (whole) {
+            double first = -kInf, second = -kInf;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                second = larger(second, smaller(first, key[i]));
+                first = larger(first, key[i]);
+            }
+            for (int x = 1; x < wide; x *= 2) {
+                const double a = __shfl_xor(first, x, 64), c = __shfl_xor(second, x, 64);
+                second = larger(smaller(first, a), larger(second, c));
+                first = larger(first, a);
+            }
+            const double v = group_value(first, second);
+            const int group = lane / wide;
+            int before = 0;
+            for (int g = 0; g < p.groups; ++g) {
+                const double w = __shfl(v, g * wide, L);
+                before += w > v || (w == v && g < group);
+            }
+            const bool stays = before < p.top_groups && group < p.groups;
+            if (kScored) {
+                const double in = over_lanes<L>(stays ? v : static_cast<double>(kInf),
+                                                [](double a, double c) { return smaller(a, c); });
+                const double out = over_lanes<L>(stays || group >= p.groups ? static_cast<double>(-kInf) : v,
+                                                 [](double a, double c) { return larger(a, c); });
+                tell(in, out, 2.0);
+            }
+            if (!stays)
+#pragma unroll
+                for (int i = 0; i < N; ++i) key[i] = -kInf;
+        }
+        if constexpr (K > 0) {
+            constexpr int n = N < K ? N : K;
+            double list[K], left = -kInf;
+#pragma unroll
+            for (int c = 0; c < N; c += n) {
+                double part[n];
+#pragma unroll
+                for (int i = 0; i < n; ++i) part[i] = key[c + i];
+                sort_keys<n>(part);
+                if constexpr (n == K) {
+                    if (c > 0) {
+                        join<K>(list, part, left);
+                        continue;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < n; ++i) list[i] = part[i];
+            }
+            left = over_lanes<L>(left, [](double a, double c) { return larger(a, c); });
+            join_lanes<L, K, n>(list, left);
+            constexpr int kHave = n * L < K ? n * L : K;  // keys in the list
+            double mine = -kInf, next = kHave == K ? left : static_cast<double>(-kInf);
+#pragma unroll
+            for (int j = 0; j < kHave; ++j) {
+                if (lane == j) mine = list[j];
+                if (lane + 1 == j) next = list[j];
+            }
+            if (biased) {
+                if (lane < p.top_k) tell(mine, next, 1.0);
+                near = lanes_any<L>(near);
+            }
+            id[0] = lane < p.top_k ? expert_of(mine) : -1;
+        } else {
+            sort_keys<N>(key);
             double last = 0x1p1020;
-            const int rounds = p.top_k + (bias ? 1 : 0);  // with a bias also the best that is left
+            const int rounds = p.top_k + (biased ? 1 : 0);  // with a bias also the best that is left
             for (int r = 0; r < rounds; ++r) {
                 const double best = over_lanes<L>(key[0], [](double a, double c) { return larger(a, c); });
-                if (bias) tell(last, best, 1.0);
+                if (biased) tell(last, best, 1.0);
                 last = best;
                 const bool pop = key[0] == best;
 #pragma unroll
@@ -306,102 +556,47 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const char* __restrict__ 
                 for (int s = 0; s < S; ++s)
                     if (r < p.top_k && r == lane + s * L) id[s] = e;
             }
-            return near;
-        };
-        // The choice by float64 values.
-        auto choose64 = [&]() {
-            double all = 0.0, v[N];
-            if (!p.sigmoid) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) all += exp(static_cast<double>(l[i]) - m);
-                all = lanes_sum<L>(all);
-            }
-            auto score = [&](double x) { return p.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - m) / all; };
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const double c = bias ? score(l[i]) + static_cast<double>(b[i]) : l[i];
-                v[i] = l[i] > -kInf && c > -kInf ? c : -kInf;  // not where either is NaN
-            }
-            if (grouped) {
-                double* value = of_group[threadIdx.x / L];
-                for (int g = 0; g < p.groups; ++g) {
-                    double first = -kInf, second = -kInf;
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const double x = e0 + i >= g * size && e0 + i < (g + 1) * size ? v[i] : -kInf;
-                        second = larger(second, smaller(first, x));
-                        first = larger(first, x);
-                    }
-#pragma unroll
-                    for (int x = 1; x < L; x *= 2) {
-                        const double a = __shfl_xor(first, x, 64), c = __shfl_xor(second, x, 64);
-                        second = larger(smaller(first, a), larger(second, c));
-                        first = larger(first, a);
-                    }
-                    double of = first;
-                    if (p.top2) of = second == -kInf ? second : (bias ? first + second : score(first) + score(second));
-                    if (lane == 0) value[g] = of;
-                }
-                const uint64_t kept = best_groups<L>(value, p, lane, [](double, double) {});
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (!(kept >> ((e0 + i) / size & 63) & 1)) v[i] = -kInf;
-            }
-            struct Best {
-                double value;
-                int expert;
-            };
-            for (int r = 0; r < p.top_k; ++r) {
-                Best best = {-kInf, kMostExperts};
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (v[i] > best.value) best = Best{v[i], e0 + i};
-#pragma unroll
-                for (int x = 1; x < L; x *= 2) {
-                    const Best o = {__shfl_xor(best.value, x, 64), __shfl_xor(best.expert, x, 64)};
-                    if (o.value > best.value || (o.value == best.value && o.expert < best.expert)) best = o;
-                }
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (best.expert == e0 + i) v[i] = -kInf;
-                const int e = best.value > -kInf ? best.expert : -1;
-#pragma unroll
-                for (int s = 0; s < S; ++s)
-                    if (r == lane + s * L) id[s] = e;
-            }
-        };
-#pragma unroll
-        for (int s = 0; s < S; ++s) id[s] = -1;
-        // float32 values tell nearly all tokens; a wavefront with one that they cannot is done again
-        if (__any(choose())) choose64();
-
-        float w[S], lw[S], most = -kInf, all = 0.0f;
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            lw[s] = id[s] >= 0 ? load_logit<T>(row, id[s]) : -kInf;
-            most = fmaxf(most, lw[s]);
         }
-        most = lanes_max<L>(most);
+        return near;
+    };
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            if (!p.renormalise)
-                w[s] = p.sigmoid ? sigmoid32(lw[s]) : expf(lw[s] - m) / sum;
-            else if (!p.sigmoid)
-                w[s] = expf(lw[s] - most);
-            else  // sigmoid(l) over e^min(most, 0), which does not underflow
-                w[s] = expf(fminf(lw[s], 0.0f) - fminf(most, 0.0f)) / (1.0f + expf(-fabsf(lw[s])));
-            if (id[s] < 0) w[s] = 0.0f;
-            all += w[s];
+    for (int s = 0; s < S; ++s) id[s] = -1;
+    const bool near = choose();
+    float w[S], lw[S], most = -kInf, all = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        lw[s] = id[s] >= 0 ? load_logit<T>(row, id[s]) : -kInf;
+        most = fmaxf(most, lw[s]);
+    }
+    most = lanes_max<L>(most);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        if (!p.renormalise)
+            w[s] = p.sigmoid ? sigmoid32(lw[s]) : expf(lw[s] - m) / sum;
+        else if (!p.sigmoid)
+            w[s] = expf(lw[s] - most);
+        else
+            w[s] = over_most(lw[s], most);
+        if (id[s] < 0) w[s] = 0.0f;
+        all += w[s];
+    }
+    if (p.renormalise) all = lanes_sum<L>(all);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int j = lane + s * L;
+        if (p.renormalise && id[s] >= 0) w[s] /= all;
+        if (j < p.top_k && mine < tokens && !(kScored && near)) {
+            ids[t * p.top_k + j] = id[s];
+            weights[t * p.top_k + j] = bad ? __builtin_nanf("") : w[s] * p.scale;
         }
-        if (p.renormalise) all = lanes_sum<L>(all);
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int j = lane + s * L;
-            if (p.renormalise && id[s] >= 0) w[s] /= all;
-            if (j < p.top_k && mine < tokens) {
-                ids[t * p.top_k + j] = id[s];
-                weights[t * p.top_k + j] = bad ? __builtin_nanf("") : w[s] * p.scale;
-            }
+    }
+    if constexpr (kScored) {
+        // float32 values tell nearly all tokens; the others are chosen again, one after the other
+        for (uint64_t left = __ballot(near && mine < tokens); left != 0;) {
+            const int at = __builtin_amdgcn_readfirstlane(__builtin_ctzll(left) / L);  // of the wavefront's tokens
+            left &= L == 64 ? 0 : ~(((1ull << (L & 63)) - 1) << (at * L));
+            const int64_t again = t0 + (threadIdx.x & ~63) / L + at;
+            route64<T>(logits, bias, ids, weights, again, p, value64[threadIdx.x / 64], group64[threadIdx.x / 64]);
         }
     }
 }
@@ -421,114 +616,113 @@ __global__ __launch_bounds__(kBlock) void route_grad_kernel(const float* __restr
     const int lane = threadIdx.x % L, e0 = lane * N;
     Slot* mine_slots = slots[threadIdx.x / L];
     const bool dense = !p.sigmoid && !p.renormalise;
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens; t0 < tokens; t0 += static_cast<int64_t>(gridDim.x) * kTokens) {
-        const int64_t mine = t0 + threadIdx.x / L, t = mine < tokens ? mine : tokens - 1;
-        const char* row = logits + t * p.experts * Elem<T>::kBytes;
-        float l[N], m = -kInf, sum = 0.0f;
-        if (dense) {
-            load_logits<T, N>(row, e0, p.experts, l);
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
+    const int64_t mine = t0 + threadIdx.x / L, t = mine < tokens ? mine : tokens - 1;
+    const char* row = logits + t * p.experts * Elem<T>::kBytes;
+    float l[N], m = -kInf, sum = 0.0f;
+    if (dense) {
+        load_logits<T, N>(row, e0, p.experts, l);
 #pragma unroll
-            for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
-            m = lanes_max<L>(m);
+        for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
+        m = lanes_max<L>(m);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                l[i] = m > -kInf ? expf(l[i] - m) : 0.0f;
-                sum += l[i];
-            }
-            sum = lanes_sum<L>(sum);
-#pragma unroll
-            for (int i = 0; i < N; ++i) l[i] = m > -kInf ? l[i] / sum : 0.0f;
+        for (int i = 0; i < N; ++i) {
+            l[i] = m > -kInf ? expf(l[i] - m) : 0.0f;
+            sum += l[i];
         }
-        int id[S];
-        float u[S], lw[S], v[S], most = -kInf;
+        sum = lanes_sum<L>(sum);
+#pragma unroll
+        for (int i = 0; i < N; ++i) l[i] = m > -kInf ? l[i] / sum : 0.0f;
+    }
+    int id[S];
+    float u[S], lw[S], v[S], most = -kInf;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int j = lane + s * L;
+        id[s] = j < p.top_k ? ids[t * p.top_k + j] : -1;
+        if (id[s] < 0 || id[s] >= p.experts) id[s] = -1;
+        u[s] = id[s] >= 0 ? grad_weights[t * p.top_k + j] * p.scale : 0.0f;
+        lw[s] = id[s] >= 0 ? load_logit<T>(row, id[s]) : -kInf;
+        most = fmaxf(most, lw[s]);
+    }
+    float dot = 0.0f, all = 0.0f;
+    if (p.renormalise) {
+        most = lanes_max<L>(most);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            const int j = lane + s * L;
-            id[s] = j < p.top_k ? ids[t * p.top_k + j] : -1;
-            if (id[s] < 0 || id[s] >= p.experts) id[s] = -1;
-            u[s] = id[s] >= 0 ? grad_weights[t * p.top_k + j] * p.scale : 0.0f;
-            lw[s] = id[s] >= 0 ? load_logit<T>(row, id[s]) : -kInf;
-            most = fmaxf(most, lw[s]);
+            v[s] = 0.0f;
+            if (id[s] >= 0 && !(most == -kInf))
+                v[s] = p.sigmoid ? over_most(lw[s], most) : expf(lw[s] - most);
+            all += v[s];
         }
-        float dot = 0.0f, all = 0.0f;
-        if (p.renormalise) {
-            most = lanes_max<L>(most);
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                v[s] = 0.0f;
-                if (id[s] >= 0 && !(most == -kInf))
-                    v[s] = p.sigmoid ? expf(fminf(lw[s], 0.0f) - fminf(most, 0.0f)) / (1.0f + expf(-fabsf(lw[s])))
-                                     : expf(lw[s] - most);
-                all += v[s];
-            }
-            all = lanes_sum<L>(all);
-#pragma unroll
-            for (int s = 0; s < S; ++s) {
-                v[s] = all == 0.0f ? 0.0f : v[s] / all;
-                dot += u[s] * v[s];
-            }
-            dot = lanes_sum<L>(dot);
-        } else if (!p.sigmoid) {
-#pragma unroll
-            for (int s = 0; s < S; ++s) dot += id[s] >= 0 && m > -kInf ? u[s] * (expf(lw[s] - m) / sum) : 0.0f;
-            dot = lanes_sum<L>(dot);
-        }
+        all = lanes_sum<L>(all);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            float d = u[s];
-            if (p.renormalise) d = v[s] * (u[s] - dot);
-            if (p.sigmoid) d *= p.renormalise ? sigmoid32(-lw[s]) : sigmoid32(lw[s]) * sigmoid32(-lw[s]);
-            mine_slots[lane + s * L] = Slot{id[s], id[s] >= 0 ? d : 0.0f};
+            v[s] = all == 0.0f ? 0.0f : v[s] / all;
+            dot += u[s] * v[s];
         }
-        __threadfence_block();
-        __builtin_amdgcn_wave_barrier();
-        float g[N];
+        dot = lanes_sum<L>(dot);
+    } else if (!p.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) g[i] = 0.0f;
-        for (int j = 0; j < p.top_k; ++j) {
-            const Slot s = mine_slots[j];
+        for (int s = 0; s < S; ++s) dot += id[s] >= 0 && m > -kInf ? u[s] * (expf(lw[s] - m) / sum) : 0.0f;
+        dot = lanes_sum<L>(dot);
+    }
 #pragma unroll
-            for (int i = 0; i < N; ++i) g[i] += s.id == e0 + i ? s.d : 0.0f;
-        }
-        __builtin_amdgcn_wave_barrier();
-        if (dense)
+    for (int s = 0; s < S; ++s) {
+        float d = u[s];
+        if (p.renormalise) d = v[s] * (u[s] - dot);
+        if (p.sigmoid) d *= p.renormalise ? sigmoid32(-lw[s]) : sigmoid32(lw[s]) * sigmoid32(-lw[s]);
+        mine_slots[lane + s * L] = Slot{id[s], id[s] >= 0 ? d : 0.0f};
+    }
+    __threadfence_block();
+    __builtin_amdgcn_wave_barrier();
+    float g[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) g[i] = l[i] * (g[i] - dot);
-        if (mine >= tokens) continue;
-        char* to = grad_logits + t * p.experts * Elem<T>::kBytes;
-        constexpr int V = N < 4 ? N : 4;
+    for (int i = 0; i < N; ++i) g[i] = 0.0f;
+    for (int j = 0; j < p.top_k; ++j) {
+        const Slot s = mine_slots[j];
 #pragma unroll
-        for (int i = 0; i < N; i += V) {
-            if (V == 4 && e0 + i + 4 <= p.experts) {
-                if constexpr (T == MOE_EPI_F32) {
-                    typedef u32x4 loose __attribute__((aligned(4)));
-                    u32x4 w;
+        for (int i = 0; i < N; ++i) g[i] += s.id == e0 + i ? s.d : 0.0f;
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (dense)
 #pragma unroll
-                    for (int j = 0; j < V; ++j) w[j] = __float_as_uint(g[i + j]);
-                    *reinterpret_cast<loose*>(to + 4 * (e0 + i)) = w;
-                } else {
-                    typedef u32x2 loose __attribute__((aligned(2)));
-                    const float f[8] = {g[i], g[i + 1 < N ? i + 1 : i], g[i + 2 < N ? i + 2 : i],
-                                        g[i + 3 < N ? i + 3 : i], 0, 0, 0, 0};
-                    const u32x4 w = Elem<T>::pack(f);
-                    *reinterpret_cast<loose*>(to + 2 * (e0 + i)) = u32x2{w[0], w[1]};
-                }
+        for (int i = 0; i < N; ++i) g[i] = l[i] * (g[i] - dot);
+    if (mine >= tokens) return;
+    char* to = grad_logits + t * p.experts * Elem<T>::kBytes;
+    constexpr int V = N < 4 ? N : 4;
+#pragma unroll
+    for (int i = 0; i < N; i += V) {
+        if (V == 4 && e0 + i + 4 <= p.experts) {
+            if constexpr (T == MOE_EPI_F32) {
+                typedef u32x4 loose __attribute__((aligned(4)));
+                u32x4 w;
+#pragma unroll
+                for (int j = 0; j < V; ++j) w[j] = __float_as_uint(g[i + j]);
+                *reinterpret_cast<loose*>(to + 4 * (e0 + i)) = w;
             } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (e0 + i + j < p.experts) Elem<T>::store1(to, e0 + i + j, g[i + j]);
+                typedef u32x2 loose __attribute__((aligned(2)));
+                const float f[8] = {g[i], g[i + 1 < N ? i + 1 : i], g[i + 2 < N ? i + 2 : i],
+                                    g[i + 3 < N ? i + 3 : i], 0, 0, 0, 0};
+                const u32x4 w = Elem<T>::pack(f);
+                *reinterpret_cast<loose*>(to + 2 * (e0 + i)) = u32x2{w[0], w[1]};
             }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (e0 + i + j < p.experts) Elem<T>::store1(to, e0 + i + j, g[i + j]);
         }
     }
 }
 
-// f(lanes of a token, experts of a lane, chosen of a lane)
+// f(lanes of a token, experts of a lane, chosen of a lane, length of a list)
 template <class F>
 void by_size(int experts, int top_k, F f) {
     auto go = [&](auto l, auto n) {
         constexpr int L = decltype(l)::value;
-        if (top_k <= L) return f(l, n, std::integral_constant<int, 1>());
-        f(l, n, std::integral_constant<int, kMostChosen / L>());
+        const std::integral_constant<int, 1> one;
+        if (top_k <= 8) return f(l, n, one, std::integral_constant<int, 8>());
+        f(l, n, std::integral_constant<int, kMostChosen / L>(), std::integral_constant<int, 0>());
     };
     const std::integral_constant<int, 16> l16, n16;
     if (experts <= 16) return go(l16, std::integral_constant<int, 1>());
@@ -537,7 +731,7 @@ void by_size(int experts, int top_k, F f) {
     if (experts <= 128) return go(l16, std::integral_constant<int, 8>());
     if (experts <= 256) return go(l16, n16);
     if (experts <= 512) return go(std::integral_constant<int, 32>(), n16);
-    f(std::integral_constant<int, 64>(), n16, std::integral_constant<int, 1>());
+    go(std::integral_constant<int, 64>(), n16);
 }
 
 template <class F>
@@ -583,11 +777,19 @@ extern "C" int moe_route_fwd(const void* logits, int dtype, const float* bias, i
                       renormalise != 0, scale};
     (void)hipGetLastError();
     by_type(dtype, [&](auto t) {
-        by_size(p.experts, p.top_k, [&](auto l, auto n, auto k) {
+        by_size(p.experts, p.top_k, [&](auto l, auto n, auto s, auto k) {
             constexpr int L = decltype(l)::value;
-            hipLaunchKernelGGL((route_kernel<decltype(t)::value, L, decltype(n)::value, decltype(k)::value>),
-                               dim3(grid_for_rows(tokens, kBlock / L)), dim3(kBlock), 0, as_stream(stream),
-                               static_cast<const char*>(logits), bias, ids, weights, tokens, p);
+            auto go = [&](auto kernel) {
+                for (int64_t t = 0; t < tokens; t += kMostTokens) {
+                    const int64_t here = tokens - t < kMostTokens ? tokens - t : kMostTokens;
+                    hipLaunchKernelGGL(kernel, dim3(grid_for_rows(here, kBlock / L)), dim3(kBlock), 0,
+                                       as_stream(stream), static_cast<const char*>(logits) + t * experts * e, bias,
+                                       ids + t * top_k, weights + t * top_k, here, p);
+                }
+            };
+            constexpr int T = decltype(t)::value, N = decltype(n)::value, S = decltype(s)::value, K = decltype(k)::value;
+            bias || (p.top2 && p.groups > 1) ? go(route_kernel<T, L, N, S, K, true>)
+                                             : go(route_kernel<T, L, N, S, K, false>);
         });
     });
     return launch_status();
@@ -611,12 +813,16 @@ extern "C" int moe_route_bwd(const float* grad_weights, const void* logits, int 
     const Choice p = {static_cast<int>(experts), static_cast<int>(top_k), 1, 1, score == MOE_EPI_SIGMOID, false,
                       renormalise != 0, scale};
     (void)hipGetLastError();
-    by_type(dtype, [&](auto t) {
-        by_size(p.experts, p.top_k, [&](auto l, auto n, auto k) {
+    by_type(dtype, [&](auto t_) {
+        by_size(p.experts, p.top_k, [&](auto l, auto n, auto s, auto k) {
             constexpr int L = decltype(l)::value;
-            hipLaunchKernelGGL((route_grad_kernel<decltype(t)::value, L, decltype(n)::value, decltype(k)::value>),
-                               dim3(grid_for_rows(tokens, kBlock / L)), dim3(kBlock), 0, as_stream(stream), grad_weights,
-                               static_cast<const char*>(logits), ids, static_cast<char*>(grad_logits), tokens, p);
+            for (int64_t t = 0; t < tokens; t += kMostTokens) {
+                const int64_t here = tokens - t < kMostTokens ? tokens - t : kMostTokens;
+                hipLaunchKernelGGL((route_grad_kernel<decltype(t_)::value, L, decltype(n)::value, decltype(s)::value>),
+                                   dim3(grid_for_rows(here, kBlock / L)), dim3(kBlock), 0, as_stream(stream),
+                                   grad_weights + t * top_k, static_cast<const char*>(logits) + t * experts * e,
+                                   ids + t * top_k, static_cast<char*>(grad_logits) + t * experts * e, here, p);
+            }
         });
     });
     return launch_status();

@@ -79,7 +79,7 @@ int64_t rms_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
  *   weight    [experts, hidden] of w_dtype (dtype or float32) in
  *   logits    [tokens, experts] float32                       out
  *   workspace moe_router_logits_workspace_bytes(tokens, hidden, experts) bytes; may be NULL if that is 0
- * experts in [1, 1024], any hidden >= 1, tokens <= INT32_MAX.
+ * experts in [1, 1024], hidden in [1, 2^24], tokens <= INT32_MAX.
  */
 int moe_router_logits_fwd(const void *x, int dtype, const void *weight, int w_dtype, float *logits, void *workspace,
                           int64_t workspace_bytes, int64_t tokens, int64_t hidden, int64_t experts, void *stream);

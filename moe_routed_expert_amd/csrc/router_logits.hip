@@ -10,14 +10,16 @@ namespace {
 
 constexpr int kBlock = 256;
 constexpr int64_t kMostExperts = 1024;
+constexpr int64_t kMostHidden = 1 << 24;  // 32 rows of it have 32-bit offsets
 
 // ---- logits ---------------------------------------------------------------------
 
 constexpr int kStep = 64;       // of hidden, in one pass of the loop
-constexpr int kTileRows = 128;  // tokens of a block: 32 for each of 4 wavefronts
+constexpr int kTileRows = 128;  // tokens of a block
 constexpr int64_t kMostRows = 1 << 24;  // tokens of a launch
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 512;
 constexpr int kFewWaves = 8;
+constexpr int64_t kFewHidden = 3000;
 
 // Pieces that x and the weight are cut into.
 template <int T, int W>
@@ -39,115 +41,97 @@ __device__ __forceinline__ void put4(float* row, int64_t e, int64_t experts, f32
     }
 }
 
-// 128 tokens x 16 NT experts, over the steps [steps z / n, steps (z + 1) / n) of hidden.
-template <int T, int W, int NT>
-__global__ __launch_bounds__(kBlock) void logits_tile_kernel(const char* __restrict__ x, const char* __restrict__ weight,
-                                                             float* __restrict__ out, int64_t tokens, int64_t hidden,
-                                                             int64_t experts) {
+constexpr int kTileWaves = 8;
+
+// 16 tokens x 16 NT experts for each of 8 wavefronts, over the steps [steps z / n,
+// steps (z + 1) / n) of hidden, kDeep - 1 of which are on their way.
+template <int T, int W, int NT, int kDeep>
+__global__ __launch_bounds__(64 * kTileWaves, 4) void logits_tile_kernel(const char* __restrict__ x,
+                                                                         const char* __restrict__ weight,
+                                                                         float* __restrict__ out, int64_t tokens,
+                                                                         int64_t hidden, int64_t experts) {
     typedef Pieces<T, W> P;
     typedef Piece8<T> X;
     typedef Piece8<W> Y;
-    constexpr int kFrags = 2 * NT, kMine = (kFrags + 3) / 4;
+    constexpr int kFrags = 2 * NT;
+    static_assert(kFrags <= kTileWaves && kDeep % 2 == 0, "");
     __shared__ u32x4 lds[2][P::kW][kFrags][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int of16 = lane % 16, k8 = lane / 16 * 8;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kTileRows + 32 * wave, e0 = blockIdx.y * 16 * NT;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kTileRows + 16 * wave + of16, e0 = blockIdx.y * 16 * NT;
     const int64_t steps = (hidden + kStep - 1) / kStep;
     const int64_t first = steps * blockIdx.z / gridDim.z, last = steps * (blockIdx.z + 1) / gridDim.z;
-    const char* px[2];
+    const int64_t e = e0 + 16 * (wave / 2) + of16;
+    const bool staging = wave < kFrags;
+    const char* px = x + ((t < tokens ? t : tokens - 1) * hidden + k8) * X::kBytes;
+    const char* pw = weight + ((e < experts ? e : experts - 1) * hidden + 32 * (wave % 2) + k8) * Y::kBytes;
+    f32x4 d[NT];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        const int64_t t = row0 + 16 * m + of16;
-        px[m] = x + ((t < tokens ? t : tokens - 1) * hidden + k8) * X::kBytes;
-    }
-    const char* pw[kMine];
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-        const int f = wave + 4 * i;
-        const int64_t e = e0 + 16 * (f / 2) + of16;
-        pw[i] = weight + ((e < experts ? e : experts - 1) * hidden + 32 * (f % 2) + k8) * Y::kBytes;
-    }
-    f32x4 d[2][NT];
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) d[m][n] = f32x4{0, 0, 0, 0};
+    for (int n = 0; n < NT; ++n) d[n] = f32x4{0, 0, 0, 0};
 
     struct Ahead {
-        typename X::Raw x[2][2];
-        typename Y::Raw w[kMine];
+        typename X::Raw x[2];
+        typename Y::Raw w;
     };
     auto load = [&](int64_t step, Ahead& a) {
-        const int64_t k = step * kStep, left = hidden - k - k8;
-        if (k + kStep <= hidden) {
+        const int64_t k = step * kStep;
+        if (staging) a.w = Y::load(pw + k * Y::kBytes);
 #pragma unroll
-            for (int i = 0; i < kMine; ++i)
-                if (kFrags >= 4 || wave < kFrags) a.w[i] = Y::load(pw[i] + k * Y::kBytes);
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) a.x[m][h] = X::load_nt(px[m] + (k + 32 * h) * X::kBytes);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kMine; ++i)
-                if (kFrags >= 4 || wave < kFrags)
-                    a.w[i] = Y::load_first(pw[i] + k * Y::kBytes, left - 32 * ((wave + 4 * i) % 2));
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) a.x[m][h] = X::load_first(px[m] + (k + 32 * h) * X::kBytes, left - 32 * h);
-        }
+        for (int h = 0; h < 2; ++h) a.x[h] = X::load(px + (k + 32 * h) * X::kBytes);
     };
     auto stage = [&](const Ahead& a, int buf) {
+        if (!staging) return;
+        u32x4 piece[P::kW];
+        cut_raw<W, P::kW>(a.w, piece);
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            if (kFrags < 4 && wave >= kFrags) continue;
-            u32x4 piece[P::kW];
-            cut_raw<W, P::kW>(a.w[i], piece);
-#pragma unroll
-            for (int p = 0; p < P::kW; ++p) lds[buf][p][wave + 4 * i][lane] = piece[p];
-        }
+        for (int p = 0; p < P::kW; ++p) lds[buf][p][wave][lane] = piece[p];
     };
     auto multiply = [&](const Ahead& a, int buf) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            u32x4 xp[2][P::kX];
-#pragma unroll
-            for (int m = 0; m < 2; ++m) cut_raw<T, P::kX>(a.x[m][h], xp[m]);
+            u32x4 xp[P::kX];
+            cut_raw<T, P::kX>(a.x[h], xp);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 u32x4 wp[P::kW];
 #pragma unroll
                 for (int p = 0; p < P::kW; ++p) wp[p] = lds[buf][p][2 * n + h][lane];
-#pragma unroll
-                for (int m = 0; m < 2; ++m) d[m][n] = mfma_pieces<P::kF16>(wp, xp[m], d[m][n]);
+                d[n] = mfma_pieces<P::kF16>(wp, xp, d[n]);
             }
         }
     };
-    auto pass = [&](int64_t s, const Ahead& now, Ahead& next, int buf) {
-        if (s + 1 < last) load(s + 1, next);
-        multiply(now, buf);
-        if (s + 1 < last) stage(next, buf ^ 1);
+    const int64_t whole = hidden / kStep < last ? hidden / kStep : last;  // the last step may have fewer than 64
+    if (first < whole) {
+        Ahead a[kDeep];
+#pragma unroll
+        for (int i = 0; i < kDeep - 1; ++i)
+            if (first + i < whole) load(first + i, a[i]);
+        stage(a[0], 0);
         __syncthreads();
-    };
-    Ahead a, b;
-    if (first < last) {
-        load(first, a);
+        for (int64_t s = first; s < whole; s += kDeep)
+#pragma unroll
+            for (int i = 0; i < kDeep; ++i) {
+                if (s + i >= whole) break;
+                if (s + i + kDeep - 1 < whole) load(s + i + kDeep - 1, a[(i + kDeep - 1) % kDeep]);
+                multiply(a[i], i & 1);
+                if (s + i + 1 < whole) stage(a[(i + 1) % kDeep], (i + 1) & 1);
+                __syncthreads();
+            }
+    }
+    if (whole < last) {
+        Ahead a;
+        const int64_t k = whole * kStep, left = hidden - k - k8;
+        if (staging) a.w = Y::load_first(pw + k * Y::kBytes, left - 32 * (wave % 2));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) a.x[h] = X::load_first(px + (k + 32 * h) * X::kBytes, left - 32 * h);
         stage(a, 0);
+        __syncthreads();
+        multiply(a, 0);
     }
-    __syncthreads();
-    for (int64_t s = first; s < last; s += 2) {
-        pass(s, a, b, 0);
-        if (s + 1 < last) pass(s + 1, b, a, 1);
-    }
-    float* to = out + blockIdx.z * tokens * experts;
+    if (t >= tokens) return;
+    float* to = out + (blockIdx.z * tokens + t) * experts;
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        const int64_t t = row0 + 16 * m + of16;
-        if (t >= tokens) continue;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) put4(to + t * experts, e0 + 16 * n + lane / 16 * 4, experts, d[m][n]);
-    }
+    for (int n = 0; n < NT; ++n) put4(to, e0 + 16 * n + lane / 16 * 4, experts, d[n]);
 }
 
 // Up to 16 MT tokens x 16 experts: 8 wavefronts share the steps of hidden that
@@ -232,13 +216,18 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(const float* __restri
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Parts that hidden is shared by: enough blocks for the chip, and a few steps each.
+// Parts that hidden is shared by. Few tokens: a launch that adds up the parts
+// costs about as much as 3000 of hidden for 16 tokens. Many: two blocks per CU.
 int64_t logits_parts(int64_t tokens, int64_t hidden, int64_t experts) {
-    const bool few = tokens <= kFewRows;
-    const int64_t blocks = few ? up(experts, 16) : up(tokens, kTileRows) * up(experts, 64);
-    const int64_t wanted = up(few ? 16 : 256, blocks), most = up(hidden, few ? 32 * kFewWaves : 4 * kStep);
+    if (tokens == 0) return 1;
+    if (tokens <= kFewRows) {
+        const int64_t n = up(hidden * (tokens <= 16 ? 1 : (tokens <= 32 ? 2 : 4)), kFewHidden);
+        const int64_t most = up(256, up(experts, 16) * up(tokens, 64));
+        return n < most ? n : most;
+    }
+    const int64_t blocks = up(tokens, kTileRows) * up(experts, 64), wanted = 512 / blocks, most = up(hidden, 8 * kStep);
     const int64_t n = wanted < most ? wanted : most;
-    return n < 1 ? 1 : n;
+    return n < 1 ? 1 : (n > 16 ? 16 : n);
 }
 
 // ---- gradients ----------------------------------------------------------------------
@@ -383,7 +372,7 @@ __global__ __launch_bounds__(kBlock) void grad_x_kernel(const float* __restrict_
                     const float f[8] = {d[0][m][0], d[0][m][1], d[0][m][2], d[0][m][3],
                                         d[1][m][0], d[1][m][1], d[1][m][2], d[1][m][3]};
                     if (h + 8 <= hidden) {
-                        __builtin_nontemporal_store(Elem<T>::pack(f), reinterpret_cast<loose*>(to));
+                        *reinterpret_cast<loose*>(to) = Elem<T>::pack(f);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -392,7 +381,7 @@ __global__ __launch_bounds__(kBlock) void grad_x_kernel(const float* __restrict_
                 } else if constexpr (T == MOE_EPI_F32) {
                     typedef f32x4 loose __attribute__((aligned(4)));
                     if (h + 4 <= hidden) {
-                        __builtin_nontemporal_store(d[0][m], reinterpret_cast<loose*>(to));
+                        *reinterpret_cast<loose*>(to) = d[0][m];
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -459,19 +448,60 @@ __global__ __launch_bounds__(kBlock) void grad_x_many_kernel(const float* __rest
     }
 }
 
-// 16 ET experts x 64 HT hidden, over the tokens of part z: the tokens are the
-// inner dimension. A wavefront reads 8 tokens' elements of its hidden and turns
-// them into operands in registers; the operands of grad are made once a block.
+// 8 bytes of a row, of which `left` elements exist.
+template <int T>
+__device__ __forceinline__ u32x2 load8(const char* p, int64_t left) {
+    u32x2 r = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8 / Elem<T>::kBytes; ++i) {
+        if (i >= left) continue;
+        if constexpr (T == MOE_EPI_F32)
+            r[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        else
+            r[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << (16 * (i % 2));
+    }
+    return r;
+}
+
+// As turn_rows for rows of 8 bytes.
+template <int T, int P>
+__device__ __forceinline__ void turn_short_rows(const u32x2 (&r)[8], u32x4 (&piece)[8 / Elem<T>::kBytes][P]) {
+    if constexpr (T == MOE_EPI_F32) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r[i][j]);
+            cut<P>(f, piece[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            u32x4 t;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                t[i] = __builtin_amdgcn_perm(r[2 * i + 1][j / 2], r[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+            cut_raw<T, P>(typename Piece8<T>::Raw{{t}}, piece[j]);
+        }
+    }
+}
+
+constexpr int kGradWaves = 8;
+
+// 16 ET experts x 16 HT hidden for each of 8 wavefronts, over the tokens of part
+// z: the tokens are the inner dimension. A wavefront reads 8 tokens' elements of
+// its hidden, 8 bytes a lane and token, and turns them into operands in
+// registers; the operands of grad are made once a block.
 template <int T, int W, int ET>
-__global__ __launch_bounds__(kBlock) void grad_weight_kernel(const float* __restrict__ grad, const char* __restrict__ x,
+__global__ __launch_bounds__(64 * kGradWaves) void grad_weight_kernel(const float* __restrict__ grad, const char* __restrict__ x,
                                                              float* __restrict__ parts, int64_t tokens, int64_t hidden,
                                                              int64_t experts) {
     typedef GradPieces<T, W> P;
-    constexpr int HT = 16 / Elem<T>::kBytes;  // hidden of a lane: 16 bytes
+    constexpr int HT = 8 / Elem<T>::kBytes;  // hidden of a lane
     __shared__ u32x4 lds[2][ET][P::kGrad][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int of16 = lane % 16, k8 = lane / 16 * 8;
-    const int64_t h = static_cast<int64_t>(blockIdx.x) * 64 * HT + wave * 16 * HT + of16 * HT;
+    const int64_t h = static_cast<int64_t>(blockIdx.x) * 16 * kGradWaves * HT + wave * 16 * HT + of16 * HT;
     const int64_t e0 = blockIdx.y * 16 * ET, mine = e0 + 16 * wave + of16;
     const int64_t steps = (tokens + 31) / 32;
     const int64_t first = steps * blockIdx.z / gridDim.z, last = steps * (blockIdx.z + 1) / gridDim.z;
@@ -482,18 +512,23 @@ __global__ __launch_bounds__(kBlock) void grad_weight_kernel(const float* __rest
 #pragma unroll
         for (int j = 0; j < HT; ++j) d[e][j] = f32x4{0, 0, 0, 0};
     struct Ahead {
-        u32x4 x[8];
+        u32x2 x[8];
         float g[8];
     };
+    // Columns past the last hidden element or expert are loaded from what comes after, or from the first ones, and
+    // not stored; only the tensors' last token, in the last step, has nothing after it.
+    // A load's address is that of a token, which the wavefront shares, and the lane's 32-bit place from there.
+    const uint32_t at = static_cast<uint32_t>((k8 * hidden + (left > 0 ? h : 0)) * Elem<T>::kBytes);
+    const uint32_t at_g = static_cast<uint32_t>((k8 * experts + (mine < experts ? mine : experts - 1)) * 4);
+    auto token_x = [&](int64_t t) { return x + t * hidden * Elem<T>::kBytes; };
+    auto token_g = [&](int64_t t) { return reinterpret_cast<const char*>(grad + t * experts); };
     auto load = [&](int64_t s, Ahead& a) {
-        const int64_t t = s * 32 + k8;
-        const char* px = x + (t * hidden + h) * Elem<T>::kBytes;
+        typedef u32x2 loose __attribute__((aligned(2)));
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            a.x[i] = t + i < tokens && left > 0 ? load16<T>(px + i * hidden * Elem<T>::kBytes, left) : u32x4{0, 0, 0, 0};
+        for (int i = 0; i < 8; ++i) a.x[i] = *reinterpret_cast<const loose*>(token_x(s * 32 + i) + at);
         if (wave < ET) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) a.g[i] = t + i < tokens && mine < experts ? grad[(t + i) * experts + mine] : 0.0f;
+            for (int i = 0; i < 8; ++i) a.g[i] = *reinterpret_cast<const float*>(token_g(s * 32 + i) + at_g);
         }
     };
     auto stage = [&](Ahead& a, int buf) {
@@ -503,10 +538,9 @@ __global__ __launch_bounds__(kBlock) void grad_weight_kernel(const float* __rest
 #pragma unroll
         for (int p = 0; p < P::kGrad; ++p) lds[buf][wave][p][lane] = piece[p];
     };
-    auto pass = [&](int64_t s, Ahead& now, Ahead& next, int buf) {
-        if (s + 1 < last) load(s + 1, next);
+    auto multiply = [&](Ahead& now, int buf) {
         u32x4 v[HT][P::kOther];
-        turn_rows<T, P::kOther>(now.x, v);
+        turn_short_rows<T, P::kOther>(now.x, v);
 #pragma unroll
         for (int e = 0; e < ET; ++e) {
             u32x4 g[P::kGrad];
@@ -515,18 +549,37 @@ __global__ __launch_bounds__(kBlock) void grad_weight_kernel(const float* __rest
 #pragma unroll
             for (int j = 0; j < HT; ++j) d[e][j] = mfma_pieces<false, P::kMost>(g, v[j], d[e][j]);
         }
-        if (s + 1 < last) stage(next, buf ^ 1);
-        __syncthreads();
     };
-    Ahead a, b;
-    if (first < last) {
-        load(first, a);
-        stage(a, 0);
+    const int64_t whole = (tokens - 1) / 32 < last ? (tokens - 1) / 32 : last;  // steps before the last token's
+    constexpr int kDeep = 4;
+    if (first < whole) {
+        Ahead a[kDeep];
+#pragma unroll
+        for (int i = 0; i < kDeep - 1; ++i)
+            if (first + i < whole) load(first + i, a[i]);
+        stage(a[0], 0);
+        __syncthreads();
+        for (int64_t s = first; s < whole; s += kDeep)
+#pragma unroll
+            for (int i = 0; i < kDeep; ++i) {
+                if (s + i >= whole) break;
+                if (s + i + kDeep - 1 < whole) load(s + i + kDeep - 1, a[(i + kDeep - 1) % kDeep]);
+                multiply(a[i], i & 1);
+                if (s + i + 1 < whole) stage(a[(i + 1) % kDeep], (i + 1) & 1);
+                __syncthreads();
+            }
     }
-    __syncthreads();
-    for (int64_t s = first; s < last; s += 2) {
-        pass(s, a, b, 0);
-        if (s + 1 < last) pass(s + 1, b, a, 1);
+    if (whole < last) {
+        Ahead a;
+        const int64_t t = whole * 32 + k8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            a.x[i] = t + i < tokens && left > 0 ? load8<T>(token_x(whole * 32 + i) + at, left) : u32x2{0, 0};
+            a.g[i] = t + i < tokens && wave < ET ? *reinterpret_cast<const float*>(token_g(whole * 32 + i) + at_g) : 0.0f;
+        }
+        stage(a, 0);
+        __syncthreads();
+        multiply(a, 0);
     }
     float* to = parts + blockIdx.z * experts * hidden;
 #pragma unroll
@@ -554,16 +607,15 @@ __global__ __launch_bounds__(kBlock) void add_weight_parts_kernel(const float* _
 
 // Parts that the tokens are shared by for the weight's gradient.
 int64_t grad_parts(int64_t tokens, int64_t hidden, int64_t experts) {
-    const int64_t blocks = up(hidden, 512) * up(experts, 64), wanted = up(512, blocks), most = up(tokens, 4 * 32);
+    const int64_t blocks = up(hidden, 512) * up(experts, 64), wanted = 256 / blocks, most = up(tokens, 4 * 32);
     const int64_t n = wanted < most ? wanted : most;
     return n < 1 ? 1 : n;
 }
 
 bool sizes_ok(int64_t tokens, int64_t hidden, int64_t experts) {
     int64_t a;
-    return tokens >= 0 && tokens <= INT32_MAX && experts >= 1 && experts <= kMostExperts &&
-           bytes_ok(tokens, hidden, 4, &a) && bytes_ok(experts, hidden, 4, &a) && bytes_ok(tokens, experts, 4, &a) &&
-           row_fits_u32_offsets(hidden, 4);
+    return tokens >= 0 && tokens <= INT32_MAX && experts >= 1 && experts <= kMostExperts && hidden <= kMostHidden &&
+           bytes_ok(tokens, hidden, 4, &a) && bytes_ok(experts, hidden, 4, &a) && bytes_ok(tokens, experts, 4, &a);
 }
 
 template <int T, int W>
@@ -573,7 +625,8 @@ void launch_logits(const void* x, const void* weight, float* logits, float* work
     float* to = n > 1 ? workspace : logits;
     const char *px = static_cast<const char*>(x), *pw = static_cast<const char*>(weight);
     if (tokens <= kFewRows) {
-        const dim3 grid(static_cast<unsigned>(up(experts, 16)), 1, static_cast<unsigned>(n)), block(64 * kFewWaves);
+        const dim3 grid(static_cast<unsigned>(up(experts, 16)), static_cast<unsigned>(up(tokens, 64)), static_cast<unsigned>(n)),
+            block(64 * kFewWaves);
         auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, px, pw, to, tokens, hidden, experts); };
         if (tokens <= 16)
             go(logits_few_kernel<T, W, 1>);
@@ -582,22 +635,23 @@ void launch_logits(const void* x, const void* weight, float* logits, float* work
         else
             go(logits_few_kernel<T, W, 4>);
     } else {
+        constexpr int kDeep = W == MOE_EPI_F32 && T != MOE_EPI_F32 ? 4 : 2;
         auto go = [&](auto kernel, int nt) {
             // a grid has fewer than 2^32 work-items; calls of so many tokens have one part
             for (int64_t t = 0; t < tokens; t += kMostRows) {
                 const int64_t here = tokens - t < kMostRows ? tokens - t : kMostRows;
                 const dim3 grid(static_cast<unsigned>(up(here, kTileRows)), static_cast<unsigned>(up(experts, 16 * nt)),
                                 static_cast<unsigned>(n));
-                hipLaunchKernelGGL(kernel, grid, dim3(kBlock), 0, st, px + t * hidden * Elem<T>::kBytes, pw,
+                hipLaunchKernelGGL(kernel, grid, dim3(64 * kTileWaves), 0, st, px + t * hidden * Elem<T>::kBytes, pw,
                                    to + t * experts, here, hidden, experts);
             }
         };
         if (experts <= 16)
-            go(logits_tile_kernel<T, W, 1>, 1);
+            go(logits_tile_kernel<T, W, 1, kDeep>, 1);
         else if (experts <= 32)
-            go(logits_tile_kernel<T, W, 2>, 2);
+            go(logits_tile_kernel<T, W, 2, kDeep>, 2);
         else
-            go(logits_tile_kernel<T, W, 4>, 4);
+            go(logits_tile_kernel<T, W, 4, kDeep>, 4);
     }
     if (n > 1) {
         const int64_t all = tokens * experts, blocks = up(all, kBlock);
@@ -641,9 +695,9 @@ void launch_grad_weight(const float* grad, const void* x, void* grad_weight, flo
                         int64_t hidden, int64_t experts, hipStream_t st) {
     const int64_t n = grad_parts(tokens, hidden, experts);
     auto go = [&](auto kernel, int et) {
-        const dim3 grid(static_cast<unsigned>(up(hidden, 64 * 16 / Elem<T>::kBytes)),
+        const dim3 grid(static_cast<unsigned>(up(hidden, 16 * kGradWaves * 8 / Elem<T>::kBytes)),
                         static_cast<unsigned>(up(experts, 16 * et)), static_cast<unsigned>(n));
-        hipLaunchKernelGGL(kernel, grid, dim3(kBlock), 0, st, grad, static_cast<const char*>(x), workspace, tokens,
+        hipLaunchKernelGGL(kernel, grid, dim3(64 * kGradWaves), 0, st, grad, static_cast<const char*>(x), workspace, tokens,
                            hidden, experts);
     };
     if (experts <= 16)

@@ -85,6 +85,19 @@ __device__ __forceinline__ void cut(float (&f)[8], u32x4 (&piece)[P]) {
             f[2 * i + 1] -= bf16_hi(w);
         }
 }
+// Four values as P pieces.
+template <int P>
+__device__ __forceinline__ void cut4(float (&f)[4], u32x2 (&piece)[P]) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t w = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+            piece[p][i] = w;
+            f[2 * i] -= bf16_lo(w);
+            f[2 * i + 1] -= bf16_hi(w);
+        }
+}
 // r as P pieces; the type itself where it has one piece.
 template <int T, int P>
 __device__ __forceinline__ void cut_raw(const typename Piece8<T>::Raw& r, u32x4 (&piece)[P]) {

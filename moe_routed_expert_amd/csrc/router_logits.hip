@@ -43,28 +43,39 @@ __device__ __forceinline__ void put4(float* row, int64_t e, int64_t experts, f32
 
 constexpr int kTileWaves = 8;
 
+// Where chunk c (8 elements) of a row lies in its 8 places of LDS, so that 16
+// rows' chunks c, one for each lane, are in all banks alike.
+__device__ __forceinline__ int place(int row, int c) { return c ^ (row & 7); }
+
 // 16 tokens x 16 NT experts for each of 8 wavefronts, over the steps [steps z / n,
-// steps (z + 1) / n) of hidden, kDeep - 1 of which are on their way.
+// steps (z + 1) / n) of hidden, kDeep - 1 of which are on their way. Rows are
+// read by 8 lanes each, 128 bytes together, and become operands in LDS: a load
+// whose lanes lie in rows of their own takes the L1 a cycle for each lane.
 template <int T, int W, int NT, int kDeep>
-__global__ __launch_bounds__(64 * kTileWaves, 4) void logits_tile_kernel(const char* __restrict__ x,
+__global__ __launch_bounds__(64 * kTileWaves, T == MOE_EPI_F32 ? 2 : 4) void logits_tile_kernel(const char* __restrict__ x,
                                                                          const char* __restrict__ weight,
                                                                          float* __restrict__ out, int64_t tokens,
                                                                          int64_t hidden, int64_t experts) {
     typedef Pieces<T, W> P;
     typedef Piece8<T> X;
     typedef Piece8<W> Y;
-    constexpr int kFrags = 2 * NT;
-    static_assert(kFrags <= kTileWaves && kDeep % 2 == 0, "");
-    __shared__ u32x4 lds[2][P::kW][kFrags][64];
+    static_assert(2 * NT <= kTileWaves && kDeep % 2 == 0, "");
+    __shared__ u32x4 xs[2][X::kWords][kTileRows][8], ws[2][P::kW][16 * NT][8];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int of16 = lane % 16, k8 = lane / 16 * 8;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kTileRows + 16 * wave + of16, e0 = blockIdx.y * 16 * NT;
+    const int of16 = lane % 16, g = lane / 16, chunk = lane % 8, row = threadIdx.x / 8;  // row: 0 .. 63
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTileRows, e0 = blockIdx.y * 16 * NT;
     const int64_t steps = (hidden + kStep - 1) / kStep;
     const int64_t first = steps * blockIdx.z / gridDim.z, last = steps * (blockIdx.z + 1) / gridDim.z;
-    const int64_t e = e0 + 16 * (wave / 2) + of16;
-    const bool staging = wave < kFrags;
-    const char* px = x + ((t < tokens ? t : tokens - 1) * hidden + k8) * X::kBytes;
-    const char* pw = weight + ((e < experts ? e : experts - 1) * hidden + 32 * (wave % 2) + k8) * Y::kBytes;
+    const bool staging = wave < 2 * NT;  // of the weight, 8 rows a wavefront
+    const int w_row = row % (16 * NT);
+    const char* px[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int64_t t = t0 + row + 64 * j;
+        px[j] = x + ((t < tokens ? t : tokens - 1) * hidden + 8 * chunk) * X::kBytes;
+    }
+    const int64_t e = e0 + w_row;
+    const char* pw = weight + ((e < experts ? e : experts - 1) * hidden + 8 * chunk) * Y::kBytes;
     f32x4 d[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) d[n] = f32x4{0, 0, 0, 0};
@@ -75,59 +86,69 @@ __global__ __launch_bounds__(64 * kTileWaves, 4) void logits_tile_kernel(const c
     };
     auto load = [&](int64_t step, Ahead& a) {
         const int64_t k = step * kStep;
-        if (staging) a.w = Y::load(pw + k * Y::kBytes);
+        a.w = Y::load(pw + k * Y::kBytes);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) a.x[h] = X::load(px + (k + 32 * h) * X::kBytes);
+        for (int j = 0; j < 2; ++j) a.x[j] = X::load(px[j] + k * X::kBytes);
     };
     auto stage = [&](const Ahead& a, int buf) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < X::kWords; ++i) xs[buf][i][row + 64 * j][place(row, chunk)] = a.x[j].w[i];
         if (!staging) return;
         u32x4 piece[P::kW];
         cut_raw<W, P::kW>(a.w, piece);
 #pragma unroll
-        for (int p = 0; p < P::kW; ++p) lds[buf][p][wave][lane] = piece[p];
+        for (int p = 0; p < P::kW; ++p) ws[buf][p][w_row][place(w_row, chunk)] = piece[p];
     };
-    auto multiply = [&](const Ahead& a, int buf) {
+    auto multiply = [&](int buf) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            u32x4 xp[P::kX];
-            cut_raw<T, P::kX>(a.x[h], xp);
+            const int at = place(of16, 4 * h + g);
+            typename X::Raw raw;
+            u32x4 wp[NT][P::kW], xp[P::kX];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                u32x4 wp[P::kW];
+            for (int i = 0; i < X::kWords; ++i) raw.w[i] = xs[buf][i][16 * wave + of16][at];
 #pragma unroll
-                for (int p = 0; p < P::kW; ++p) wp[p] = lds[buf][p][2 * n + h][lane];
-                d[n] = mfma_pieces<P::kF16>(wp, xp, d[n]);
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int p = 0; p < P::kW; ++p) wp[n][p] = ws[buf][p][16 * n + of16][at];
+            cut_raw<T, P::kX>(raw, xp);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) d[n] = mfma_pieces<P::kF16>(wp[n], xp, d[n]);
         }
     };
     const int64_t whole = hidden / kStep < last ? hidden / kStep : last;  // the last step may have fewer than 64
     if (first < whole) {
         Ahead a[kDeep];
+        // Loads past the last step repeat it: a load that stands in a branch makes the compiler wait for the newest
+        // one where an older one is used.
+        auto ahead = [&](int64_t s) { return s < whole ? s : whole - 1; };
 #pragma unroll
-        for (int i = 0; i < kDeep - 1; ++i)
-            if (first + i < whole) load(first + i, a[i]);
+        for (int i = 0; i < kDeep - 1; ++i) load(ahead(first + i), a[i]);
         stage(a[0], 0);
         __syncthreads();
         for (int64_t s = first; s < whole; s += kDeep)
 #pragma unroll
             for (int i = 0; i < kDeep; ++i) {
                 if (s + i >= whole) break;
-                if (s + i + kDeep - 1 < whole) load(s + i + kDeep - 1, a[(i + kDeep - 1) % kDeep]);
-                multiply(a[i], i & 1);
-                if (s + i + 1 < whole) stage(a[(i + 1) % kDeep], (i + 1) & 1);
+                load(ahead(s + i + kDeep - 1), a[(i + kDeep - 1) % kDeep]);
+                multiply(i & 1);
+                stage(a[(i + 1) % kDeep], (i + 1) & 1);
                 __syncthreads();
             }
     }
     if (whole < last) {
         Ahead a;
-        const int64_t k = whole * kStep, left = hidden - k - k8;
-        if (staging) a.w = Y::load_first(pw + k * Y::kBytes, left - 32 * (wave % 2));
+        const int64_t k = whole * kStep, left = hidden - k - 8 * chunk;
+        a.w = Y::load_first(pw + k * Y::kBytes, left);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) a.x[h] = X::load_first(px + (k + 32 * h) * X::kBytes, left - 32 * h);
+        for (int j = 0; j < 2; ++j) a.x[j] = X::load_first(px[j] + k * X::kBytes, left);
         stage(a, 0);
         __syncthreads();
-        multiply(a, 0);
+        multiply(0);
     }
+    const int64_t t = t0 + 16 * wave + of16;
     if (t >= tokens) return;
     float* to = out + (blockIdx.z * tokens + t) * experts;
 #pragma unroll
@@ -502,7 +523,10 @@ __global__ __launch_bounds__(64 * kGradWaves) void grad_weight_kernel(const floa
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int of16 = lane % 16, k8 = lane / 16 * 8;
     const int64_t h = static_cast<int64_t>(blockIdx.x) * 16 * kGradWaves * HT + wave * 16 * HT + of16 * HT;
-    const int64_t e0 = blockIdx.y * 16 * ET, mine = e0 + 16 * wave + of16;
+    // the operands of grad: tile wave % ET, 4 of a lane's 8 tokens in each of two wavefronts
+    const int tile = wave % ET, half = wave / ET % 2;
+    const bool staging = wave < 2 * ET;
+    const int64_t e0 = blockIdx.y * 16 * ET, mine = e0 + 16 * tile + of16;
     const int64_t steps = (tokens + 31) / 32;
     const int64_t first = steps * blockIdx.z / gridDim.z, last = steps * (blockIdx.z + 1) / gridDim.z;
     const int64_t left = hidden - h;
@@ -513,59 +537,60 @@ __global__ __launch_bounds__(64 * kGradWaves) void grad_weight_kernel(const floa
         for (int j = 0; j < HT; ++j) d[e][j] = f32x4{0, 0, 0, 0};
     struct Ahead {
         u32x2 x[8];
-        float g[8];
+        float g[4];
     };
     // Columns past the last hidden element or expert are loaded from what comes after, or from the first ones, and
     // not stored; only the tensors' last token, in the last step, has nothing after it.
     // A load's address is that of a token, which the wavefront shares, and the lane's 32-bit place from there.
     const uint32_t at = static_cast<uint32_t>((k8 * hidden + (left > 0 ? h : 0)) * Elem<T>::kBytes);
-    const uint32_t at_g = static_cast<uint32_t>((k8 * experts + (mine < experts ? mine : experts - 1)) * 4);
+    const uint32_t at_g = static_cast<uint32_t>(((k8 + 4 * half) * experts + (mine < experts ? mine : experts - 1)) * 4);
     auto token_x = [&](int64_t t) { return x + t * hidden * Elem<T>::kBytes; };
     auto token_g = [&](int64_t t) { return reinterpret_cast<const char*>(grad + t * experts); };
     auto load = [&](int64_t s, Ahead& a) {
         typedef u32x2 loose __attribute__((aligned(2)));
 #pragma unroll
         for (int i = 0; i < 8; ++i) a.x[i] = *reinterpret_cast<const loose*>(token_x(s * 32 + i) + at);
-        if (wave < ET) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) a.g[i] = *reinterpret_cast<const float*>(token_g(s * 32 + i) + at_g);
-        }
+        for (int i = 0; i < 4; ++i) a.g[i] = *reinterpret_cast<const float*>(token_g(s * 32 + i) + at_g);
     };
     auto stage = [&](Ahead& a, int buf) {
-        if (wave >= ET) return;
-        u32x4 piece[P::kGrad];
-        cut<P::kGrad>(a.g, piece);
+        if (!staging) return;
+        u32x2 piece[P::kGrad];
+        cut4<P::kGrad>(a.g, piece);
 #pragma unroll
-        for (int p = 0; p < P::kGrad; ++p) lds[buf][wave][p][lane] = piece[p];
+        for (int p = 0; p < P::kGrad; ++p) reinterpret_cast<u32x2*>(&lds[buf][tile][p][lane])[half] = piece[p];
     };
     auto multiply = [&](Ahead& now, int buf) {
-        u32x4 v[HT][P::kOther];
+        u32x4 v[HT][P::kOther], g[ET][P::kGrad];
+#pragma unroll
+        for (int e = 0; e < ET; ++e)
+#pragma unroll
+            for (int p = 0; p < P::kGrad; ++p) g[e][p] = lds[buf][e][p][lane];
+        __builtin_amdgcn_sched_barrier(0);
         turn_short_rows<T, P::kOther>(now.x, v);
 #pragma unroll
-        for (int e = 0; e < ET; ++e) {
-            u32x4 g[P::kGrad];
+        for (int e = 0; e < ET; ++e)
 #pragma unroll
-            for (int p = 0; p < P::kGrad; ++p) g[p] = lds[buf][e][p][lane];
-#pragma unroll
-            for (int j = 0; j < HT; ++j) d[e][j] = mfma_pieces<false, P::kMost>(g, v[j], d[e][j]);
-        }
+            for (int j = 0; j < HT; ++j) d[e][j] = mfma_pieces<false, P::kMost>(g[e], v[j], d[e][j]);
     };
     const int64_t whole = (tokens - 1) / 32 < last ? (tokens - 1) / 32 : last;  // steps before the last token's
     constexpr int kDeep = 4;
     if (first < whole) {
         Ahead a[kDeep];
+        // Loads past the last step repeat it: a load that stands in a branch makes the compiler wait for the newest
+        // one where an older one is used.
+        auto ahead = [&](int64_t s) { return s < whole ? s : whole - 1; };
 #pragma unroll
-        for (int i = 0; i < kDeep - 1; ++i)
-            if (first + i < whole) load(first + i, a[i]);
+        for (int i = 0; i < kDeep - 1; ++i) load(ahead(first + i), a[i]);
         stage(a[0], 0);
         __syncthreads();
         for (int64_t s = first; s < whole; s += kDeep)
 #pragma unroll
             for (int i = 0; i < kDeep; ++i) {
                 if (s + i >= whole) break;
-                if (s + i + kDeep - 1 < whole) load(s + i + kDeep - 1, a[(i + kDeep - 1) % kDeep]);
+                load(ahead(s + i + kDeep - 1), a[(i + kDeep - 1) % kDeep]);
                 multiply(a[i], i & 1);
-                if (s + i + 1 < whole) stage(a[(i + 1) % kDeep], (i + 1) & 1);
+                stage(a[(i + 1) % kDeep], (i + 1) & 1);
                 __syncthreads();
             }
     }
@@ -575,8 +600,10 @@ __global__ __launch_bounds__(64 * kGradWaves) void grad_weight_kernel(const floa
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             a.x[i] = t + i < tokens && left > 0 ? load8<T>(token_x(whole * 32 + i) + at, left) : u32x2{0, 0};
-            a.g[i] = t + i < tokens && wave < ET ? *reinterpret_cast<const float*>(token_g(whole * 32 + i) + at_g) : 0.0f;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            a.g[i] = t + 4 * half + i < tokens ? *reinterpret_cast<const float*>(token_g(whole * 32 + i) + at_g) : 0.0f;
         stage(a, 0);
         __syncthreads();
         multiply(a, 0);
@@ -635,7 +662,7 @@ void launch_logits(const void* x, const void* weight, float* logits, float* work
         else
             go(logits_few_kernel<T, W, 4>);
     } else {
-        constexpr int kDeep = W == MOE_EPI_F32 && T != MOE_EPI_F32 ? 4 : 2;
+        constexpr int kDeep = 4;
         auto go = [&](auto kernel, int nt) {
             // a grid has fewer than 2^32 work-items; calls of so many tokens have one part
             for (int64_t t = 0; t < tokens; t += kMostRows) {

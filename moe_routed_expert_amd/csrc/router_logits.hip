@@ -17,9 +17,8 @@ constexpr int64_t kMostHidden = 1 << 24;  // 32 rows of it have 32-bit offsets
 constexpr int kStep = 64;       // of hidden, in one pass of the loop
 constexpr int kTileRows = 128;  // tokens of a block
 constexpr int64_t kMostRows = 1 << 24;  // tokens of a launch
-constexpr int kFewRows = 512;
 constexpr int kFewWaves = 8;
-constexpr int64_t kFewHidden = 3000;
+constexpr int64_t kFewHidden = 8192;
 
 // Pieces that x and the weight are cut into.
 template <int T, int W>
@@ -155,9 +154,10 @@ __global__ __launch_bounds__(64 * kTileWaves, T == MOE_EPI_F32 ? 2 : 4) void log
     for (int n = 0; n < NT; ++n) put4(to, e0 + 16 * n + lane / 16 * 4, experts, d[n]);
 }
 
-// Up to 16 MT tokens x 16 experts: 8 wavefronts share the steps of hidden that
-// the block has, and their sums are added in their order.
-template <int T, int W, int MT>
+// 16 tokens x 16 experts: 8 wavefronts share the steps of hidden that
+// the block has, and their sums are added in their order. Rows are read as above,
+// and become operands in LDS that a wavefront has for itself.
+template <int T, int W>
 __global__ __launch_bounds__(64 * kFewWaves) void logits_few_kernel(const char* __restrict__ x,
                                                                     const char* __restrict__ weight,
                                                                     float* __restrict__ out, int64_t tokens,
@@ -165,64 +165,99 @@ __global__ __launch_bounds__(64 * kFewWaves) void logits_few_kernel(const char* 
     typedef Pieces<T, W> P;
     typedef Piece8<T> X;
     typedef Piece8<W> Y;
-    __shared__ f32x4 part[kFewWaves][MT][64];
+    constexpr int kWords = X::kWords + Y::kWords;  // 2 KB each
+    __shared__ u32x4 rows[kFewWaves][kWords][16][8];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int of16 = lane % 16, k8 = lane / 16 * 8;
-    const int64_t e = blockIdx.x * 16 + of16, row0 = static_cast<int64_t>(blockIdx.y) * 16 * MT;
-    const char* pw = weight + ((e < experts ? e : experts - 1) * hidden + k8) * Y::kBytes;
-    const char* px[MT];
+    const int of16 = lane % 16, g = lane / 16, chunk = lane % 8, row = lane / 8;  // row, and row + 8
+    const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 16;
+    auto(*mine)[16][8] = rows[wave];
+    const char *pw[2], *px[2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int64_t t = row0 + 16 * m + of16;
-        px[m] = x + ((t < tokens ? t : tokens - 1) * hidden + k8) * X::kBytes;
+    for (int j = 0; j < 2; ++j) {
+        const int64_t e = blockIdx.x * 16 + row + 8 * j;
+        pw[j] = weight + ((e < experts ? e : experts - 1) * hidden + 8 * chunk) * Y::kBytes;
+        const int64_t t = row0 + row + 8 * j;
+        px[j] = x + ((t < tokens ? t : tokens - 1) * hidden + 8 * chunk) * X::kBytes;
     }
-    f32x4 d[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) d[m] = f32x4{0, 0, 0, 0};
-    const int64_t steps = (hidden + 31) / 32, full = hidden / 32, all = static_cast<int64_t>(gridDim.z) * kFewWaves;
+    f32x4 d = {0, 0, 0, 0};
+    const int64_t steps = (hidden + kStep - 1) / kStep, all = static_cast<int64_t>(gridDim.z) * kFewWaves;
     const int64_t me = blockIdx.z * kFewWaves + wave;
     const int64_t first = steps * me / all, last = steps * (me + 1) / all;
-    auto multiply = [&](const typename Y::Raw& w, const typename X::Raw (&v)[MT]) {
-        u32x4 wp[P::kW];
-        cut_raw<W, P::kW>(w, wp);
+    const int64_t whole = hidden / kStep < last ? hidden / kStep : last;  // the last step may have fewer than 64
+    struct Ahead {
+        typename Y::Raw w[2];
+        typename X::Raw x[2];
+    };
+    auto load = [&](int64_t step, Ahead& a) {
+        const int64_t k = step * kStep;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            u32x4 xp[P::kX];
-            cut_raw<T, P::kX>(v[m], xp);
-            d[m] = mfma_pieces<P::kF16>(wp, xp, d[m]);
+        for (int j = 0; j < 2; ++j) {
+            a.w[j] = Y::load(pw[j] + k * Y::kBytes);
+            a.x[j] = X::load(px[j] + k * X::kBytes);
         }
     };
-    int64_t s = first;
-    constexpr int kAhead = 4;
-    for (; s + kAhead <= (last < full ? last : full); s += kAhead) {
-        typename Y::Raw w[kAhead];
-        typename X::Raw v[kAhead][MT];
+    auto multiply = [&](const Ahead& a) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            w[i] = Y::load(pw + (s + i) * 32 * Y::kBytes);
+        for (int j = 0; j < 2; ++j) {
+            const int r = row + 8 * j, at = place(r, chunk);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) v[i][m] = X::load(px[m] + (s + i) * 32 * X::kBytes);
+            for (int i = 0; i < Y::kWords; ++i) mine[i][r][at] = a.w[j].w[i];
+#pragma unroll
+            for (int i = 0; i < X::kWords; ++i) mine[Y::kWords + i][r][at] = a.x[j].w[i];
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) multiply(w[i], v[i]);
+        for (int h = 0; h < 2; ++h) {
+            const int at = place(of16, 4 * h + g);
+            typename Y::Raw w;
+            typename X::Raw v;
+            u32x4 wp[P::kW], xp[P::kX];
+#pragma unroll
+            for (int i = 0; i < Y::kWords; ++i) w.w[i] = mine[i][of16][at];
+#pragma unroll
+            for (int i = 0; i < X::kWords; ++i) v.w[i] = mine[Y::kWords + i][of16][at];
+            cut_raw<W, P::kW>(w, wp);
+            cut_raw<T, P::kX>(v, xp);
+            d = mfma_pieces<P::kF16>(wp, xp, d);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+    constexpr int kDeep = 4;
+    if (first < whole) {
+        Ahead a[kDeep];
+        auto ahead = [&](int64_t s) { return s < whole ? s : whole - 1; };
+#pragma unroll
+        for (int i = 0; i < kDeep - 1; ++i) load(ahead(first + i), a[i]);
+        for (int64_t s = first; s < whole; s += kDeep)
+#pragma unroll
+            for (int i = 0; i < kDeep; ++i) {
+                if (s + i >= whole) break;
+                load(ahead(s + i + kDeep - 1), a[(i + kDeep - 1) % kDeep]);
+                multiply(a[i]);
+            }
     }
-    for (; s < last; ++s) {
-        const int64_t left = hidden - s * 32 - k8;
-        typename X::Raw v[MT];
+    if (whole < last) {
+        Ahead a;
+        const int64_t k = whole * kStep, left = hidden - k - 8 * chunk;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) v[m] = X::load_first(px[m] + s * 32 * X::kBytes, left);
-        multiply(Y::load_first(pw + s * 32 * Y::kBytes, left), v);
+        for (int j = 0; j < 2; ++j) {
+            a.w[j] = Y::load_first(pw[j] + k * Y::kBytes, left);
+            a.x[j] = X::load_first(px[j] + k * X::kBytes, left);
+        }
+        multiply(a);
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) part[wave][m][lane] = d[m];
+    // the wavefronts' sums take the place of their rows
+    f32x4* part = reinterpret_cast<f32x4*>(&rows[0][0][0][0]);
     __syncthreads();
-    if (wave >= MT) return;
-    f32x4 sum = part[0][wave][lane];
+    part[wave * 64 + lane] = d;
+    __syncthreads();
+    if (wave > 0) return;
 #pragma unroll
-    for (int i = 1; i < kFewWaves; ++i) sum += part[i][wave][lane];
-    const int64_t t = row0 + 16 * wave + of16;
-    if (t < tokens)
-        put4(out + (blockIdx.z * tokens + t) * experts, blockIdx.x * 16 + lane / 16 * 4, experts, sum);
+    for (int i = 1; i < kFewWaves; ++i) d += part[i * 64 + lane];
+    const int64_t t = row0 + of16;
+    if (t < tokens) put4(out + (blockIdx.z * tokens + t) * experts, blockIdx.x * 16 + lane / 16 * 4, experts, d);
 }
 
 // out[i] = the sum of parts[s][i], in their order
@@ -237,15 +272,15 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(const float* __restri
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Parts that hidden is shared by. Few tokens: a launch that adds up the parts
-// costs about as much as 3000 of hidden for 16 tokens. Many: two blocks per CU.
+// Few tokens: as many blocks of 16 tokens x 16 experts as the chip has CUs. 1024 x 7168 x 64 11.6 us so, 12.6 by
+// tiles of 128 tokens; 2048 19.7 and 14.9; 1024 x 2048 x 256, four blocks a CU, 11.7 and 10.9.
+bool few(int64_t tokens, int64_t experts) { return up(experts, 16) * up(tokens, 16) <= 256; }
+
+// Parts that hidden is shared by. A launch that adds them up is not worth it up to 8192 of hidden for few tokens (32
+// x 7168 x 64 7.5 us, in two parts 9.0); tiles have two blocks per CU and at least 8 steps each.
 int64_t logits_parts(int64_t tokens, int64_t hidden, int64_t experts) {
     if (tokens == 0) return 1;
-    if (tokens <= kFewRows) {
-        const int64_t n = up(hidden * (tokens <= 16 ? 1 : (tokens <= 32 ? 2 : 4)), kFewHidden);
-        const int64_t most = up(256, up(experts, 16) * up(tokens, 64));
-        return n < most ? n : most;
-    }
+    if (few(tokens, experts)) return up(hidden, kFewHidden) < 16 ? up(hidden, kFewHidden) : 16;
     const int64_t blocks = up(tokens, kTileRows) * up(experts, 64), wanted = 512 / blocks, most = up(hidden, 8 * kStep);
     const int64_t n = wanted < most ? wanted : most;
     return n < 1 ? 1 : (n > 16 ? 16 : n);
@@ -651,16 +686,10 @@ void launch_logits(const void* x, const void* weight, float* logits, float* work
     const int64_t n = logits_parts(tokens, hidden, experts);
     float* to = n > 1 ? workspace : logits;
     const char *px = static_cast<const char*>(x), *pw = static_cast<const char*>(weight);
-    if (tokens <= kFewRows) {
-        const dim3 grid(static_cast<unsigned>(up(experts, 16)), static_cast<unsigned>(up(tokens, 64)), static_cast<unsigned>(n)),
+    if (few(tokens, experts)) {
+        const dim3 grid(static_cast<unsigned>(up(experts, 16)), static_cast<unsigned>(up(tokens, 16)), static_cast<unsigned>(n)),
             block(64 * kFewWaves);
-        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, px, pw, to, tokens, hidden, experts); };
-        if (tokens <= 16)
-            go(logits_few_kernel<T, W, 1>);
-        else if (tokens <= 32)
-            go(logits_few_kernel<T, W, 2>);
-        else
-            go(logits_few_kernel<T, W, 4>);
+        hipLaunchKernelGGL((logits_few_kernel<T, W>), grid, block, 0, st, px, pw, to, tokens, hidden, experts);
     } else {
         constexpr int kDeep = 4;
         auto go = [&](auto kernel, int nt) {

@@ -350,14 +350,15 @@ __global__ __launch_bounds__(kBlock) void grad_x_kernel(const float* __restrict_
     typedef GradPieces<W, T> P;
     typedef Piece8<MOE_EPI_F32> G;
     constexpr int V = 16 / Elem<W>::kBytes;  // weights of a 16-byte load
-    __shared__ u32x4 lds[HT * KS * P::kOther][64];
+    constexpr int kTileBytes = 16 * Elem<T>::kBytes;  // of 16 hidden elements of a token
+    __shared__ u32x4 lds[HT * KS * P::kOther][64], results[kBlock / 64][MT][16][8];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int of16 = lane % 16, k8 = lane / 16 * 8;
     const int64_t h0 = static_cast<int64_t>(blockIdx.x) * 16 * HT;
     // Operand row m of tile j is the hidden element that makes a lane's results
     // neighbours in memory: with 16-bit results two tiles give 8 of them.
-    constexpr bool kPairs = T != MOE_EPI_F32 && HT % 2 == 0;
-    auto place = [&](int h, int& tile, int& m) {  // of hidden element h0 + h
+    constexpr bool kPairs = T != MOE_EPI_F32;
+    auto tile_of = [&](int h, int& tile, int& m) {  // of hidden element h0 + h
         if constexpr (kPairs) {
             const int in32 = h % 32;
             tile = h / 32 * 2 + in32 % 8 / 4;
@@ -378,7 +379,7 @@ __global__ __launch_bounds__(kBlock) void grad_x_kernel(const float* __restrict_
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             int tile, m;
-            place(hv + j, tile, m);
+            tile_of(hv + j, tile, m);
 #pragma unroll
             for (int p = 0; p < P::kOther; ++p)
                 lds[(tile * KS + e8 / 32) * P::kOther + p][m + 16 * (e8 % 32 / 8)] = piece[j][p];
@@ -400,8 +401,11 @@ __global__ __launch_bounds__(kBlock) void grad_x_kernel(const float* __restrict_
                 cut_raw<MOE_EPI_F32, P::kGrad>(raw, g[m][k]);
             }
         }
-        constexpr int kAtOnce = kPairs ? 2 : 1;
-#pragma unroll 2
+        // kAtOnce tiles of results, 128 bytes of each token or what the block has of them, go through LDS, from which
+        // 8 lanes store a token's: stores whose lanes lie in rows of their own take a cycle for each lane.
+        constexpr int kAtOnce = HT < 128 / kTileBytes ? HT : 128 / kTileBytes, kChunks = kAtOnce * kTileBytes / 16;
+        constexpr int kEach = 16 / Elem<T>::kBytes;  // elements of a chunk
+#pragma unroll 1
         for (int j = 0; j < HT; j += kAtOnce) {
             f32x4 d[kAtOnce][MT];
 #pragma unroll
@@ -417,38 +421,49 @@ __global__ __launch_bounds__(kBlock) void grad_x_kernel(const float* __restrict_
                     for (int m = 0; m < MT; ++m) d[a][m] = mfma_pieces<false, P::kMost>(w, g[m][k], d[a][m]);
                 }
             }
-            const int64_t h = h0 + 16 * j + (kPairs ? 8 : 4) * (lane / 16);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                const int64_t t = t0 + 16 * m + of16;
-                if (t >= end) continue;
-                char* to = grad_x + (t * hidden + h) * Elem<T>::kBytes;
+                u32x4(*turn)[8] = results[wave][m];
                 if constexpr (kPairs) {
-                    typedef u32x4 loose __attribute__((aligned(2)));
-                    const float f[8] = {d[0][m][0], d[0][m][1], d[0][m][2], d[0][m][3],
-                                        d[1][m][0], d[1][m][1], d[1][m][2], d[1][m][3]};
-                    if (h + 8 <= hidden) {
-                        *reinterpret_cast<loose*>(to) = Elem<T>::pack(f);
-                    } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (h + i < hidden) Elem<T>::store1(to, i, f[i]);
-                    }
-                } else if constexpr (T == MOE_EPI_F32) {
-                    typedef f32x4 loose __attribute__((aligned(4)));
-                    if (h + 4 <= hidden) {
-                        *reinterpret_cast<loose*>(to) = d[0][m];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (h + i < hidden) Elem<T>::store1(to, i, d[0][m][i]);
+                    for (int a = 0; a < kAtOnce; a += 2) {
+                        const float f[8] = {d[a][m][0], d[a][m][1], d[a][m][2], d[a][m][3],
+                                            d[a + 1][m][0], d[a + 1][m][1], d[a + 1][m][2], d[a + 1][m][3]};
+                        turn[of16][place(of16, 2 * a + lane / 16)] = Elem<T>::pack(f);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (h + i < hidden) Elem<T>::store1(to, i, d[0][m][i]);
+                    for (int a = 0; a < kAtOnce; ++a)
+                        turn[of16][place(of16, 4 * a + lane / 16)] = __builtin_bit_cast(u32x4, d[a][m]);
                 }
             }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 16 * kChunks / 64; ++i) {
+                    typedef u32x4 loose __attribute__((aligned(2)));
+                    const int at = lane + 64 * i, row = at / kChunks, c = at % kChunks;
+                    const u32x4 v = results[wave][m][row][place(row, c)];
+                    const int64_t t = t0 + 16 * m + row, h = h0 + 16 * j + kEach * c;
+                    if (t >= end || h >= hidden) continue;
+                    char* to = grad_x + (t * hidden + h) * Elem<T>::kBytes;
+                    if (h + kEach <= hidden) {
+                        __builtin_nontemporal_store(v, reinterpret_cast<loose*>(to));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kEach; ++e) {
+                            if (h + e >= hidden) continue;
+                            if constexpr (T == MOE_EPI_F32)
+                                reinterpret_cast<uint32_t*>(to)[e] = v[e];
+                            else
+                                reinterpret_cast<uint16_t*>(to)[e] = static_cast<uint16_t>(v[e / 2] >> (16 * (e % 2)));
+                        }
+                    }
+                }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
         }
     }
 }
@@ -547,8 +562,10 @@ constexpr int kGradWaves = 8;
 // 16 ET experts x 16 HT hidden for each of 8 wavefronts, over the tokens of part
 // z: the tokens are the inner dimension. A wavefront reads 8 tokens' elements of
 // its hidden, 8 bytes a lane and token, and turns them into operands in
-// registers; the operands of grad are made once a block.
-template <int T, int W, int ET>
+// registers; the operands of grad are made once a block. kOnce: no other block
+// reads the same elements, which then need not stay in the caches (65536 x 7168
+// x 64 251 -> 211 us; 16384 x 2048 x 256, read by four blocks, 54 -> 59).
+template <int T, int W, int ET, bool kOnce>
 __global__ __launch_bounds__(64 * kGradWaves) void grad_weight_kernel(const float* __restrict__ grad, const char* __restrict__ x,
                                                              float* __restrict__ parts, int64_t tokens, int64_t hidden,
                                                              int64_t experts) {
@@ -584,7 +601,13 @@ __global__ __launch_bounds__(64 * kGradWaves) void grad_weight_kernel(const floa
     auto load = [&](int64_t s, Ahead& a) {
         typedef u32x2 loose __attribute__((aligned(2)));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a.x[i] = *reinterpret_cast<const loose*>(token_x(s * 32 + i) + at);
+        for (int i = 0; i < 8; ++i) {
+            const loose* p = reinterpret_cast<const loose*>(token_x(s * 32 + i) + at);
+            if constexpr (kOnce)
+                a.x[i] = __builtin_nontemporal_load(p);
+            else
+                a.x[i] = *p;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) a.g[i] = *reinterpret_cast<const float*>(token_g(s * 32 + i) + at_g);
     };
@@ -720,7 +743,7 @@ template <int T, int W>
 void launch_grad_x(const float* grad, const void* weight, void* grad_x, int64_t tokens, int64_t hidden, int64_t experts,
                    hipStream_t st) {
     auto go = [&](auto kernel, int width, int wave_tokens) {
-        const int64_t columns = up(hidden, width), wanted = up(1024, columns);
+        const int64_t columns = up(hidden, width), wanted = columns < 512 ? 512 / columns : 1;  // two blocks per CU
         int64_t each = up(up(tokens, wanted), 4 * wave_tokens) * 4 * wave_tokens;
         if (up(tokens, each) > 65535) each = up(up(tokens, 65535), 4 * wave_tokens) * 4 * wave_tokens;
         const dim3 grid(static_cast<unsigned>(columns), static_cast<unsigned>(up(tokens, each)));
@@ -757,11 +780,13 @@ void launch_grad_weight(const float* grad, const void* x, void* grad_weight, flo
                            hidden, experts);
     };
     if (experts <= 16)
-        go(grad_weight_kernel<T, W, 1>, 1);
+        go(grad_weight_kernel<T, W, 1, true>, 1);
     else if (experts <= 32)
-        go(grad_weight_kernel<T, W, 2>, 2);
+        go(grad_weight_kernel<T, W, 2, true>, 2);
+    else if (experts <= 64)
+        go(grad_weight_kernel<T, W, 4, true>, 4);
     else
-        go(grad_weight_kernel<T, W, 4>, 4);
+        go(grad_weight_kernel<T, W, 4, false>, 4);
     const int64_t all = experts * hidden, blocks = up(all, kBlock);
     hipLaunchKernelGGL(add_weight_parts_kernel<W>, dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)),
                        dim3(kBlock), 0, st, workspace, grad_weight, static_cast<int>(n), all);

@@ -10,6 +10,8 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -31,18 +33,32 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
 
 
-def build(verbose: bool = False, extra_flags=(), out: str = LIB) -> str:
-    cmd = [HIPCC, *FLAGS, *extra_flags, f"-I{INCLUDE}", f"-I{CSRC}", *sources(), "-o", out + ".tmp"]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
+def _messages(text: str):
     # hipcc's host pass does not know the packed-fp32 feature and says so: harmless.
     noise = "'-packed-fp32-ops' is not a recognized feature"
-    msgs = [l for l in (res.stdout + res.stderr).splitlines() if noise not in l and l.strip()]
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
-    if verbose and msgs:
-        print("\n".join(msgs))
+    return [l for l in text.splitlines() if noise not in l and l.strip()]
+
+
+def build(verbose: bool = False, extra_flags=(), out: str = LIB) -> str:
+    """Compile every source, several at a time, and link the library."""
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        msgs = _messages(res.stdout + res.stderr)
+        if res.returncode != 0:
+            raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
+        if verbose and msgs:
+            print("\n".join(msgs))
+
+    flags = [f for f in FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as folder:
+        objects = [os.path.join(folder, os.path.basename(s) + ".o") for s in sources()]
+        commands = [[HIPCC, *flags, *extra_flags, f"-I{INCLUDE}", f"-I{CSRC}", "-c", s, "-o", o]
+                    for s, o in zip(sources(), objects)]
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(run, commands))
+        run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *extra_flags, *objects, "-o", out + ".tmp"])
     os.replace(out + ".tmp", out)
     return out
 

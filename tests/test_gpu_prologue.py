@@ -620,3 +620,68 @@ def test_calls_on_another_stream_and_two_at_once():
     torch.cuda.synchronize()
     for a, b in found:
         assert torch.equal(a, want) and torch.equal(b, gw)
+
+
+# ---- large calls ------------------------------------------------------------------------------------
+
+def test_calls_past_2_32_bytes_and_of_several_launches():
+    """The last rows of tensors beyond 2^32 bytes, and calls of more rows than one launch has: the same as those rows in
+    a call of their own."""
+    rows, cols = 330_000, 7168
+    x = torch.empty((rows, cols), dtype=BF16, device="cuda")
+    x.view(torch.int16).fill_(0x3F80)                      # ones
+    tail = slice(rows - 300, rows)
+    x[tail] = torch.randn(300, cols, device="cuda").to(BF16)
+    w = torch.randn(cols, device="cuda").to(BF16)
+    out = torch.empty_like(x)
+    epi.rms_norm_fwd(x, w, out, 1e-6)
+    part = torch.empty((300, cols), dtype=BF16, device="cuda")
+    epi.rms_norm_fwd(x[tail], w, part, 1e-6)
+    assert torch.equal(out[tail], part)
+    router = torch.randn(8, cols, device="cuda").to(BF16)
+    logits = torch.empty((rows, 8), device="cuda")
+    epi.moe_router_logits_fwd(x, router, logits, space(epi.moe_router_logits_workspace_bytes(rows, cols, 8)))
+    check(logits[tail], *ref.product(ref.f64(x[tail]), ref.f64(router).T), F32, "logits")
+    g = torch.randn(rows, 8, device="cuda")
+    epi.moe_router_logits_bwd(g, x, router, out, None)
+    check(out[tail], *ref.product(ref.f64(g[tail]), ref.f64(router), 2), BF16, "grad_x")
+    # the tail alone counts: all other gradients are 0
+    g[:rows - 300] = 0
+    gw = torch.empty_like(router)
+    epi.moe_router_logits_bwd(g, x, router, None, gw, space(epi.moe_router_logits_bwd_workspace_bytes(rows, cols, 8)))
+    check(gw, *ref.product(ref.f64(g[tail]).T, ref.f64(x[tail]), 2), BF16, "grad_weight")
+    del x, out, logits, g
+
+    rows = (1 << 20) + 77
+    x, w = torch.randn(rows, 24, device="cuda"), torch.randn(24, device="cuda")
+    out, q, scale = torch.empty_like(x), torch.empty(x.shape, dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    epi.rms_norm_fwd(x, w, out, 1e-6, q=q, scale=scale)
+    few = torch.empty((100, 24), device="cuda")
+    epi.rms_norm_fwd(x[-100:], w, few, 1e-6)
+    assert torch.equal(out[-100:], few)
+    logits = torch.randn(rows, 4, device="cuda")
+    ids, weights = epi.moe_route(logits, 2, score="sigmoid", bias=torch.zeros(4, device="cuda"))
+    ids2, weights2 = epi.moe_route(logits[-100:], 2, score="sigmoid", bias=torch.zeros(4, device="cuda"))
+    assert torch.equal(ids[-100:], ids2) and torch.equal(weights[-100:], weights2)
+    gw, gl, gl2 = torch.randn(rows, 2, device="cuda"), torch.empty_like(logits), torch.empty(100, 4, device="cuda")
+    epi.moe_route_bwd(gw, logits, ids, gl)
+    epi.moe_route_bwd(gw[-100:], logits[-100:], ids[-100:], gl2)
+    assert torch.equal(gl[-100:], gl2)
+    rows = (1 << 24) + 40
+    x, w = torch.randn(rows, 2, device="cuda").to(BF16), torch.randn(3, 2, device="cuda").to(BF16)
+    logits = epi.moe_router_logits(x, w)
+    for part in (slice(0, 50), slice((1 << 24) - 20, rows)):
+        check(logits[part], *ref.product(ref.f64(x[part]), ref.f64(w).T), F32, "logits")
+
+
+@pytest.mark.parametrize("dtype,weight", PAIRS)
+def test_router_products_of_small_values(dtype, weight):
+    """Factors whose pieces or products leave the normal range of their type: a value that a matrix instruction takes
+    for 0 is below 2^-126 in bfloat16 and float32 and 2^-14 in float16, so the sums are right to hidden times that of
+    the other factor."""
+    rng = np.random.default_rng(30)
+    sigma = 2.0 ** -16 if dtype == F16 else 2.0 ** -110
+    x, w = normal(rng, (40, 64), dtype, sigma), normal(rng, (16, 64), weight)
+    want, slack = ref.product(ref.f64(x), ref.f64(w).T)
+    least = 2.0 ** -14 if dtype == F16 and weight == F16 else 2.0 ** -126
+    check(epi.moe_router_logits(x, w), want, slack + least * np.abs(ref.f64(w)).sum(1)[None], F32, "logits")

@@ -1,4 +1,20 @@
 // Choice of each token's experts, the chosen experts' weights, and their gradient (gfx950).
+//
+// A token takes 16 lanes (32 and 64 above 256 and 512 experts) with up to 16
+// experts in a row each. A lane sorts its own, and lists are joined lane by
+// lane, which keeps the 8 largest of two sorted lists by comparing one with the
+// other reversed; more than 8 are taken one after the other from sorted lanes.
+// Sorting moves float64 keys that hold the expert's number below the value.
+//
+// Bound by vector instructions: 65536 tokens, 8 of 256 experts by logits 23 us
+// (10 at a copy's rate), in groups by biased sigmoids 48 us; 131072 tokens, 8
+// of 64 24 us. A kernel takes each token once, without a loop around it: with
+// one the compiler keeps the constants of exponentials and divisions in
+// registers, 204 instead of 84 for 256 experts, and the times are 31, 75 and 28.
+//
+// The gradient is bound by memory where every score counts (131072 x 64 19.6
+// us, 3.9 TB/s): a token's slots go through LDS, and each lane adds up those of
+// its experts, in their order.
 #include <type_traits>
 
 #include "epi_common.h"

@@ -1,4 +1,22 @@
 // Root-mean-square norm with the residual's addition, and its gradients (gfx950).
+//
+//   h = round(x + residual),  n = 1 / sqrt(mean(h^2) + eps),  y = h n weight
+//   grad_x = n (g - a mean(g a)) + grad_residual,  grad_weight = sum_r grad_out a
+//   with a = h n, g = grad_out weight
+//
+// Bound by memory: a row is read once and kept in registers, as it is stored,
+// between its sum and its results; 65536 x 7168 bf16 with the residual 637 us
+// (5.9 TB/s), 16384 x 7168 with rows also in 8 bits 174 us (6.1 TB/s).
+//
+// Lanes of a row are chosen as in quantize_rows.hip, which has both sides of
+// each: the fewest that hold it with four vectors each, and up to 512 rows more
+// lanes with one or two. The order of a row's sum is that of its vectors and
+// not of its lanes, so the choice does not show in the results.
+//
+// Gradients: a lane also keeps the sums of its columns of the weight's gradient
+// over the rows of its block, of which there are up to four per CU; the blocks'
+// sums are added by a second launch. 32768 x 7168 bf16 367 + 9 us (5.2 TB/s);
+// with four vectors a lane instead of two the registers held one block a CU.
 #include <type_traits>
 
 #include "bf16_pieces.h"

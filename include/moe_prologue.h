@@ -74,7 +74,9 @@ int64_t rms_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
  * The router's product: logits[t, e] = sum_h x[t, h] * weight[e, h], products
  * of all bits of both, float32 sums. x and weight of one 16-bit type follow
  * IEEE arithmetic; where one of them is float32, a row of x or of weight that
- * holds an infinity or a NaN gives NaN or an infinity.
+ * holds an infinity or a NaN gives NaN or an infinity. The order of a sum depends
+ * on the sizes of the call, so a token's logits may differ in their last bits in
+ * calls of other sizes.
  *   x         [tokens, hidden] of dtype                       in
  *   weight    [experts, hidden] of w_dtype (dtype or float32) in
  *   logits    [tokens, experts] float32                       out

@@ -4,7 +4,9 @@
 // experts in a row each. A lane sorts its own, and lists are joined lane by
 // lane, which keeps the 8 largest of two sorted lists by comparing one with the
 // other reversed; more than 8 are taken one after the other from sorted lanes.
-// Sorting moves float64 keys that hold the expert's number below the value.
+// Keys hold the expert's number below the value: float64 for logits, whose order
+// is exact, 32 bits for scores, of which those too near to tell are chosen again
+// in float64.
 //
 // Bound by vector instructions: 65536 tokens, 8 of 256 experts by logits 23 us
 // (10 at a copy's rate), in groups by biased sigmoids 48 us; 131072 tokens, 8
@@ -62,6 +64,10 @@ __device__ __forceinline__ float partner(float v) {
     return __int_as_float(partner<kXor>(__float_as_int(v)));
 }
 template <int kXor>
+__device__ __forceinline__ uint32_t partner(uint32_t v) {
+    return static_cast<uint32_t>(partner<kXor>(static_cast<int>(v)));
+}
+template <int kXor>
 __device__ __forceinline__ double partner(double v) {
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
     const uint32_t lo = static_cast<uint32_t>(partner<kXor>(static_cast<int>(u)));
@@ -96,6 +102,10 @@ __device__ __forceinline__ bool lanes_any(bool v) {
 // A key is a float32 value as a float64, whose last 10 bits (of the 29 that the
 // value leaves free) are the expert's number, turned so that of equal values the
 // lowest expert has the largest key. -inf: not to be chosen.
+//
+// Scores are of a narrow range and known to a few float32 steps: their keys are
+// 32 bits, the place between the token's least and largest in the upper 22 and
+// the expert's number below. 0: not to be chosen.
 
 constexpr uint64_t kNumber = kMostExperts - 1;
 
@@ -124,9 +134,11 @@ __device__ __forceinline__ double smaller(double a, double b) {
     asm("v_min_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
     return d;
 }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t smaller(uint32_t a, uint32_t b) { return a < b ? a : b; }
 // Descending, by Batcher's odd-even merge.
-template <int N>
-__device__ __forceinline__ void sort_keys(double (&key)[N]) {
+template <int N, class V>
+__device__ __forceinline__ void sort_keys(V (&key)[N]) {
 #pragma unroll
     for (int p = 1; p < N; p *= 2)
 #pragma unroll
@@ -136,28 +148,28 @@ __device__ __forceinline__ void sort_keys(double (&key)[N]) {
 #pragma unroll
                 for (int i = 0; i < k; ++i)
                     if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
-                        const double a = key[i + j], b = key[i + j + k];
+                        const V a = key[i + j], b = key[i + j + k];
                         key[i + j] = larger(a, b);
                         key[i + j + k] = smaller(a, b);
                     }
 }
 
 // A sequence that rises and falls, descending.
-template <int N, int M>
-__device__ __forceinline__ void settle(double (&key)[M]) {
+template <int N, int M, class V>
+__device__ __forceinline__ void settle(V (&key)[M]) {
 #pragma unroll
     for (int d = N / 2; d >= 1; d /= 2)
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (!(i & d)) {
-                const double a = key[i], b = key[i + d];
+                const V a = key[i], b = key[i + d];
                 key[i] = larger(a, b);
                 key[i + d] = smaller(a, b);
             }
 }
 // The K largest of two descending lists of K, in `a`; `left` grows to the largest that is left out.
-template <int K>
-__device__ __forceinline__ void join(double (&a)[K], const double (&b)[K], double& left) {
+template <int K, class V>
+__device__ __forceinline__ void join(V (&a)[K], const V (&b)[K], V& left) {
 #pragma unroll
     for (int i = 0; i < K; ++i) {
         left = larger(left, smaller(a[i], b[K - 1 - i]));
@@ -166,8 +178,8 @@ __device__ __forceinline__ void join(double (&a)[K], const double (&b)[K], doubl
     settle<K>(a);
 }
 // The K largest keys of L lanes that have n each, descending, in every lane.
-template <int L, int K, int n, int kXor = 1>
-__device__ __forceinline__ void join_lanes(double (&key)[K], double& left) {
+template <int L, int K, int n, int kXor = 1, class V>
+__device__ __forceinline__ void join_lanes(V (&key)[K], V& left) {
     if constexpr (kXor < L) {
         if constexpr (2 * n <= K) {
 #pragma unroll
@@ -175,7 +187,7 @@ __device__ __forceinline__ void join_lanes(double (&key)[K], double& left) {
             settle<2 * n>(key);
             join_lanes<L, K, 2 * n, 2 * kXor>(key, left);
         } else {
-            double other[K];
+            V other[K];
 #pragma unroll
             for (int i = 0; i < K; ++i) other[i] = partner<kXor>(key[i]);
             join<K>(key, other, left);
@@ -183,6 +195,30 @@ __device__ __forceinline__ void join_lanes(double (&key)[K], double& left) {
             join_lanes<L, K, n, 2 * kXor>(key, left);
         }
     }
+}
+
+// The K largest keys of L lanes that have N each, descending, in every lane.
+template <int L, int K, int N, class V>
+__device__ __forceinline__ void best_keys(const V (&key)[N], V (&list)[K], V& left) {
+    constexpr int n = N < K ? N : K;
+    static_assert(n * L >= K, "");
+#pragma unroll
+    for (int c = 0; c < N; c += n) {
+        V part[n];
+#pragma unroll
+        for (int i = 0; i < n; ++i) part[i] = key[c + i];
+        sort_keys<n>(part);
+        if constexpr (n == K) {
+            if (c > 0) {
+                join<K>(list, part, left);
+                continue;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < n; ++i) list[i] = part[i];
+    }
+    if constexpr (N > K) left = over_lanes<L>(left, [](V a, V c) { return larger(a, c); });
+    join_lanes<L, K, n>(list, left);
 }
 
 // ---- scores ----------------------------------------------------------------------------
@@ -201,15 +237,14 @@ __device__ __forceinline__ float rough_sigmoid(float l) {
 __device__ __forceinline__ float over_most(float l, float most) {
     return expf(fminf(l, 0.0f) - fminf(most, 0.0f)) / (1.0f + expf(-fabsf(l)));
 }
-// What a float32 score may be off. Steps of 2^-24: a sigmoid
-// 0.4 for the exponential's argument (x e^-x), 2 each for the exponential and the
-// reciprocal, and 2 roundings, below 2^-21; a softmax |l - m| of itself (m - l is
-// at most log(experts) on average over the scores, which the sum is off by, and
-// at most 0.4 of the largest score for the score itself), up to 22 additions and
-// 8 for exponentials and quotient: below 2^-18 of the largest score, 1 / sum.
-__device__ __forceinline__ double score_error(bool sigmoid, float sum) {
-    return sigmoid ? 0x1p-21 : 0x1p-18 / static_cast<double>(sum);
-}
+// What a float32 score may be off, in steps of 2^-24. A sigmoid: 0.3 for the
+// exponential's argument and 0.5 for its last place (passed on by e / (1 + e)^2),
+// 1 for the sum, 1 for the reciprocal's last place and 0.25 for the product,
+// below 2^-22. A softmax: |l - m| of itself (m - l is at most log(experts) on
+// average over the scores, which the sum is off by, and at most 0.4 of the
+// largest score for the score itself), up to 22 additions and 8 for exponentials
+// and quotient, below 2^-18 of the largest score, 1 / sum.
+__device__ __forceinline__ float score_error(bool sigmoid, float sum) { return sigmoid ? 0x1p-22f : 0x1p-18f / sum; }
 
 template <int T>
 __device__ __forceinline__ float load_logit(const char* row, int e) {
@@ -274,15 +309,23 @@ __device__ __forceinline__ uint64_t best_groups(const double* value, const Choic
 __device__ const double kOverFactorial[14] = {1.0 / 6227020800.0, 1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0,
                                               1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0, 1.0 / 120.0,
                                               1.0 / 24.0, 1.0 / 6.0, 0.5, 1.0, 1.0};
-__device__ __forceinline__ double exp64(double x) {
-    x = fmin(fmax(x, -800.0), 800.0);  // 0 and infinity from there on
-    const double n = rint(x * 0x1.71547652b82fep+0);
-    double r = fma(-n, 0x1.62e42fefa39efp-1, x);
-    r = fma(-n, 0x1.abc9e3b39803fp-56, r);
-    double sum = kOverFactorial[0];
+template <int N>
+__device__ __forceinline__ void exp64(double (&x)[N]) {
+    double n[N], r[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        x[j] = fmin(fmax(x[j], -800.0), 800.0);  // 0 and infinity from there on
+        n[j] = rint(x[j] * 0x1.71547652b82fep+0);
+        r[j] = fma(-n[j], 0x1.62e42fefa39efp-1, x[j]);
+        r[j] = fma(-n[j], 0x1.abc9e3b39803fp-56, r[j]);
+        x[j] = kOverFactorial[0];
+    }
 #pragma unroll 1
-    for (int i = 1; i < 14; ++i) sum = fma(sum, r, kOverFactorial[i]);
-    return ldexp(sum, static_cast<int>(n));
+    for (int i = 1; i < 14; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = fma(x[j], r[j], kOverFactorial[i]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = ldexp(x[j], static_cast<int>(n[j]));
 }
 
 // Token t by float64 values, by the whole wavefront, an expert that is chosen in each lane. Few tokens come here, so
@@ -295,44 +338,67 @@ __device__ __forceinline__ void route64(const char* logits, const float* bias, i
     float m = -kInf;
     double all = 0.0;
     bool bad = false;
+    // four experts at a time, so that their loads and exponentials go side by side
+    auto each4 = [&](auto f) {
 #pragma unroll 1
-    for (int e = lane; e < p.experts; e += 64) {
-        const float l = load_logit<T>(row, e);
-        bad |= l != l || (!p.sigmoid && l == kInf);
-        m = fmaxf(m, l);
-    }
-    bad = lanes_any<64>(bad);
+        for (int e = lane; e < p.experts; e += 256) {
+            float l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) l[j] = e + 64 * j < p.experts ? load_logit<T>(row, e + 64 * j) : -kInf;
+            f(e, l);
+        }
+    };
     if (!p.sigmoid) {
+        each4([&](int, const float (&l)[4]) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m = fmaxf(m, l[j]);
+        });
         m = lanes_max<64>(m);
-#pragma unroll 1
-        for (int e = lane; e < p.experts; e += 64) all += exp64(static_cast<double>(load_logit<T>(row, e)) - m);
+        each4([&](int, const float (&l)[4]) {
+            double x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = static_cast<double>(l[j]) - m;
+            exp64(x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) all += l[j] > -kInf ? x[j] : 0.0;
+        });
         all = lanes_sum<64>(all);
     }
     // an expert's value, its score where groups count sums of those and there is no bias
     const bool sums = p.top2 && p.groups > 1;
     auto fill = [&](bool by_score) {
-#pragma unroll 1
-        for (int e = lane; e < p.experts; e += 64) {
-            const float l = load_logit<T>(row, e);
-            double v = l;
-            if (by_score) v = p.sigmoid ? 1.0 / (1.0 + exp64(-v)) : exp64(v - m) / all;
-            if (bias) v += static_cast<double>(bias[e]);
-            value[e] = l > -kInf && v > -kInf ? v : -kInf;  // not where either is NaN
-        }
+        each4([&](int e, const float (&l)[4]) {
+            double x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                bad |= l[j] != l[j] || (!p.sigmoid && l[j] == kInf);
+                x[j] = p.sigmoid ? -static_cast<double>(l[j]) : static_cast<double>(l[j]) - m;
+            }
+            exp64(x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (e + 64 * j >= p.experts) continue;
+                double v = l[j];
+                if (by_score) v = p.sigmoid ? 1.0 / (1.0 + x[j]) : x[j] / all;
+                if (bias) v += static_cast<double>(bias[e + 64 * j]);
+                value[e + 64 * j] = l[j] > -kInf && v > -kInf ? v : -kInf;  // not where either is NaN
+            }
+        });
         __threadfence_block();
         __builtin_amdgcn_wave_barrier();
     };
     fill(bias || sums);
+    bad = lanes_any<64>(bad);
     uint64_t kept = ~0ull;
     if (p.groups > 1) {
         if (lane < p.groups) {
             double first = -kInf, second = -kInf;
 
-#pragma unroll 1
+#pragma unroll 4
             for (int i = 0; i < size; ++i) {
                 const double v = value[lane * size + i];
-                second = larger(second, smaller(first, v));
-                first = larger(first, v);
+                second = fmax(second, fmin(first, v));
+                first = fmax(first, v);
             }
             of_group[lane] = sums ? first + second : first;
         }
@@ -430,139 +496,54 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const char* __restrict__ 
     }
 
     int id[S];
-    // The choice by float32 values; returns whether some were too near to tell.
+    // The choice by logits, which is exact.
     auto choose = [&]() {
-        const float over = p.sigmoid ? 0.0f : 1.0f / sum;
-        auto score = [&](float v) { return p.sigmoid ? rough_sigmoid(v) : rough_exp(v - m) * over; };
-        const double off = kScored ? 2.0 * score_error(p.sigmoid, sum) : 0.0;
-        bool near = false;
-        // a >= c; each of `times` scores off, and their sums with the bias rounded
-        auto tell = [&](double a, double c, double times) { near |= a - c <= times * off + fabs(a) * 0x1p-22; };
-        auto group_value = [&](double first, double second) -> double {
-            if (!kScored || !p.top2 || second == -kInf) return kScored && p.top2 ? second : value_of(first);
-            if (biased) return value_of(first) + value_of(second);
-            return static_cast<double>(score(static_cast<float>(value_of(first)))) +
-                   score(static_cast<float>(value_of(second)));
-        };
-        float c[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) c[i] = l[i];
-        if (biased) {
-            if (p.sigmoid) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) c[i] = l[i] > -kInf ? rough_sigmoid(l[i]) + b[i] : -kInf;
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) c[i] = l[i] > -kInf ? rough_exp(l[i] - m) * over + b[i] : -kInf;
-            }
-        }
         double key[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) key[i] = key_of(c[i], e0 + i);
+        for (int i = 0; i < N; ++i) key[i] = key_of(l[i], e0 + i);
+        const auto larger2 = [](double a, double c) { return larger(a, c); };
         if (grouped && !whole) {
             double* value = of_group[threadIdx.x / L];
             for (int g = 0; g < p.groups; ++g) {
-                double first = -kInf, second = -kInf;
+                double first = -kInf;
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const double v = e0 + i >= g * size && e0 + i < (g + 1) * size ? key[i] : -kInf;
-                    second = larger(second, smaller(first, v));
-                    first = larger(first, v);
-                }
-#pragma unroll
-                for (int x = 1; x < L; x *= 2) {
-                    const double a = __shfl_xor(first, x, 64), c = __shfl_xor(second, x, 64);
-                    second = larger(smaller(first, a), larger(second, c));
-                    first = larger(first, a);
-                }
-                const double v = group_value(first, second);
-                if (lane == 0) value[g] = v;
+                for (int i = 0; i < N; ++i)
+                    if (e0 + i >= g * size && e0 + i < (g + 1) * size) first = larger(first, key[i]);
+                first = over_lanes<L>(first, larger2);
+                if (lane == 0) value[g] = value_of(first);
             }
             const uint64_t kept = best_groups<L>(value, p, lane);
-            if (kScored) {
-                double in = kInf, out = -kInf;  // the least of the groups that stay, the largest of the others
-                for (int g = 0; g < p.groups; ++g) {
-                    const bool stays = kept >> g & 1;
-                    in = smaller(in, stays ? value[g] : static_cast<double>(kInf));
-                    out = larger(out, stays ? static_cast<double>(-kInf) : value[g]);
-                }
-                tell(in, out, 2.0);
-            }
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 if (!(kept >> ((e0 + i) / size & 63) & 1)) key[i] = -kInf;
         }
         if (whole) {
-            double first = -kInf, second = -kInf;
+            double first = -kInf;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                second = larger(second, smaller(first, key[i]));
-                first = larger(first, key[i]);
-            }
-            for (int x = 1; x < wide; x *= 2) {
-                const double a = __shfl_xor(first, x, 64), c = __shfl_xor(second, x, 64);
-                second = larger(smaller(first, a), larger(second, c));
-                first = larger(first, a);
-            }
-            const double v = group_value(first, second);
+            for (int i = 0; i < N; ++i) first = larger(first, key[i]);
+            for (int x = 1; x < wide; x *= 2) first = larger(first, __shfl_xor(first, x, 64));
+            const double v = value_of(first);
             const int group = lane / wide;
             int before = 0;
             for (int g = 0; g < p.groups; ++g) {
                 const double w = __shfl(v, g * wide, L);
                 before += w > v || (w == v && g < group);
             }
-            const bool stays = before < p.top_groups && group < p.groups;
-            if (kScored) {
-                const double in = over_lanes<L>(stays ? v : static_cast<double>(kInf),
-                                                [](double a, double c) { return smaller(a, c); });
-                const double out = over_lanes<L>(stays || group >= p.groups ? static_cast<double>(-kInf) : v,
-                                                 [](double a, double c) { return larger(a, c); });
-                tell(in, out, 2.0);
-            }
-            if (!stays)
+            if (before >= p.top_groups || group >= p.groups)
 #pragma unroll
                 for (int i = 0; i < N; ++i) key[i] = -kInf;
         }
         if constexpr (K > 0) {
-            constexpr int n = N < K ? N : K;
-            double list[K], left = -kInf;
+            double list[K], left = -kInf, mine = -kInf;
+            best_keys<L, K>(key, list, left);
 #pragma unroll
-            for (int c = 0; c < N; c += n) {
-                double part[n];
-#pragma unroll
-                for (int i = 0; i < n; ++i) part[i] = key[c + i];
-                sort_keys<n>(part);
-                if constexpr (n == K) {
-                    if (c > 0) {
-                        join<K>(list, part, left);
-                        continue;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < n; ++i) list[i] = part[i];
-            }
-            left = over_lanes<L>(left, [](double a, double c) { return larger(a, c); });
-            join_lanes<L, K, n>(list, left);
-            constexpr int kHave = n * L < K ? n * L : K;  // keys in the list
-            double mine = -kInf, next = kHave == K ? left : static_cast<double>(-kInf);
-#pragma unroll
-            for (int j = 0; j < kHave; ++j) {
+            for (int j = 0; j < K; ++j)
                 if (lane == j) mine = list[j];
-                if (lane + 1 == j) next = list[j];
-            }
-            if (biased) {
-                if (lane < p.top_k) tell(mine, next, 1.0);
-                near = lanes_any<L>(near);
-            }
             id[0] = lane < p.top_k ? expert_of(mine) : -1;
         } else {
             sort_keys<N>(key);
-            double last = 0x1p1020;
-            const int rounds = p.top_k + (biased ? 1 : 0);  // with a bias also the best that is left
-            for (int r = 0; r < rounds; ++r) {
-                const double best = over_lanes<L>(key[0], [](double a, double c) { return larger(a, c); });
-                if (biased) tell(last, best, 1.0);
-                last = best;
+            for (int r = 0; r < p.top_k; ++r) {
+                const double best = over_lanes<L>(key[0], larger2);
                 const bool pop = key[0] == best;
 #pragma unroll
                 for (int i = 0; i + 1 < N; ++i) key[i] = pop ? key[i + 1] : key[i];
@@ -570,14 +551,153 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const char* __restrict__ 
                 const int e = expert_of(best);
 #pragma unroll
                 for (int s = 0; s < S; ++s)
+                    if (r == lane + s * L) id[s] = e;
+            }
+        }
+    };
+    // The choice by float32 scores; returns whether some were too near to tell.
+    auto choose_scored = [&]() {
+        const float over = p.sigmoid ? 0.0f : 1.0f / sum;
+        const float score_off = score_error(p.sigmoid, sum), off = biased ? score_off : 0.0f;
+        bool near = false;
+        float c[N], low = kInf, high = -kInf;
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = l[i] > -kInf ? l[i] : -kInf;  // for NaN too
+        if (biased) {
+            if (p.sigmoid) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) c[i] = rough_sigmoid(l[i]) + b[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) c[i] = rough_exp(l[i] - m) * over + b[i];
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) c[i] = l[i] > -kInf && c[i] > -kInf ? c[i] : -kInf;
+        }
+        auto group_value = [&](float first, float second) {
+            if (!p.top2 || second == -kInf) return p.top2 ? second : first;
+            return biased ? first + second
+                          : (p.sigmoid ? rough_sigmoid(first) + rough_sigmoid(second)
+                                       : (rough_exp(first - m) + rough_exp(second - m)) * over);
+        };
+        // the groups' values: each of two scores off on either side, and their sums rounded
+        auto tell_groups = [&](float in, float out) { near |= in - out <= 4.0f * score_off + fabsf(in) * 0x1p-21f; };
+        if (grouped && !whole) {
+            double* value = of_group[threadIdx.x / L];
+            for (int g = 0; g < p.groups; ++g) {
+                float first = -kInf, second = -kInf;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float v = e0 + i >= g * size && e0 + i < (g + 1) * size ? c[i] : -kInf;
+                    second = fmaxf(second, fminf(first, v));
+                    first = fmaxf(first, v);
+                }
+#pragma unroll
+                for (int x = 1; x < L; x *= 2) {
+                    const float a = __shfl_xor(first, x, 64), o = __shfl_xor(second, x, 64);
+                    second = fmaxf(fminf(first, a), fmaxf(second, o));
+                    first = fmaxf(first, a);
+                }
+                const float v = group_value(first, second);
+                if (lane == 0) value[g] = v;
+            }
+            const uint64_t kept = best_groups<L>(value, p, lane);
+            float in = kInf, out = -kInf;  // the least of the groups that stay, the largest of the others
+            for (int g = 0; g < p.groups; ++g) {
+                const float v = static_cast<float>(value[g]);
+                const bool stays = kept >> g & 1;
+                in = fminf(in, stays ? v : kInf);
+                out = fmaxf(out, stays ? -kInf : v);
+            }
+            tell_groups(in, out);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (!(kept >> ((e0 + i) / size & 63) & 1)) c[i] = -kInf;
+        }
+        if (whole) {
+            float first = -kInf, second = -kInf;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                second = fmaxf(second, fminf(first, c[i]));
+                first = fmaxf(first, c[i]);
+            }
+            for (int x = 1; x < wide; x *= 2) {
+                const float a = __shfl_xor(first, x, 64), o = __shfl_xor(second, x, 64);
+                second = fmaxf(fminf(first, a), fmaxf(second, o));
+                first = fmaxf(first, a);
+            }
+            const float v = group_value(first, second);
+            const int group = lane / wide;
+            int before = 0;
+            for (int g = 0; g < p.groups; ++g) {
+                const float w = __shfl(v, g * wide, L);
+                before += w > v || (w == v && g < group);
+            }
+            const bool stays = before < p.top_groups && group < p.groups;
+            tell_groups(-lanes_max<L>(stays ? -v : -kInf), lanes_max<L>(stays || group >= p.groups ? -kInf : v));
+            if (!stays)
+#pragma unroll
+                for (int i = 0; i < N; ++i) c[i] = -kInf;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            low = fminf(low, c[i] > -kInf ? c[i] : kInf);
+            high = fmaxf(high, c[i]);
+        }
+        low = -lanes_max<L>(-low);
+        high = lanes_max<L>(high);
+        // places 1 .. 2^22 - 1; a token whose range is no positive number is chosen again, unless it has none to choose
+        const float range = high - low, scale = 4194302.0f / range;
+        near |= !(range > 0.0f && scale > 0.0f && scale < kInf) && high > -kInf;
+        uint32_t key[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t at = static_cast<uint32_t>((c[i] - low) * scale) + 1;
+            key[i] = c[i] > -kInf ? (at < 0x3FFFFFu ? at : 0x3FFFFFu) << 10 | (kMostExperts - 1 - (e0 + i)) : 0;
+        }
+        // places: each of two scores off and rounded with its bias, and of each place a unit cut off and half a unit of
+        // roundings (the scale's own is the same for all)
+        const float far = (2.0f * off + fmaxf(fabsf(low), fabsf(high)) * 0x1p-24f) * scale + 3.0f;
+        auto tell = [&](uint32_t a, uint32_t o) { near |= o != 0 && static_cast<float>((a >> 10) - (o >> 10)) <= far; };
+        auto number = [](uint32_t k) { return k == 0 ? -1 : kMostExperts - 1 - static_cast<int>(k & (kMostExperts - 1)); };
+        const auto larger2 = [](uint32_t a, uint32_t o) { return larger(a, o); };
+        if constexpr (K > 0) {
+            uint32_t list[K], left = 0, mine = 0;
+            best_keys<L, K>(key, list, left);
+            uint32_t next = left;
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                if (lane == j) mine = list[j];
+                if (lane + 1 == j) next = list[j];
+            }
+            if (lane < p.top_k) tell(mine, next);
+            id[0] = lane < p.top_k ? number(mine) : -1;
+        } else {
+            sort_keys<N>(key);
+            uint32_t last = 0xFFFFFFFFu;
+            for (int r = 0; r <= p.top_k; ++r) {  // also the best that is left
+                const uint32_t best = over_lanes<L>(key[0], larger2);
+                if (r > 0) tell(last, best);
+                last = best;
+                const bool pop = key[0] == best;
+#pragma unroll
+                for (int i = 0; i + 1 < N; ++i) key[i] = pop ? key[i + 1] : key[i];
+                key[N - 1] = pop ? 0 : key[N - 1];
+                const int e = number(best);
+#pragma unroll
+                for (int s = 0; s < S; ++s)
                     if (r < p.top_k && r == lane + s * L) id[s] = e;
             }
         }
-        return near;
+        return lanes_any<L>(near);
     };
 #pragma unroll
     for (int s = 0; s < S; ++s) id[s] = -1;
-    const bool near = choose();
+    bool near = false;
+    if constexpr (kScored)
+        near = choose_scored();
+    else
+        choose();
     float w[S], lw[S], most = -kInf, all = 0.0f;
 #pragma unroll
     for (int s = 0; s < S; ++s) {

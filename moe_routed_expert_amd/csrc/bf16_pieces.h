@@ -44,12 +44,6 @@ struct Piece8 {
         for (int i = 0; i < kWords; ++i) r.w[i] = *reinterpret_cast<const loose*>(p + 16 * i);
         return r;
     }
-    __device__ __forceinline__ static Raw load_nt(const char* p) {
-        Raw r;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) r.w[i] = __builtin_nontemporal_load(reinterpret_cast<const loose*>(p + 16 * i));
-        return r;
-    }
     // the first n of eight elements, zeros after them
     __device__ __forceinline__ static Raw load_first(const char* p, int64_t n) {
         if (n >= 8) return load(p);

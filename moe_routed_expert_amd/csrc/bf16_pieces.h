@@ -3,9 +3,9 @@
 // The matrix cores multiply float32 at an eighth of their 16-bit rate, so a
 // float32 is cut into up to three bfloat16 pieces, each the nearest bfloat16 to
 // what the ones before leave: x = x0 + x1 + x2 exactly (8 significant bits and a
-// sign each), |x1| <= 2^-9 |x|, |x2| <= 2^-18 |x|. Products of pieces are exact in
+// sign each), |x1| <= 2^-8 |x|, |x2| <= 2^-16 |x|. Products of pieces are exact in
 // float32. Of the pairs of pieces those with i + j <= 2 are summed; what is left
-// out is below 2^-26 of a product. A float16 (11 bits) is two pieces.
+// out is at most 2^-23 of a product. A float16 (11 bits) is two pieces.
 #pragma once
 
 #include "epi_common.h"
@@ -113,14 +113,14 @@ __device__ __forceinline__ void turn8(const u32x4 (&r)[8], u32x4 (&out)[8]) {
             out[j][i] = __builtin_amdgcn_perm(r[2 * i + 1][j / 2], r[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
 }
 
-// The sum over the pairs of pieces that count: i + j <= kMost.
-template <bool kF16, int kMost = 2, int PA, int PB>
+// The sum over the pairs of pieces that count: i + j <= 2.
+template <bool kF16, int PA, int PB>
 __device__ __forceinline__ f32x4 mfma_pieces(const u32x4 (&a)[PA], const u32x4 (&b)[PB], f32x4 d) {
 #pragma unroll
     for (int i = PA - 1; i >= 0; --i)
 #pragma unroll
         for (int j = PB - 1; j >= 0; --j)
-            if (i + j <= kMost) d = mfma16<kF16>(a[i], b[j], d);
+            if (i + j <= 2) d = mfma16<kF16>(a[i], b[j], d);
     return d;
 }
 

@@ -304,14 +304,16 @@ int64_t logits_parts(int64_t tokens, int64_t hidden, int64_t experts) {
 
 // ---- gradients ----------------------------------------------------------------------
 
-// Pieces of the factors. A result of 16 bits is rounded to 2^-9 of itself or
-// 2^-12: two pieces of the float32 factors (2^-17 of each term) are beyond that
-// even where terms cancel to a hundredth; a float32 result takes all three.
-template <int T, int Out>
+// Pieces of the factors: all bits of both, also where the result has 16. The
+// terms of a sum may cancel (gradients of a softmax's logits add up to 0 over a
+// token's experts), and then what two pieces of a float32 leave out is more than
+// the result's rounding. The third piece of grad_logits takes 416 us instead of
+// 381 (both gradients, 65536 x 7168 x 64 bf16), that of a float32 weight also
+// 87 instead of 57 (grad_x, 16384 x 7168 x 64).
+template <int T>
 struct GradPieces {
-    static constexpr int kMost = Out == MOE_EPI_F32 ? 2 : 1;   // largest i + j of a pair that counts
-    static constexpr int kGrad = kMost + 1;
-    static constexpr int kOther = T == MOE_EPI_BF16 ? 1 : (T == MOE_EPI_F16 ? 2 : kMost + 1);
+    static constexpr int kGrad = 3;
+    static constexpr int kOther = T == MOE_EPI_BF16 ? 1 : (T == MOE_EPI_F16 ? 2 : 3);
 };
 
 // The elements j of eight rows of 16 bytes each, as pieces.
@@ -363,7 +365,7 @@ template <int T, int W, int KS, int HT, int MT>
 __global__ __launch_bounds__(kBlock) void grad_x_kernel(const float* __restrict__ grad, const char* __restrict__ weight,
                                                         char* __restrict__ grad_x, int64_t tokens, int64_t hidden,
                                                         int64_t experts, int64_t tokens_a_block) {
-    typedef GradPieces<W, T> P;
+    typedef GradPieces<W> P;
     typedef Piece8<MOE_EPI_F32> G;
     constexpr int V = 16 / Elem<W>::kBytes;  // weights of a 16-byte load
     constexpr int kTileBytes = 16 * Elem<T>::kBytes;  // of 16 hidden elements of a token
@@ -434,7 +436,7 @@ __global__ __launch_bounds__(kBlock) void grad_x_kernel(const float* __restrict_
 #pragma unroll
                     for (int p = 0; p < P::kOther; ++p) w[p] = lds[((j + a) * KS + k) * P::kOther + p][lane];
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) d[a][m] = mfma_pieces<false, P::kMost>(w, g[m][k], d[a][m]);
+                    for (int m = 0; m < MT; ++m) d[a][m] = mfma_pieces<false>(w, g[m][k], d[a][m]);
                 }
             }
 #pragma unroll
@@ -490,7 +492,7 @@ __global__ __launch_bounds__(kBlock) void grad_x_many_kernel(const float* __rest
                                                              const char* __restrict__ weight,
                                                              char* __restrict__ grad_x, int64_t tokens, int64_t hidden,
                                                              int64_t experts, int64_t tokens_a_block) {
-    typedef GradPieces<W, T> P;
+    typedef GradPieces<W> P;
     typedef Piece8<MOE_EPI_F32> G;
     constexpr int V = 16 / Elem<W>::kBytes, KS = kMostExperts / 32;
     __shared__ u32x4 lds[KS * P::kOther][64];
@@ -525,7 +527,7 @@ __global__ __launch_bounds__(kBlock) void grad_x_many_kernel(const float* __rest
             cut_raw<MOE_EPI_F32, P::kGrad>(raw, g);
 #pragma unroll
             for (int p = 0; p < P::kOther; ++p) w[p] = lds[k * P::kOther + p][lane];
-            d = mfma_pieces<false, P::kMost>(w, g, d);
+            d = mfma_pieces<false>(w, g, d);
         }
         if (t >= end) continue;
         const int64_t h = h0 + lane / 16 * 4;
@@ -585,7 +587,7 @@ template <int T, int W, int ET, bool kOnce>
 __global__ __launch_bounds__(64 * kGradWaves) void grad_weight_kernel(const float* __restrict__ grad, const char* __restrict__ x,
                                                              float* __restrict__ parts, int64_t tokens, int64_t hidden,
                                                              int64_t experts) {
-    typedef GradPieces<T, W> P;
+    typedef GradPieces<T> P;
     constexpr int HT = 8 / Elem<T>::kBytes;  // hidden of a lane
     __shared__ u32x4 lds[2][ET][P::kGrad][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -645,7 +647,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void grad_weight_kernel(const floa
 #pragma unroll
         for (int e = 0; e < ET; ++e)
 #pragma unroll
-            for (int j = 0; j < HT; ++j) d[e][j] = mfma_pieces<false, P::kMost>(g[e], v[j], d[e][j]);
+            for (int j = 0; j < HT; ++j) d[e][j] = mfma_pieces<false>(g[e], v[j], d[e][j]);
     };
     const int64_t whole = (tokens - 1) / 32 < last ? (tokens - 1) / 32 : last;  // steps before the last token's
     constexpr int kDeep = 4;
@@ -767,7 +769,7 @@ void launch_grad_x(const float* grad, const void* weight, void* grad_x, int64_t 
                            static_cast<char*>(grad_x), tokens, hidden, experts, each);
     };
     // hidden of a block: as many as 64 KB of LDS hold, up to 512
-    constexpr int kW = GradPieces<W, T>::kOther;
+    constexpr int kW = GradPieces<W>::kOther;
     auto by_steps = [&](auto ks) {
         constexpr int KS = decltype(ks)::value, kFit = 64 * 1024 / (KS * kW * 1024), MT = KS > 4 ? 1 : 2;
         constexpr int HT = kFit >= 32 ? 32 : (kFit >= 16 ? 16 : (kFit >= 8 ? 8 : (kFit >= 4 ? 4 : 2)));

@@ -326,6 +326,30 @@ def test_router_logits_gradients_against_differences():
             assert abs(num - float((grad.double() * d.double()).sum())) <= 4 * (hidden + 16) * ref.EPS * size
 
 
+@pytest.mark.parametrize("dtype,weight", PAIRS)
+def test_router_gradients_keep_all_bits_where_terms_cancel(dtype, weight):
+    """Sums of two terms that cancel to 2^-12 of their size: a 16-bit result is rounded to 2^-20 of the terms or less, so
+    factors of fewer bits than float32 has would show. The other terms are products with 0, which round nothing."""
+    rng = np.random.default_rng(31)
+    for tokens, hidden, experts in ((3, 40, 5), (200, 264, 40), (70, 136, 100), (40, 72, 300)):
+        u = 16 * rng.standard_normal((2, max(tokens, experts)))
+        u[1] = -u[0] * (1 + 2.0 ** -12 * u[1])
+        # two experts whose rows of the weight are equal
+        w, g = normal(rng, (experts, hidden), weight), np.zeros((tokens, experts), np.float32)
+        w[experts - 1] = w[1]
+        g[:, [1, experts - 1]] = u[:, :tokens].T
+        gx, gd = sentinel((tokens, hidden), dtype), torch.from_numpy(g).cuda()
+        epi.moe_router_logits_bwd(gd, sentinel((tokens, hidden), dtype), w, gx, None)
+        check(gx, *ref.product(g[:, [1, experts - 1]].astype(np.float64), ref.f64(w[[1, experts - 1]])), dtype, "grad_x")
+        # two tokens of equal rows
+        x, g = normal(rng, (tokens, hidden), dtype), np.zeros((tokens, experts), np.float32)
+        x[tokens - 1] = x[1]
+        g[[1, tokens - 1]] = u[:, :experts]
+        gw, gd = sentinel((experts, hidden), weight), torch.from_numpy(g).cuda()
+        epi.moe_router_logits_bwd(gd, x, w, None, gw, space(epi.moe_router_logits_bwd_workspace_bytes(tokens, hidden, experts)))
+        check(gw, *ref.product(g[[1, tokens - 1]].astype(np.float64).T, ref.f64(x[[1, tokens - 1]])), weight, "grad_weight")
+
+
 # ---- choice of the experts ----------------------------------------------------------------------
 
 FORMS = [dict(score=s, bias=b, groups=g) for s in ("softmax", "sigmoid") for b in (False, True)

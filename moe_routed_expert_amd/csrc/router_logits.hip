@@ -20,6 +20,7 @@
 #include "bf16_pieces.h"
 #include "epi_common.h"
 #include "moe_prologue.h"
+#include "router_map.h"
 
 namespace moe_epi {
 namespace {
@@ -597,7 +598,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void grad_weight_kernel(const floa
     const int tile = wave % ET, half = wave / ET % 2;
     const bool staging = wave < 2 * ET;
     const int64_t e0 = blockIdx.y * 16 * ET, mine = e0 + 16 * tile + of16;
-    const int64_t steps = (tokens + 31) / 32;
+    const int64_t steps = (tokens + kGradStep - 1) / kGradStep;
     const int64_t first = steps * blockIdx.z / gridDim.z, last = steps * (blockIdx.z + 1) / gridDim.z;
     const int64_t left = hidden - h;
     f32x4 d[ET][HT];
@@ -610,7 +611,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void grad_weight_kernel(const floa
         float g[4];
     };
     // Columns past the last hidden element or expert are loaded from what comes after, or from the first ones, and
-    // not stored; only the tensors' last token, in the last step, has nothing after it.
+    // not stored; the last steps, whose tokens have too little after them, load by bounds (router_map.h).
     // A load's address is that of a token, which the wavefront shares, and the lane's 32-bit place from there.
     const uint32_t at = static_cast<uint32_t>((k8 * hidden + (left > 0 ? h : 0)) * Elem<T>::kBytes);
     const uint32_t at_g = static_cast<uint32_t>(((k8 + 4 * half) * experts + (mine < experts ? mine : experts - 1)) * 4);
@@ -620,14 +621,14 @@ __global__ __launch_bounds__(64 * kGradWaves) void grad_weight_kernel(const floa
         typedef u32x2 loose __attribute__((aligned(2)));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const loose* p = reinterpret_cast<const loose*>(token_x(s * 32 + i) + at);
+            const loose* p = reinterpret_cast<const loose*>(token_x(s * kGradStep + i) + at);
             if constexpr (kOnce)
                 a.x[i] = __builtin_nontemporal_load(p);
             else
                 a.x[i] = *p;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a.g[i] = *reinterpret_cast<const float*>(token_g(s * 32 + i) + at_g);
+        for (int i = 0; i < 4; ++i) a.g[i] = *reinterpret_cast<const float*>(token_g(s * kGradStep + i) + at_g);
     };
     auto stage = [&](Ahead& a, int buf) {
         if (!staging) return;
@@ -649,7 +650,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void grad_weight_kernel(const floa
 #pragma unroll
             for (int j = 0; j < HT; ++j) d[e][j] = mfma_pieces<false>(g[e], v[j], d[e][j]);
     };
-    const int64_t whole = (tokens - 1) / 32 < last ? (tokens - 1) / 32 : last;  // steps before the last token's
+    const int64_t inside = steps_inside(tokens, hidden, HT), whole = inside < last ? inside : last;
     constexpr int kDeep = 4;
     if (first < whole) {
         Ahead a[kDeep];
@@ -670,19 +671,20 @@ __global__ __launch_bounds__(64 * kGradWaves) void grad_weight_kernel(const floa
                 __syncthreads();
             }
     }
-    if (whole < last) {
+#pragma unroll 1
+    for (int64_t s = whole < first ? first : whole; s < last; ++s) {
         Ahead a;
-        const int64_t t = whole * 32 + k8;
+        const int64_t t = s * kGradStep + k8;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            a.x[i] = t + i < tokens && left > 0 ? load8<T>(token_x(whole * 32 + i) + at, left) : u32x2{0, 0};
+            a.x[i] = t + i < tokens && left > 0 ? load8<T>(token_x(s * kGradStep + i) + at, left) : u32x2{0, 0};
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            a.g[i] = t + 4 * half + i < tokens ? *reinterpret_cast<const float*>(token_g(whole * 32 + i) + at_g) : 0.0f;
-        stage(a, 0);
+            a.g[i] = t + 4 * half + i < tokens ? *reinterpret_cast<const float*>(token_g(s * kGradStep + i) + at_g) : 0.0f;
+        stage(a, s & 1);
         __syncthreads();
-        multiply(a, 0);
+        multiply(a, s & 1);
     }
     float* to = parts + blockIdx.z * experts * hidden;
 #pragma unroll
@@ -710,7 +712,7 @@ __global__ __launch_bounds__(kBlock) void add_weight_parts_kernel(const float* _
 
 // Parts that the tokens are shared by for the weight's gradient.
 int64_t grad_parts(int64_t tokens, int64_t hidden, int64_t experts) {
-    const int64_t blocks = up(hidden, 512) * up(experts, 64), wanted = 256 / blocks, most = up(tokens, 4 * 32);
+    const int64_t blocks = up(hidden, 512) * up(experts, 64), wanted = 256 / blocks, most = up(tokens, 4 * kGradStep);
     const int64_t n = wanted < most ? wanted : most;
     return n < 1 ? 1 : n;
 }

@@ -283,6 +283,19 @@ def test_router_logits_gradients(dtype, weight, tokens, hidden, experts):
         assert torch.equal(bits(gx), bits(gx2)) and torch.equal(bits(gw), bits(gw2))
 
 
+@pytest.mark.parametrize("dtype,weight", PAIRS)
+@pytest.mark.parametrize("hidden", [1, 2, 3, 5])
+def test_router_weight_gradient_of_short_rows(dtype, weight, hidden):
+    """Rows shorter than a lane's load, in numbers around a step's and a part's."""
+    rng = np.random.default_rng(33)
+    for tokens in (31, 32, 33, 34, 65, 66, 97, 130, 161, 290):
+        x, g = normal(rng, (tokens, hidden), dtype), normal(rng, (tokens, 6), F32)
+        gw = sentinel((6, hidden), weight)
+        epi.moe_router_logits_bwd(g, x, normal(rng, (6, hidden), weight), None, gw,
+                                  space(epi.moe_router_logits_bwd_workspace_bytes(tokens, hidden, 6)))
+        check(gw, *ref.product(ref.f64(g).T, ref.f64(x)), weight, "grad_weight")
+
+
 def test_router_logits_of_no_tokens():
     w, none = torch.ones(8, 16, device="cuda"), torch.empty(0, 16, device="cuda")
     assert epi.moe_router_logits(none, w).shape == (0, 8)

@@ -73,11 +73,11 @@ int64_t rms_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
 /*
  * The router's product: logits[t, e] = sum_h x[t, h] * weight[e, h], products
  * of all bits of both (of two float32 factors up to 2^-23 of the product is left
- * out), float32 sums. x and weight of one 16-bit type follow
- * IEEE arithmetic; where one of them is float32, a row of x or of weight that
- * holds an infinity or a NaN gives NaN or an infinity. The order of a sum depends
- * on the sizes of the call, so a token's logits may differ in their last bits in
- * calls of other sizes.
+ * out), float32 sums. x and weight of one 16-bit type follow IEEE arithmetic; where
+ * one of them is float32, a row of x or of weight that holds an infinity or a NaN
+ * gives NaN or an infinity, and every finite factor is taken as it is. The order of
+ * a sum depends on the sizes of the call, so a token's logits may differ in their
+ * last bits in calls of other sizes.
  *   x         [tokens, hidden] of dtype                       in
  *   weight    [experts, hidden] of w_dtype (dtype or float32) in
  *   logits    [tokens, experts] float32                       out
@@ -95,6 +95,8 @@ int64_t moe_router_logits_workspace_bytes(int64_t tokens, int64_t hidden, int64_
  *   grad_x[t, h]      = sum_e grad_logits[t, e] * weight[e, h]
  *   grad_weight[e, h] = sum_t grad_logits[t, e] * x[t, h]
  * (products as in the forward call, float32 sums, rounded once). Every element is written.
+ * A sum with an infinity or a NaN among its factors is NaN or an infinity, also
+ * where IEEE arithmetic has an infinity, and no other sum is.
  *   grad_logits [tokens, experts] float32                       in
  *   x           [tokens, hidden] of dtype; may be NULL if grad_weight is           in
  *   weight      [experts, hidden] of w_dtype (dtype or float32); may be NULL if grad_x is   in

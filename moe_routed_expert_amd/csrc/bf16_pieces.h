@@ -66,18 +66,28 @@ struct Piece8 {
     }
 };
 
+// Two values' piece, which leaves f what the next pieces are of. Values beyond
+// the largest bfloat16 have that as theirs, and not an infinity: what is left of
+// a finite one is its next pieces, and of an infinity or a NaN its last piece,
+// which is not held back (kLast). Float32 logits of 16384 x 7168 x 64 take 137
+// us so, 133 without.
+template <bool kLast>
+__device__ __forceinline__ uint32_t cut2(float& a, float& b) {
+    constexpr float kMost = 0x1.fep127f;
+    const uint32_t w = kLast ? pack_bf16x2(a, b)
+                             : pack_bf16x2(__builtin_amdgcn_fmed3f(a, -kMost, kMost), __builtin_amdgcn_fmed3f(b, -kMost, kMost));
+    a -= bf16_lo(w);
+    b -= bf16_hi(w);
+    return w;
+}
 // f as P pieces.
 template <int P>
 __device__ __forceinline__ void cut(float (&f)[8], u32x4 (&piece)[P]) {
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-            piece[p][i] = w;
-            f[2 * i] -= bf16_lo(w);
-            f[2 * i + 1] -= bf16_hi(w);
-        }
+        for (int i = 0; i < 4; ++i)
+            piece[p][i] = p + 1 < P ? cut2<false>(f[2 * i], f[2 * i + 1]) : cut2<true>(f[2 * i], f[2 * i + 1]);
 }
 // Four values as P pieces.
 template <int P>
@@ -85,12 +95,8 @@ __device__ __forceinline__ void cut4(float (&f)[4], u32x2 (&piece)[P]) {
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t w = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-            piece[p][i] = w;
-            f[2 * i] -= bf16_lo(w);
-            f[2 * i + 1] -= bf16_hi(w);
-        }
+        for (int i = 0; i < 2; ++i)
+            piece[p][i] = p + 1 < P ? cut2<false>(f[2 * i], f[2 * i + 1]) : cut2<true>(f[2 * i], f[2 * i + 1]);
 }
 // r as P pieces; the type itself where it has one piece.
 template <int T, int P>

@@ -363,6 +363,66 @@ def test_router_gradients_keep_all_bits_where_terms_cancel(dtype, weight):
         check(gw, *ref.product(g[[1, tokens - 1]].astype(np.float64).T, ref.f64(x[[1, tokens - 1]])), weight, "grad_weight")
 
 
+@pytest.mark.parametrize("dtype,weight", [(BF16, F32), (F16, F32), (F32, F32)])
+def test_router_products_of_the_largest_float32(dtype, weight):
+    """Finite float32 factors above the largest bfloat16, which round to an infinite one, have finite products."""
+    rng = np.random.default_rng(32)
+    tokens, hidden, experts = 150, 200, 20
+    largest = np.finfo(np.float32).max
+    beyond = np.array([largest, -largest, 3.395e38, -3.397e38, 3.39e38, 3.3895314e38, -3.38e38], np.float32)
+
+    def put(shape):
+        """One of them in each row, zeros in the rest."""
+        a = np.zeros(shape, np.float32)
+        a[np.arange(shape[0]), rng.integers(0, shape[1], shape[0])] = rng.choice(beyond, shape[0])
+        return torch.from_numpy(a).cuda()
+
+    def small(shape, to):
+        return normal(rng, shape, to).clamp(-3, 3) * 2.0 ** -6
+
+    x, w = small((tokens, hidden), dtype), put((experts, hidden))
+    check(epi.moe_router_logits(x, w), *ref.product(ref.f64(x), ref.f64(w).T), F32, "logits")
+    if dtype == F32:
+        x, w = put((tokens, hidden)), small((experts, hidden), F32)
+        check(epi.moe_router_logits(x, w), *ref.product(ref.f64(x), ref.f64(w).T), F32, "logits")
+    g, x = put((tokens, experts)), small((tokens, hidden), dtype)
+    gw = sentinel((experts, hidden), weight)
+    g[1:] *= 2.0 ** -6                                     # a sum over the tokens has one of the largest
+    g[1:, 3] = 0
+    epi.moe_router_logits_bwd(g, x, w, None, gw, space(epi.moe_router_logits_bwd_workspace_bytes(tokens, hidden, experts)))
+    check(gw, *ref.product(ref.f64(g).T, ref.f64(x)), weight, "grad_weight")
+    if dtype != F16:                                       # whose results would be infinite
+        g, w, gx = put((tokens, experts)), small((experts, hidden), weight), sentinel((tokens, hidden), dtype)
+        epi.moe_router_logits_bwd(g, x, w, gx, None)
+        check(gx, *ref.product(ref.f64(g), ref.f64(w)), dtype, "grad_x")
+        g, w = small((tokens, experts), F32), put((experts, hidden)) * 2.0 ** -3
+        w[1] = float(largest)
+        epi.moe_router_logits_bwd(g, x, w, gx, None)
+        check(gx, *ref.product(ref.f64(g), ref.f64(w)), dtype, "grad_x")
+
+
+@pytest.mark.parametrize("dtype,weight", PAIRS)
+def test_router_gradients_with_infinities_and_nans(dtype, weight):
+    """They reach the sums that have them among their factors, and no other."""
+    rng = np.random.default_rng(34)
+    tokens, hidden, experts = 70, 200, 20
+    x, w, g = normal(rng, (tokens, hidden), dtype), normal(rng, (experts, hidden), weight), normal(rng, (tokens, experts), F32)
+
+    def call():
+        gx, gw = sentinel(x.shape, dtype), sentinel(w.shape, weight)
+        epi.moe_router_logits_bwd(g, x, w, gx, gw, space(epi.moe_router_logits_bwd_workspace_bytes(tokens, hidden, experts)))
+        return gx.cpu(), gw.cpu()
+
+    clean = call()
+    g[3, 5], g[69, 7], x[17, 100], w[6, 9] = float("inf"), float("nan"), -float("inf"), float("inf")
+    bad = torch.zeros(tokens, hidden, dtype=torch.bool), torch.zeros(experts, hidden, dtype=torch.bool)
+    bad[0][[3, 69]] = bad[0][:, 9] = True
+    bad[1][[5, 7]] = bad[1][:, 100] = True
+    for got, want, of in zip(call(), clean, bad):
+        assert not bool(torch.isfinite(got[of]).any())
+        assert torch.equal(got[~of], want[~of])
+
+
 # ---- choice of the experts ----------------------------------------------------------------------
 
 FORMS = [dict(score=s, bias=b, groups=g) for s in ("softmax", "sigmoid") for b in (False, True)

@@ -655,9 +655,9 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const char* __restrict__ 
             const uint32_t at = static_cast<uint32_t>((c[i] - low) * scale) + 1;
             key[i] = c[i] > -kInf ? (at < 0x3FFFFFu ? at : 0x3FFFFFu) << 10 | (kMostExperts - 1 - (e0 + i)) : 0;
         }
-        // places: each of two scores off and rounded with its bias, and of each place a unit cut off and half a unit of
-        // roundings (the scale's own is the same for all)
-        const float far = (2.0f * off + fmaxf(fabsf(low), fabsf(high)) * 0x1p-24f) * scale + 3.0f;
+        // places: each of two scores off and rounded with its bias (to half an ulp, 2^-24 of the sum), and of each place
+        // a unit cut off and half a unit of roundings (the scale's own is the same for all)
+        const float far = (2.0f * off + fmaxf(fabsf(low), fabsf(high)) * 0x1p-23f) * scale + 3.0f;
         auto tell = [&](uint32_t a, uint32_t o) { near |= o != 0 && static_cast<float>((a >> 10) - (o >> 10)) <= far; };
         auto number = [](uint32_t k) { return k == 0 ? -1 : kMostExperts - 1 - static_cast<int>(k & (kMostExperts - 1)); };
         const auto larger2 = [](uint32_t a, uint32_t o) { return larger(a, o); };

@@ -515,6 +515,27 @@ def test_a_tokens_choice_is_the_same_in_calls_of_all_sizes(form):
         assert torch.equal(a, ids[at:at + n]) and torch.equal(b, weights[at:at + n])
 
 
+@pytest.mark.parametrize("offset", [0.02, 1.02, 16.02, 17.0, 33.0, 64.1, 130.0, 513.0])
+@pytest.mark.parametrize("experts,top_k", [(16, 8), (16, 11), (200, 8)])
+def test_route_by_scores_that_a_common_bias_makes_coarse(offset, experts, top_k):
+    """With a large part in common float32's biased scores are an ulp of that part apart, and each of two is off by up to
+    half of it. A token's first two experts are within 2^-25 of a border between two float32 values, where what their
+    scores are off decides to which side each goes: they keep the order of 64 bits."""
+    rng = np.random.default_rng(int(offset) + experts + top_k)
+    tokens = 1500
+    for spread in (0.05, 0.2, 0.4):
+        bias = (offset + rng.uniform(0, spread, experts)).astype(np.float32)
+        bias[[2, experts - 1]] = np.float32(offset + spread), np.float32(offset + 1.01 * spread)
+        logits = rng.uniform(-0.3, 0.3, (tokens, experts))
+        ulp = float(np.spacing(np.float32(offset + spread + 0.6)))
+        border = (np.floor((offset + spread + rng.uniform(0.6, 0.7, tokens)) / ulp) + 0.5) * ulp
+        for e in (2, experts - 1):
+            s = border - float(bias[e]) + rng.uniform(-1, 1, tokens) * 2.0 ** -25
+            logits[:, e] = np.log(s / (1 - s))
+        check_route(torch.from_numpy(logits.astype(np.float32)).cuda(), top_k, torch.from_numpy(bias).cuda(),
+                    dict(score="sigmoid", groups=(1, 1, "max")), True, 1.0)
+
+
 GRADS = [(s, r) for s in ("softmax", "sigmoid") for r in (False, True)]
 
 

@@ -464,6 +464,7 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const char* __restrict__ 
                                                        int64_t tokens, Choice p) {
     constexpr int kTokens = kBlock / L;
     __shared__ double of_group[kTokens][kMostGroups];  // only of groups that do not lie in whole lanes
+    __shared__ f32x2_t range_group[kScored ? kTokens : 1][kScored ? kMostGroups : 1];
     __shared__ double value64[kScored ? kBlock / 64 : 1][kScored ? (L * N < 64 ? 64 : L * N) : 1];
     __shared__ double group64[kScored ? kBlock / 64 : 1][kScored ? kMostGroups : 1];
     const int lane = threadIdx.x % L, e0 = lane * N, size = p.experts / p.groups;
@@ -580,10 +581,24 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const char* __restrict__ 
                           : (p.sigmoid ? rough_sigmoid(first) + rough_sigmoid(second)
                                        : (rough_exp(first - m) + rough_exp(second - m)) * over);
         };
-        // the groups' values: each of two scores off on either side, and their sums rounded
-        auto tell_groups = [&](float in, float out) { near |= in - out <= 4.0f * score_off + fabsf(in) * 0x1p-21f; };
+        // Where a group's value is: it is off by two scores, each rounded with its bias, which may be far larger than
+        // the sum of both, and by that sum's rounding: 2^-24 of the biased scores' sizes each time, and once more for
+        // the border. A sum beyond float32 may be anywhere; -inf for a lack of experts is what it is.
+        struct Within {
+            float least, most;
+        };
+        auto range_of_group = [&](float v, float first, float second) {
+            if ((p.top2 ? second : first) == -kInf) return Within{-kInf, -kInf};
+            if (!(fabsf(v) < kInf)) return Within{-kInf, kInf};
+            const float sizes = biased ? fabsf(first) + (p.top2 ? fabsf(second) : 0.0f) : fabsf(v);
+            const float off_by = 2.0f * score_off + sizes * 0x1p-22f;
+            return Within{v - off_by, v + off_by};
+        };
+        // in: the least of the groups that stay, out: the most of the others
+        auto tell_groups = [&](float in, float out) { near |= out > -kInf && !(in > out); };
         if (grouped && !whole) {
             double* value = of_group[threadIdx.x / L];
+            f32x2_t* range = range_group[kScored ? threadIdx.x / L : 0];
             for (int g = 0; g < p.groups; ++g) {
                 float first = -kInf, second = -kInf;
 #pragma unroll
@@ -599,15 +614,18 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const char* __restrict__ 
                     first = fmaxf(first, a);
                 }
                 const float v = group_value(first, second);
-                if (lane == 0) value[g] = v;
+                if (lane == 0) {
+                    const Within r = range_of_group(v, first, second);
+                    value[g] = v;
+                    range[g] = f32x2_t{r.least, r.most};
+                }
             }
             const uint64_t kept = best_groups<L>(value, p, lane);
-            float in = kInf, out = -kInf;  // the least of the groups that stay, the largest of the others
+            float in = kInf, out = -kInf;
             for (int g = 0; g < p.groups; ++g) {
-                const float v = static_cast<float>(value[g]);
                 const bool stays = kept >> g & 1;
-                in = fminf(in, stays ? v : kInf);
-                out = fmaxf(out, stays ? -kInf : v);
+                in = fminf(in, stays ? range[g][0] : kInf);
+                out = fmaxf(out, stays ? -kInf : range[g][1]);
             }
             tell_groups(in, out);
 #pragma unroll
@@ -634,7 +652,8 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const char* __restrict__ 
                 before += w > v || (w == v && g < group);
             }
             const bool stays = before < p.top_groups && group < p.groups;
-            tell_groups(-lanes_max<L>(stays ? -v : -kInf), lanes_max<L>(stays || group >= p.groups ? -kInf : v));
+            const Within r = range_of_group(v, first, second);
+            tell_groups(-lanes_max<L>(stays ? -r.least : -kInf), lanes_max<L>(stays || group >= p.groups ? -kInf : r.most));
             if (!stays)
 #pragma unroll
                 for (int i = 0; i < N; ++i) c[i] = -kInf;

@@ -536,6 +536,40 @@ def test_route_by_scores_that_a_common_bias_makes_coarse(offset, experts, top_k)
                     dict(score="sigmoid", groups=(1, 1, "max")), True, 1.0)
 
 
+@pytest.mark.parametrize("size", [2, 3, 4])
+@pytest.mark.parametrize("offset", [0.5, 4.0, 16.0, 32.0, 100.0])
+def test_route_by_groups_whose_biases_cancel(offset, size):
+    """A group's two best have biases of opposite sign: the roundings of both stay in their sum, which is small. Groups
+    that are nearer than those keep the order of 64 bits."""
+    rng = np.random.default_rng(int(offset) + size)
+    groups, tokens = 4, 1500
+    bias = np.full((groups, size), -4 * offset) + rng.uniform(-0.05, 0.05, (groups, size))
+    bias[:, 0] += 5 * offset
+    bias[:, 1] += 3 * offset
+    bias = bias.astype(np.float32)
+    logits = rng.uniform(-0.3, 0.3, (tokens, groups, size)).astype(np.float32)
+    s = ref.scores(logits.astype(np.float64), "sigmoid") + bias
+    for g in (1, 2, 3):                                    # the sum of the first group, by the second expert's score
+        want = s[:, 0, :2].sum(1) - s[:, g, 0] - float(bias[g, 1]) + rng.uniform(-1, 1, tokens) * 2.0 ** -22
+        logits[:, g, 1] = np.log(want / (1 - want))
+    logits = torch.from_numpy(logits.reshape(tokens, groups * size)).cuda()
+    check_route(logits, 4, torch.from_numpy(bias.reshape(-1)).cuda(), dict(score="sigmoid", groups=(groups, 2, "top2")), True,
+                1.0)
+
+
+@pytest.mark.parametrize("size", [2, 3])
+def test_route_by_groups_whose_sums_are_beyond_float32(size):
+    """Sums of two finite biases that float32 does not hold, an infinite bias, and groups with fewer than two experts."""
+    rng = np.random.default_rng(size)
+    tokens = 40
+    for best in ([2.0e38, 2.5e38, 3e38, 1e38], [3e38, 3e38, 3.1e38, 3e38], [np.inf, 1.0, 3e38, np.inf],
+                 [-np.inf, 1.0, 2.0, -np.inf], [-3e38, -2e38, -2.5e38, -3.1e38]):
+        bias = np.array(best)[:, None] * np.linspace(1, 0.9, size)
+        for score in ("sigmoid", "softmax"):
+            check_route(normal(rng, (tokens, 4 * size), F32), 4, torch.from_numpy(bias.reshape(-1).astype(np.float32)).cuda(),
+                        dict(score=score, groups=(4, 2, "top2")), True, 1.0)
+
+
 GRADS = [(s, r) for s in ("softmax", "sigmoid") for r in (False, True)]
 
 

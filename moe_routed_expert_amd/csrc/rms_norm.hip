@@ -525,24 +525,29 @@ __global__ __launch_bounds__(kBlock) void grad_weight_parts_kernel(const void* g
     parts[p * cols + c] = sum;
 }
 
-// 64 columns a block; its 16 wavefronts share the parts, and their sums are added in order.
+// 64 columns a block, and a multiple of the grid's beyond; its 16 wavefronts share the parts, and their sums are added in
+// order.
 template <int W>
 __global__ __launch_bounds__(1024) void grad_weight_kernel(const float* __restrict__ parts, void* __restrict__ grad_weight,
                                                            int64_t n, int64_t cols) {
     __shared__ float sums[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-    float sum = 0.0f;
-    if (c < cols) {
+    for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * 64; c0 < cols; c0 += static_cast<int64_t>(gridDim.x) * 64) {
+        const int64_t c = c0 + lane;
+        float sum = 0.0f;
+        if (c < cols) {
 #pragma unroll 8
-        for (int64_t p = n * wave / 16; p < n * (wave + 1) / 16; ++p) sum += parts[p * cols + c];
-    }
-    sums[wave][lane] = sum;
-    __syncthreads();
-    if (wave != 0 || c >= cols) return;
+            for (int64_t p = n * wave / 16; p < n * (wave + 1) / 16; ++p) sum += parts[p * cols + c];
+        }
+        sums[wave][lane] = sum;
+        __syncthreads();
+        if (wave == 0 && c < cols) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) sum += sums[i][lane];
-    Elem<W>::store1(grad_weight, c, sum);
+            for (int i = 1; i < 16; ++i) sum += sums[i][lane];
+            Elem<W>::store1(grad_weight, c, sum);
+        }
+        __syncthreads();  // sums is used again
+    }
 }
 
 constexpr int64_t kMostHeld = 8192;  // columns that the lanes of a block hold: with 1024 lanes the registers do not do
@@ -707,7 +712,7 @@ extern "C" int rms_norm_bwd(const void* grad_out, const void* h, int dtype, cons
                                 grad_weight ? parts : nullptr, n_parts, rows, cols, st);
         }
         if (grad_weight)
-            hipLaunchKernelGGL((grad_weight_kernel<W>), dim3(static_cast<unsigned>((cols + 63) / 64)), dim3(1024), 0, st,
+            hipLaunchKernelGGL((grad_weight_kernel<W>), dim3(grid_for_rows(cols, 64)), dim3(1024), 0, st,
                                parts, grad_weight, n_parts, cols);
     });
     return launch_status();

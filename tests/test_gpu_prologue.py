@@ -826,6 +826,17 @@ def test_calls_past_2_32_bytes_and_of_several_launches():
         check(logits[part], *ref.product(ref.f64(x[part]), ref.f64(w).T), F32, "logits")
 
 
+def test_norm_gradients_of_more_columns_than_a_grid_of_blocks():
+    """2^28 columns and some: one launch of a block for each 64 of them would have 2^32 work-items."""
+    cols = (1 << 28) + 72
+    h = torch.randn(1, cols, device="cuda").to(BF16)
+    g, w = h.flip(1), torch.ones(cols, dtype=BF16, device="cuda")
+    rstd = torch.full((1,), 0.75, device="cuda")
+    gx, gw = torch.empty_like(h), sentinel((cols,), BF16)
+    epi.rms_norm_bwd(g, h, w, rstd, gx, gw, space(epi.rms_norm_bwd_workspace_bytes(1, cols)))
+    assert torch.equal(gw, (g[0].float() * (h[0].float() * 0.75)).to(BF16))   # one row: one product, rounded
+
+
 @pytest.mark.parametrize("dtype,weight", PAIRS)
 def test_router_products_of_small_values(dtype, weight):
     """Factors whose pieces or products leave the normal range of their type: a value that a matrix instruction takes

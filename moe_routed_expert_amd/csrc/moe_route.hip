@@ -4,9 +4,12 @@
 // experts in a row each. A lane sorts its own, and lists are joined lane by
 // lane, which keeps the 8 largest of two sorted lists by comparing one with the
 // other reversed; more than 8 are taken one after the other from sorted lanes.
-// Keys hold the expert's number below the value: float64 for logits, whose order
-// is exact, 32 bits for scores, of which those too near to tell are chosen again
-// in float64.
+// Keys are float64, with the expert's number below a float32 value. The order of
+// logits is exact; a token with biased scores too near to tell, or groups' sums,
+// is chosen again in float64, by its whole wavefront: with equal biases and bfloat16
+// logits, of which many are equal, that is a third of the tokens (65536 x 256 in
+// groups 140 us instead of 48). An expert that a bias of -1e4 or -1e9 switches off
+// changes nothing (47 us).
 //
 // Bound by vector instructions: 65536 tokens, 8 of 256 experts by logits 23 us
 // (10 at a copy's rate), in groups by biased sigmoids 48 us; 131072 tokens, 8
@@ -64,10 +67,6 @@ __device__ __forceinline__ float partner(float v) {
     return __int_as_float(partner<kXor>(__float_as_int(v)));
 }
 template <int kXor>
-__device__ __forceinline__ uint32_t partner(uint32_t v) {
-    return static_cast<uint32_t>(partner<kXor>(static_cast<int>(v)));
-}
-template <int kXor>
 __device__ __forceinline__ double partner(double v) {
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
     const uint32_t lo = static_cast<uint32_t>(partner<kXor>(static_cast<int>(u)));
@@ -102,10 +101,6 @@ __device__ __forceinline__ bool lanes_any(bool v) {
 // A key is a float32 value as a float64, whose last 10 bits (of the 29 that the
 // value leaves free) are the expert's number, turned so that of equal values the
 // lowest expert has the largest key. -inf: not to be chosen.
-//
-// Scores are of a narrow range and known to a few float32 steps: their keys are
-// 32 bits, the place between the token's least and largest in the upper 22 and
-// the expert's number below. 0: not to be chosen.
 
 constexpr uint64_t kNumber = kMostExperts - 1;
 
@@ -134,11 +129,9 @@ __device__ __forceinline__ double smaller(double a, double b) {
     asm("v_min_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
     return d;
 }
-__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint32_t smaller(uint32_t a, uint32_t b) { return a < b ? a : b; }
 // Descending, by Batcher's odd-even merge.
-template <int N, class V>
-__device__ __forceinline__ void sort_keys(V (&key)[N]) {
+template <int N>
+__device__ __forceinline__ void sort_keys(double (&key)[N]) {
 #pragma unroll
     for (int p = 1; p < N; p *= 2)
 #pragma unroll
@@ -148,28 +141,28 @@ __device__ __forceinline__ void sort_keys(V (&key)[N]) {
 #pragma unroll
                 for (int i = 0; i < k; ++i)
                     if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
-                        const V a = key[i + j], b = key[i + j + k];
+                        const double a = key[i + j], b = key[i + j + k];
                         key[i + j] = larger(a, b);
                         key[i + j + k] = smaller(a, b);
                     }
 }
 
 // A sequence that rises and falls, descending.
-template <int N, int M, class V>
-__device__ __forceinline__ void settle(V (&key)[M]) {
+template <int N, int M>
+__device__ __forceinline__ void settle(double (&key)[M]) {
 #pragma unroll
     for (int d = N / 2; d >= 1; d /= 2)
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (!(i & d)) {
-                const V a = key[i], b = key[i + d];
+                const double a = key[i], b = key[i + d];
                 key[i] = larger(a, b);
                 key[i + d] = smaller(a, b);
             }
 }
 // The K largest of two descending lists of K, in `a`; `left` grows to the largest that is left out.
-template <int K, class V>
-__device__ __forceinline__ void join(V (&a)[K], const V (&b)[K], V& left) {
+template <int K>
+__device__ __forceinline__ void join(double (&a)[K], const double (&b)[K], double& left) {
 #pragma unroll
     for (int i = 0; i < K; ++i) {
         left = larger(left, smaller(a[i], b[K - 1 - i]));
@@ -178,8 +171,8 @@ __device__ __forceinline__ void join(V (&a)[K], const V (&b)[K], V& left) {
     settle<K>(a);
 }
 // The K largest keys of L lanes that have n each, descending, in every lane.
-template <int L, int K, int n, int kXor = 1, class V>
-__device__ __forceinline__ void join_lanes(V (&key)[K], V& left) {
+template <int L, int K, int n, int kXor = 1>
+__device__ __forceinline__ void join_lanes(double (&key)[K], double& left) {
     if constexpr (kXor < L) {
         if constexpr (2 * n <= K) {
 #pragma unroll
@@ -187,7 +180,7 @@ __device__ __forceinline__ void join_lanes(V (&key)[K], V& left) {
             settle<2 * n>(key);
             join_lanes<L, K, 2 * n, 2 * kXor>(key, left);
         } else {
-            V other[K];
+            double other[K];
 #pragma unroll
             for (int i = 0; i < K; ++i) other[i] = partner<kXor>(key[i]);
             join<K>(key, other, left);
@@ -198,13 +191,13 @@ __device__ __forceinline__ void join_lanes(V (&key)[K], V& left) {
 }
 
 // The K largest keys of L lanes that have N each, descending, in every lane.
-template <int L, int K, int N, class V>
-__device__ __forceinline__ void best_keys(const V (&key)[N], V (&list)[K], V& left) {
+template <int L, int K, int N>
+__device__ __forceinline__ void best_keys(const double (&key)[N], double (&list)[K], double& left) {
     constexpr int n = N < K ? N : K;
     static_assert(n * L >= K, "");
 #pragma unroll
     for (int c = 0; c < N; c += n) {
-        V part[n];
+        double part[n];
 #pragma unroll
         for (int i = 0; i < n; ++i) part[i] = key[c + i];
         sort_keys<n>(part);
@@ -217,7 +210,7 @@ __device__ __forceinline__ void best_keys(const V (&key)[N], V (&list)[K], V& le
 #pragma unroll
         for (int i = 0; i < n; ++i) list[i] = part[i];
     }
-    if constexpr (N > K) left = over_lanes<L>(left, [](V a, V c) { return larger(a, c); });
+    if constexpr (N > K) left = over_lanes<L>(left, [](double a, double c) { return larger(a, c); });
     join_lanes<L, K, n>(list, left);
 }
 
@@ -559,9 +552,9 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const char* __restrict__ 
     // The choice by float32 scores; returns whether some were too near to tell.
     auto choose_scored = [&]() {
         const float over = p.sigmoid ? 0.0f : 1.0f / sum;
-        const float score_off = score_error(p.sigmoid, sum), off = biased ? score_off : 0.0f;
+        const float score_off = score_error(p.sigmoid, sum);
         bool near = false;
-        float c[N], low = kInf, high = -kInf;
+        float c[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) c[i] = l[i] > -kInf ? l[i] : -kInf;  // for NaN too
         if (biased) {
@@ -658,51 +651,39 @@ __global__ __launch_bounds__(kBlock) void route_kernel(const char* __restrict__ 
 #pragma unroll
                 for (int i = 0; i < N; ++i) c[i] = -kInf;
         }
+        double key[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            low = fminf(low, c[i] > -kInf ? c[i] : kInf);
-            high = fmaxf(high, c[i]);
-        }
-        low = -lanes_max<L>(-low);
-        high = lanes_max<L>(high);
-        // places 1 .. 2^22 - 1; a token whose range is no positive number is chosen again, unless it has none to choose
-        const float range = high - low, scale = 4194302.0f / range;
-        near |= !(range > 0.0f && scale > 0.0f && scale < kInf) && high > -kInf;
-        uint32_t key[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint32_t at = static_cast<uint32_t>((c[i] - low) * scale) + 1;
-            key[i] = c[i] > -kInf ? (at < 0x3FFFFFu ? at : 0x3FFFFFu) << 10 | (kMostExperts - 1 - (e0 + i)) : 0;
-        }
-        // places: each of two scores off and rounded with its bias (to half an ulp, 2^-24 of the sum), and of each place
-        // a unit cut off and half a unit of roundings (the scale's own is the same for all)
-        const float far = (2.0f * off + fmaxf(fabsf(low), fabsf(high)) * 0x1p-23f) * scale + 3.0f;
-        auto tell = [&](uint32_t a, uint32_t o) { near |= o != 0 && static_cast<float>((a >> 10) - (o >> 10)) <= far; };
-        auto number = [](uint32_t k) { return k == 0 ? -1 : kMostExperts - 1 - static_cast<int>(k & (kMostExperts - 1)); };
-        const auto larger2 = [](uint32_t a, uint32_t o) { return larger(a, o); };
+        for (int i = 0; i < N; ++i) key[i] = key_of(c[i], e0 + i);
+        // Two biased scores of which a is not the smaller: each off, and rounded with its bias to half an ulp, 2^-24 of
+        // itself. Logits are exact.
+        auto tell = [&](double a, double o) {
+            const double more = value_of(a), less = value_of(o);
+            near |= biased && o > -kInf && more - less <= 2.0 * score_off + (fabs(more) + fabs(less)) * 0x1p-24;
+        };
+        const auto larger2 = [](double a, double o) { return larger(a, o); };
         if constexpr (K > 0) {
-            uint32_t list[K], left = 0, mine = 0;
+            double list[K], left = -kInf, mine = -kInf;
             best_keys<L, K>(key, list, left);
-            uint32_t next = left;
+            double next = left;
 #pragma unroll
             for (int j = 0; j < K; ++j) {
                 if (lane == j) mine = list[j];
                 if (lane + 1 == j) next = list[j];
             }
             if (lane < p.top_k) tell(mine, next);
-            id[0] = lane < p.top_k ? number(mine) : -1;
+            id[0] = lane < p.top_k ? expert_of(mine) : -1;
         } else {
             sort_keys<N>(key);
-            uint32_t last = 0xFFFFFFFFu;
+            double last = -kInf;
             for (int r = 0; r <= p.top_k; ++r) {  // also the best that is left
-                const uint32_t best = over_lanes<L>(key[0], larger2);
+                const double best = over_lanes<L>(key[0], larger2);
                 if (r > 0) tell(last, best);
                 last = best;
                 const bool pop = key[0] == best;
 #pragma unroll
                 for (int i = 0; i + 1 < N; ++i) key[i] = pop ? key[i + 1] : key[i];
-                key[N - 1] = pop ? 0 : key[N - 1];
-                const int e = number(best);
+                key[N - 1] = pop ? static_cast<double>(-kInf) : key[N - 1];
+                const int e = expert_of(best);
 #pragma unroll
                 for (int s = 0; s < S; ++s)
                     if (r < p.top_k && r == lane + s * L) id[s] = e;

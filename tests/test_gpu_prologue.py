@@ -515,6 +515,28 @@ def test_a_tokens_choice_is_the_same_in_calls_of_all_sizes(form):
         assert torch.equal(a, ids[at:at + n]) and torch.equal(b, weights[at:at + n])
 
 
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: f"{f['score']}-{'bias' if f['bias'] else 'plain'}-{f['groups']}")
+@pytest.mark.parametrize("experts,top_k", [(16, 5), (64, 8), (256, 8), (320, 12)])
+def test_route_with_experts_that_finite_values_switch_off(form, experts, top_k):
+    """Biases and logits far below all others leave the others' order as it is, also that of near ones; so does a
+    bias far above."""
+    rng = np.random.default_rng(experts)
+    base = rng.standard_normal((300, experts)).astype(np.float32)
+    base[:, 9] = base[:, 4] + rng.integers(-1, 2, 300).astype(np.float32) * np.float32(2 ** -21)
+    base[:, [4, 9]] += 2
+    off = rng.choice(experts, 3, replace=False)
+    for value in (-1e4, -1e9, -3.4e38, 1e9):
+        logits, bias = base.copy(), None
+        if form["bias"]:
+            bias = rng.standard_normal(experts).astype(np.float32) * np.float32(0.01)
+            bias[9] = bias[4]
+            bias[off] = value
+            bias = torch.from_numpy(bias).cuda()
+        else:
+            logits[:, off] = -abs(value)
+        check_route(torch.from_numpy(logits).cuda(), top_k, bias, form, True, 1.0)
+
+
 @pytest.mark.parametrize("offset", [0.02, 1.02, 16.02, 17.0, 33.0, 64.1, 130.0, 513.0])
 @pytest.mark.parametrize("experts,top_k", [(16, 8), (16, 11), (200, 8)])
 def test_route_by_scores_that_a_common_bias_makes_coarse(offset, experts, top_k):

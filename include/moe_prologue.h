@@ -34,7 +34,8 @@ typedef enum moe_epi_group_score { MOE_EPI_GROUP_MAX = 0, MOE_EPI_GROUP_TOP2 = 1
  *   scale = max|y| / 127, q = rint(127 y / max|y|)     (as quantize_rows_int8_fwd, of the unrounded y)
  * A row of zeros in y has scale 0 and q 0; a row with an infinity or a NaN in y
  * has scale NaN and q 0. The sum of squares is float32: rows whose squares
- * overflow it have n = 0, as 1 / sqrt(inf) is.
+ * overflow it have n = 0, as 1 / sqrt(inf) is, and squares below its range count
+ * as 0.
  *   x            [rows, cols] of dtype               in
  *   residual     [rows, cols] of dtype, or NULL      in
  *   weight       [cols] of w_dtype (dtype or float32)  in
@@ -75,9 +76,9 @@ int64_t rms_norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
  * of all bits of both (of two float32 factors up to 2^-23 of the product is left
  * out), float32 sums. x and weight of one 16-bit type follow IEEE arithmetic; where
  * one of them is float32, a row of x or of weight that holds an infinity or a NaN
- * gives NaN or an infinity, and every finite factor is taken as it is. The order of
- * a sum depends on the sizes of the call, so a token's logits may differ in their
- * last bits in calls of other sizes.
+ * gives NaN or an infinity, and a float32 factor is taken to 2^-134 (all bits of it
+ * from 2^-110 on). The order of a sum depends on the sizes of the call, so a token's
+ * logits may differ in their last bits in calls of other sizes.
  *   x         [tokens, hidden] of dtype                       in
  *   weight    [experts, hidden] of w_dtype (dtype or float32) in
  *   logits    [tokens, experts] float32                       out

@@ -3,8 +3,8 @@
 // The matrix cores multiply float32 at an eighth of their 16-bit rate, so a
 // float32 is cut into up to three bfloat16 pieces, each the nearest bfloat16 to
 // what the ones before leave: x = x0 + x1 + x2 exactly (8 significant bits and a
-// sign each), |x1| <= 2^-8 |x|, |x2| <= 2^-16 |x|. Products of pieces are exact in
-// float32. Of the pairs of pieces those with i + j <= 2 are summed; what is left
+// sign each) from 2^-110 on, below to 2^-134, half the least bfloat16; |x1| <=
+// 2^-8 |x|, |x2| <= 2^-16 |x|. Products of pieces are exact in float32. Of the pairs of pieces those with i + j <= 2 are summed; what is left
 // out is at most 2^-23 of a product. A float16 (11 bits) is two pieces.
 #pragma once
 

@@ -870,3 +870,16 @@ def test_router_products_of_small_values(dtype, weight):
     want, slack = ref.product(ref.f64(x), ref.f64(w).T)
     least = 2.0 ** -14 if dtype == F16 and weight == F16 else 2.0 ** -126
     check(epi.moe_router_logits(x, w), want, slack + least * np.abs(ref.f64(w)).sum(1)[None], F32, "logits")
+
+
+def test_router_products_take_the_least_factors():
+    """One product per sum: factors of 16 bits down to their least are taken as they are, float32 ones to 2^-134."""
+    for dtype, weight, values in ((BF16, BF16, [2.0 ** -133, 5 * 2.0 ** -133, 2.0 ** -126]),
+                                  (F16, F16, [2.0 ** -24, 3 * 2.0 ** -24, 2.0 ** -14]), (F16, F32, [2.0 ** -24, 5 * 2.0 ** -24]),
+                                  (F32, F32, [1.2345678e-38, 1.2345678e-36, -7.654321e-40, 1.2345678e-33, 2.0 ** -149])):
+        v = torch.tensor(values, device="cuda").to(dtype)
+        x, w = torch.zeros(len(values), 72, dtype=dtype, device="cuda"), torch.zeros(5, 72, dtype=weight, device="cuda")
+        x[:, 67], w[2, 67], w[3, 67] = v, 1.0, -0.5
+        want = ref.f64(x) @ ref.f64(w).T
+        check(epi.moe_router_logits(x, w), want, (2.0 ** -134 if dtype == F32 else 0) * np.abs(ref.f64(w)).sum(1)[None] +
+              2 * ref.EPS * np.abs(want), F32, "logits")

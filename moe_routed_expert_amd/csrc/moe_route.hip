@@ -11,14 +11,14 @@
 // groups 140 us instead of 48). An expert that a bias of -1e4 or -1e9 switches off
 // changes nothing (47 us).
 //
-// Bound by vector instructions: 65536 tokens, 8 of 256 experts by logits 23 us
-// (10 at a copy's rate), in groups by biased sigmoids 48 us; 131072 tokens, 8
-// of 64 24 us. A kernel takes each token once, without a loop around it: with
+// Bound by vector instructions: 65536 tokens, 8 of 256 experts by logits 22 us
+// (15 at a copy's rate), in groups by biased sigmoids 48 us; 131072 tokens, 8
+// of 64 25 us. A kernel takes each token once, without a loop around it: with
 // one the compiler keeps the constants of exponentials and divisions in
 // registers, 204 instead of 84 for 256 experts, and the times are 31, 75 and 28.
 //
-// The gradient is bound by memory where every score counts (131072 x 64 19.6
-// us, 3.9 TB/s): a token's slots go through LDS, and each lane adds up those of
+// The gradient is bound by memory where every score counts (131072 x 64 19.2
+// us, 4.0 TB/s): a token's slots go through LDS, and each lane adds up those of
 // its experts, in their order.
 #include <type_traits>
 

@@ -5,8 +5,8 @@
 //   with a = h n, g = grad_out weight
 //
 // Bound by memory: a row is read once and kept in registers, as it is stored,
-// between its sum and its results; 65536 x 7168 bf16 with the residual 637 us
-// (5.9 TB/s), 16384 x 7168 with rows also in 8 bits 174 us (6.1 TB/s).
+// between its sum and its results; 65536 x 7168 bf16 with the residual 639 us
+// (5.9 TB/s), 16384 x 7168 with rows also in 8 bits 175 us (6.0 TB/s).
 //
 // Lanes of a row are chosen as in quantize_rows.hip, which has both sides of
 // each: the fewest that hold it with four vectors each, and up to 512 rows more
@@ -15,8 +15,10 @@
 //
 // Gradients: a lane also keeps the sums of its columns of the weight's gradient
 // over the rows of its block, of which there are up to four per CU; the blocks'
-// sums are added by a second launch. 32768 x 7168 bf16 367 + 9 us (5.2 TB/s);
-// with four vectors a lane instead of two the registers held one block a CU.
+// sums are added by a second launch. 32768 x 7168 bf16 365 + 9 us (5.2 TB/s);
+// with four vectors a lane instead of two the registers held one block a CU. Rows
+// wider than 8192 columns are read by elements, twice for grad_x and once more for
+// the weight: 8192 x 12288 351 us, where the bytes take 125.
 #include <type_traits>
 
 #include "bf16_pieces.h"

@@ -11,10 +11,13 @@
 //                5.7 TB/s; straight into operands 381;
 //   grad_x       the weight's columns lie in LDS as operands, each wavefront
 //                takes its tokens through all of them, and results go through
-//                LDS to be stored by rows: 65536 x 7168 x 64 198 us, 5.5 TB/s;
+//                LDS to be stored by rows: 65536 x 7168 x 64 201 us, 5.4 TB/s;
 //   grad_weight  8 tokens' elements are turned into operands in registers; the
-//                tokens are split over parts, which a second launch adds: 171
-//                us, 6.6 TB/s.
+//                tokens are split over parts, which a second launch adds: 212
+//                us, 5.3 TB/s (with two pieces of grad_logits 171, see below).
+// A block has at most 64 experts (grad_x: as many columns of hidden as fit in 64
+// KB with all of them), so that with more of them the tokens or grad_logits are
+// read more often: 65536 x 2048 x 256 bf16 167 us, of which 69 are the bytes'.
 #include <type_traits>
 
 #include "bf16_pieces.h"
@@ -294,7 +297,8 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool few(int64_t tokens, int64_t experts) { return up(experts, 16) * up(tokens, 16) <= 256; }
 
 // Parts that hidden is shared by. A launch that adds them up is not worth it up to 8192 of hidden for few tokens (32
-// x 7168 x 64 7.5 us, in two parts 9.0); tiles have two blocks per CU and at least 8 steps each.
+// x 7168 x 64 7.5 us, in two parts 9.0); tiles have two blocks per CU and about 8 steps each, 4 at
+// least.
 int64_t logits_parts(int64_t tokens, int64_t hidden, int64_t experts) {
     if (tokens == 0) return 1;
     if (few(tokens, experts)) return up(hidden, kFewHidden) < 16 ? up(hidden, kFewHidden) : 16;
@@ -487,7 +491,8 @@ __global__ __launch_bounds__(kBlock) void grad_x_kernel(const float* __restrict_
     }
 }
 
-// As above for more than 256 experts, 256 at a time: 16 hidden a block.
+// As above for more than 256 experts, 16 hidden a block: all experts' operands lie in LDS, and a wavefront reads and
+// cuts the gradients of 32 experts at a time.
 template <int T, int W>
 __global__ __launch_bounds__(kBlock) void grad_x_many_kernel(const float* __restrict__ grad,
                                                              const char* __restrict__ weight,
